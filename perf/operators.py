@@ -304,7 +304,7 @@ def _pack(x, up=False):
     n = x.numel()
     b = torch.nn.functional.pad(x, (0, -n % 128)).view(-1, 128)
     amax = b.abs().amax(dim=1)
-    kept = amax >= 2.0 ** -118
+    kept = ~(amax < 2.0 ** -118)
     inv = torch.where(kept, 448 / amax, 0.0)
     y = b * inv[:, None]
     q = y.to(E4M3)
@@ -375,7 +375,7 @@ def _run_own(s, op):
     if op in ("route", "route8"):
         kg.kg_route(s["idx"], s["ks"], s["pos"], s["src"], s["ws"])
         if op == "route8":
-            kg.kg_dispatch_fp8(s["X"], s["src"], s["case"]["k"], s["Q"], s["sa"])
+            kg.kg_dispatch_fp8(s["X"], s["pos"], s["Q"], s["sa"])
             return dict(ks=s["ks"], pos=s["pos"], src=s["src"], q=s["Q"].view(E4M3), sa=s["sa"])
         kg.kg_dispatch(s["X"], s["pos"], s["Xp"])
         kg.kg_combine(s["Y"], s["pos"], s["w"], s["out"])
