@@ -13,3 +13,7 @@ from ._binding import (KG_BF16, KG_E4M3_F32SCALE, KG_E4M3_UE8M0, KG_ERR_ALIAS,  
                        kg_wgrad_ws_raw, kg_wgrad_noalloc_raw, new_workspace, scale_rows_of, KG_SRC_BF16, KG_SRC_E4M3_1X128,
                        kg_requant, kg_requant_raw, kg_dgrad, kg_dgrad_raw,
                        kg_wgrad_nt, kg_wgrad_nt_raw)
+from ._binding import (KG_ADAMW_8BIT, KG_ADAMW_G_BF16, KG_ADAMW_P_BF16, KG_ROWS_BF16,  # noqa: F401
+                       KG_ROWS_F32)
+from .layer import (AdamWTable, kg_adamw, kg_combine, kg_combine_bwd, kg_dispatch,  # noqa: F401
+                    kg_dispatch_fp8, kg_fprop, kg_route, new_route_workspace)

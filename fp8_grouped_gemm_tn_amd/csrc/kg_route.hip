@@ -1,0 +1,696 @@
+// kg_route.hip -- tokens into expert order and back on gfx950, C ABI kg_route,
+// kg_dispatch, kg_dispatch_fp8, kg_combine, kg_combine_bwd.
+//
+// The products of an expert layer (kg_fprop, kg_dgrad, kg_wgrad) read rows in expert
+// order: expert g's rows are contiguous. With idx [T, k] the experts that a router chose
+// for each token, slot s = t * k + j holds expert e(s) = idx[t][j] (G, "dropped", when it
+// lies outside [0, G)), and
+//   row(s)  = the rank of s in the order by (e(s), s): a stable counting sort;
+//   ks[g]   = number of slots of expert g;
+//   pos[s]  = row(s), or ~row(s) (negative) for a dropped slot;
+//   src[r]  = s for row(s) = r, or ~s.
+// Dropped slots take the rows behind the last expert's, so the rows are a permutation of
+// the slots and every row is written exactly once (zeros for the dropped ones).
+//   dispatch      Xp[row] = X[t]          its gradient is combine without weights
+//   dispatch_fp8  the same as e4m3 codes with one scale per row and 128 channels
+//   combine       out[t] = sum_j w[t][j] Y[pos[t][j]]
+//   combine_bwd   dY[row] = w[t][j] dOut[t],  dw[t][j] = <dOut[t], Y[row]>
+// All of it is bound by memory: each kernel reads and writes its rows once.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kg_device.h"
+#include "kg_host.h"
+#include "kgwgrad.h"
+
+namespace kg {
+
+constexpr int kRouteMaxGroups = 1024;
+constexpr int kRouteKeys = kRouteMaxGroups + 1;  // + the dropped slots
+
+// ------------------------------------------------------------------------------ sort plan
+
+// Waves of a sorting workgroup; each ranks a contiguous run of slots in order.
+constexpr int kSortWaves = 4, kSortThreads = 64 * kSortWaves;
+// Slots per workgroup of the two-pass plan.
+constexpr int kSortBlock = 2048;
+// Up to this many slots one workgroup of kSoloWaves waves does everything in one launch.
+constexpr int kSoloWaves = 16;
+constexpr int kSoloSlots = 4096;
+
+__device__ __forceinline__ int slot_key(const int32_t* idx, int64_t s, int G) {
+  const int e = idx[s];
+  return (unsigned)e < (unsigned)G ? e : G;
+}
+
+// Adds the slots [s0, s1) of this wave to its histogram row.
+__device__ __forceinline__ void wave_count(const int32_t* idx, int64_t s0, int64_t s1, int G,
+                                           int* row) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t s = s0 + lane; s < s1; s += 64) atomicAdd(row + slot_key(idx, s, G), 1);
+}
+
+// Ranks the slots [s0, s1) of this wave in order: next[e] is the row of the wave's next slot
+// of expert e. Lanes of one expert find each other by one ballot per bit of the key; the
+// lowest of them moves next[e] on by their number, so a slot's row does not depend on timing.
+__device__ __forceinline__ void wave_rank(const int32_t* idx, int64_t s0, int64_t s1, int G,
+                                          int bits, volatile int* next, int32_t* pos,
+                                          int32_t* src) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t base = s0; base < s1; base += 64) {
+    const int64_t s = base + lane;
+    const bool on = s < s1;
+    const int e = on ? slot_key(idx, s, G) : 0;
+    uint64_t peers = __ballot(on);
+    for (int b = 0; b < bits; ++b) {
+      const bool bit = (e >> b) & 1;
+      const uint64_t m = __ballot(bit);
+      peers &= bit ? m : ~m;
+    }
+    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    int row = 0;
+    if (on) row = next[e] + rank;
+    __builtin_amdgcn_wave_barrier();  // every lane has read next[e] before it moves on
+    if (on && rank == 0) next[e] = row + __popcll(peers);
+    __builtin_amdgcn_wave_barrier();
+    if (on) {
+      const bool kept = e < G;
+      pos[s] = kept ? row : ~row;
+      if (src != nullptr) src[row] = kept ? (int32_t)s : ~(int32_t)s;
+    }
+  }
+}
+
+// Exclusive scan over keys 0 .. G of total[], in place, by the whole workgroup (each
+// thread owns PER consecutive keys). `part` holds one int per wave.
+template <int THREADS>
+__device__ __forceinline__ void scan_keys(int* total, int G, int* part) {
+  constexpr int PER = (kRouteKeys + THREADS - 1) / THREADS;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  int v[PER], own = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * PER + i;
+    v[i] = e <= G ? total[e] : 0;
+    own += v[i];
+  }
+  int incl = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += u;
+  }
+  if (lane == 63) part[w] = incl;
+  __syncthreads();
+  int run = incl - own;
+  for (int i = 0; i < w; ++i) run += part[i];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * PER + i;
+    if (e <= G) total[e] = run;
+    run += v[i];
+  }
+  __syncthreads();
+}
+
+// Everything in one workgroup: the waves count their runs of slots, the counts are scanned
+// over waves and experts, the waves rank their runs.
+__global__ __launch_bounds__(64 * kSoloWaves) void kg_route_solo_kernel(
+    const int32_t* idx, int n, int G, int bits, int32_t* ks, int32_t* pos, int32_t* src) {
+  extern __shared__ int sm[];
+  __shared__ int part[kSoloWaves];
+  const int keys = G + 1, t = threadIdx.x, w = t >> 6;
+  int* hist = sm;                       // [kSoloWaves][keys]
+  int* total = sm + kSoloWaves * keys;  // [keys]
+  for (int i = t; i < kSoloWaves * keys; i += 64 * kSoloWaves) hist[i] = 0;
+  __syncthreads();
+  const int run = ((n + kSoloWaves - 1) / kSoloWaves + 63) & ~63;
+  const int s0 = min(n, w * run), s1 = min(n, s0 + run);
+  wave_count(idx, s0, s1, G, hist + w * keys);
+  __syncthreads();
+  for (int e = t; e < keys; e += 64 * kSoloWaves) {
+    int sum = 0;
+    for (int i = 0; i < kSoloWaves; ++i) {
+      const int c = hist[i * keys + e];
+      hist[i * keys + e] = sum;
+      sum += c;
+    }
+    total[e] = sum;
+    if (e < G) ks[e] = sum;
+  }
+  __syncthreads();
+  scan_keys<64 * kSoloWaves>(total, G, part);
+  for (int e = t; e < keys; e += 64 * kSoloWaves)
+    for (int i = 0; i < kSoloWaves; ++i) hist[i * keys + e] += total[e];
+  __syncthreads();
+  wave_rank(idx, s0, s1, G, bits, hist + w * keys, pos, src);
+}
+
+// Pass 1: counts of every block of slots, counts[block][key].
+__global__ __launch_bounds__(kSortThreads) void kg_route_count_kernel(const int32_t* idx,
+                                                                     int64_t n, int G,
+                                                                     int32_t* counts) {
+  extern __shared__ int sm[];
+  const int keys = G + 1;
+  for (int i = threadIdx.x; i < keys; i += kSortThreads) sm[i] = 0;
+  __syncthreads();
+  const int64_t s0 = (int64_t)blockIdx.x * kSortBlock;
+  const int64_t s1 = s0 + kSortBlock < n ? s0 + kSortBlock : n;
+  for (int64_t s = s0 + threadIdx.x; s < s1; s += kSortThreads)
+    atomicAdd(sm + slot_key(idx, s, G), 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < keys; i += kSortThreads)
+    counts[(int64_t)blockIdx.x * keys + i] = sm[i];
+}
+
+// Pass 2: for every key the exclusive scan of its counts over the blocks, in place, and its
+// total. One thread per key walks the blocks, a wave reads 64 neighbouring keys.
+__global__ __launch_bounds__(64) void kg_route_scan_kernel(int32_t* counts, int blocks, int G,
+                                                          int32_t* totals) {
+  const int keys = G + 1, e = blockIdx.x * 64 + threadIdx.x;
+  if (e >= keys) return;
+  int sum = 0;
+  for (int b = 0; b < blocks; ++b) {
+    const int64_t at = (int64_t)b * keys + e;
+    const int c = counts[at];
+    counts[at] = sum;
+    sum += c;
+  }
+  totals[e] = sum;
+}
+
+// Pass 3: every block ranks its slots behind its experts' earlier blocks.
+__global__ __launch_bounds__(kSortThreads) void kg_route_rank_kernel(
+    const int32_t* idx, int64_t n, int G, int bits, const int32_t* counts, const int32_t* totals,
+    int32_t* ks, int32_t* pos, int32_t* src) {
+  extern __shared__ int sm[];
+  __shared__ int part[kSortWaves];
+  const int keys = G + 1, t = threadIdx.x, w = t >> 6;
+  int* hist = sm;                       // [kSortWaves][keys]
+  int* total = sm + kSortWaves * keys;  // [keys]
+  for (int e = t; e < keys; e += kSortThreads) {
+    const int c = totals[e];
+    total[e] = c;
+    if (blockIdx.x == 0 && e < G) ks[e] = c;
+  }
+  for (int i = t; i < kSortWaves * keys; i += kSortThreads) hist[i] = 0;
+  __syncthreads();
+  const int64_t b0 = (int64_t)blockIdx.x * kSortBlock;
+  const int64_t b1 = b0 + kSortBlock < n ? b0 + kSortBlock : n;
+  constexpr int run = kSortBlock / kSortWaves;
+  const int64_t s0 = b0 + w * run < b1 ? b0 + w * run : b1, s1 = s0 + run < b1 ? s0 + run : b1;
+  wave_count(idx, s0, s1, G, hist + w * keys);
+  scan_keys<kSortThreads>(total, G, part);
+  for (int e = t; e < keys; e += kSortThreads) {
+    int sum = total[e] + counts[(int64_t)blockIdx.x * keys + e];
+    for (int i = 0; i < kSortWaves; ++i) {
+      const int c = hist[i * keys + e];
+      hist[i * keys + e] = sum;
+      sum += c;
+    }
+  }
+  __syncthreads();
+  wave_rank(idx, s0, s1, G, bits, hist + w * keys, pos, src);
+}
+
+// ---------------------------------------------------------------------------------- rows
+
+// 16 bytes at any address that the element type allows (gfx950 takes unaligned accesses).
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef int v2i_any __attribute__((ext_vector_type(2), aligned(1)));
+
+struct RowShape {
+  int64_t T;
+  int64_t rows;  // T * k
+  int k, H;
+  int lanes;  // threads per token: a power of two up to the workgroup's 256
+};
+
+__device__ __forceinline__ float bf16_to_f32(uint32_t u) { return __uint_as_float(u << 16); }
+
+// The nearest bf16, ties to even (a NaN stays a NaN).
+__device__ __forceinline__ uint32_t f32_to_bf16(float x) {
+  return __builtin_bit_cast(unsigned short, (__bf16)x);
+}
+
+// N values of a row: bf16 or fp32, 16 bytes.
+template <bool BF16>
+struct Vec {
+  static constexpr int N = BF16 ? 8 : 4;
+  static constexpr int ELEM = BF16 ? 2 : 4;
+  static __device__ __forceinline__ void unpack(const v4i& x, float (&f)[N]) {
+    if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_to_f32((uint32_t)x[i] & 0xFFFFu);
+        f[2 * i + 1] = __uint_as_float((uint32_t)x[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = __int_as_float(x[i]);
+    }
+  }
+  static __device__ __forceinline__ v4i pack(const float (&f)[N]) {
+    v4i x;
+    if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = (int)(f32_to_bf16(f[2 * i]) | f32_to_bf16(f[2 * i + 1]) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __float_as_int(f[i]);
+    }
+    return x;
+  }
+  static __device__ __forceinline__ float load1(const unsigned char* p) {
+    return BF16 ? bf16_to_f32(*(const unsigned short*)p) : *(const float*)p;
+  }
+  static __device__ __forceinline__ void store1(unsigned char* p, float x) {
+    if constexpr (BF16)
+      *(unsigned short*)p = (unsigned short)f32_to_bf16(x);
+    else
+      *(float*)p = x;
+  }
+};
+
+__device__ __forceinline__ v4i load16(const unsigned char* p) { return *(const v4i_any*)p; }
+__device__ __forceinline__ void store16(unsigned char* p, const v4i& x) { *(v4i_any*)p = x; }
+
+// The row that slot value `at` (of pos) names, or -1 for one outside [0, rows): a bad value
+// reads and writes nothing.
+__device__ __forceinline__ int64_t named_row(int at, int64_t rows) {
+  const int r = at < 0 ? ~at : at;
+  return r < rows ? r : -1;
+}
+
+// Xp[pos] = X[token], or zeros for dropped slots. A token's threads read its row once and
+// write it to its k rows.
+template <int ELEM>
+__global__ __launch_bounds__(256) void kg_dispatch_kernel(const unsigned char* X, int64_t ldx,
+                                                          const int32_t* pos, RowShape s,
+                                                          unsigned char* Xp) {
+  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
+  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
+  if (t >= s.T) return;
+  const int64_t bytes = (int64_t)s.H * ELEM;
+  const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / ELEM;
+  const unsigned char* x = X + t * ldx * ELEM;
+  const int32_t* p = pos + t * s.k;
+  for (int c = lane; c < chunks; c += s.lanes) {
+    const v4i v = load16(x + 16 * (int64_t)c);
+    for (int j = 0; j < s.k; ++j) {
+      const int at = p[j];
+      const int64_t r = named_row(at, s.rows);
+      if (r >= 0) store16(Xp + r * bytes + 16 * (int64_t)c, at < 0 ? v4i{0, 0, 0, 0} : v);
+    }
+  }
+  if (lane < tail) {
+    const int64_t o = 16 * (int64_t)chunks + lane * ELEM;
+    for (int j = 0; j < s.k; ++j) {
+      const int at = p[j];
+      const int64_t r = named_row(at, s.rows);
+      if (r < 0) continue;
+      if constexpr (ELEM == 2)
+        *(unsigned short*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const unsigned short*)(x + o);
+      else
+        *(uint32_t*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const uint32_t*)(x + o);
+    }
+  }
+}
+
+// Largest of 16 neighbouring lanes' values.
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// Codes of four quotients x / s (binary32, rounded to nearest; e4m3: nearest, ties to the
+// even code), NaN as 0x7F, as kg_requant rounds them. By the choice of s a finite |x / s| stays
+// below 464, from where 448 would no longer be the nearest value (the scale of a block of
+// subnormal numbers is rounded to 2^-149, which moves it by less than 1/256).
+__device__ __forceinline__ int codes4(float a, float b, float c, float d, float s) {
+  uint32_t q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a / s, b / s, 0, false);
+  q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c / s, d / s, (int)q, true);
+  // the conversion's NaN is 0xFF or 0x7F: clear the sign of bytes whose low bits are ones
+  return (int)(q ^ (((q & 0x7F7F7F7Fu) + 0x01010101u) & q & 0x80808080u));
+}
+
+// e4m3 rows: 16 lanes hold one 128-channel block, 8 channels each; its scale is
+// amax / 448 (1 for a block of zeros). The codes and the scale go to the token's k rows.
+__global__ __launch_bounds__(256) void kg_dispatch_fp8_kernel(const unsigned char* X, int64_t ldx,
+                                                              const int32_t* pos, RowShape s,
+                                                              unsigned char* Q, float* sa) {
+  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
+  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
+  if (t >= s.T) return;  // whole groups of 16 lanes or more: the shuffles below stay inside
+  const int chunks = s.H >> 3;  // 8 channels each; H is a multiple of 16
+  const int padded = (chunks + 15) & ~15;
+  const unsigned char* x = X + t * ldx * 2;
+  const int32_t* p = pos + t * s.k;
+  for (int c = lane; c < padded; c += s.lanes) {
+    float f[8] = {};
+    if (c < chunks) Vec<true>::unpack(load16(x + 16 * (int64_t)c), f);
+    float amax = 0.f;  // fmaxf passes over NaNs
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    amax = max16(amax);
+    const float sc = amax == 0.f ? 1.0f : amax / 448.0f;
+    const v2i q = {codes4(f[0], f[1], f[2], f[3], sc), codes4(f[4], f[5], f[6], f[7], sc)};
+    for (int j = 0; j < s.k; ++j) {
+      const int at = p[j];
+      const int64_t r = named_row(at, s.rows);
+      if (r < 0) continue;
+      if (c < chunks) *(v2i_any*)(Q + r * s.H + 8 * (int64_t)c) = at < 0 ? v2i{0, 0} : q;
+      if ((c & 15) == 0) sa[(int64_t)(c >> 4) * s.rows + r] = at < 0 ? 1.0f : sc;
+    }
+  }
+}
+
+// out[t] = sum_j w[t][j] Y[pos[t][j]] in fp32, j in order, rounded once. Dropped slots are
+// left out, whatever their weight holds. Up to eight rows are read before the first is used.
+template <bool BF16>
+__global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* Y,
+                                                         const int32_t* pos, const float* w,
+                                                         RowShape s, unsigned char* out,
+                                                         int64_t ldo) {
+  using V = Vec<BF16>;
+  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
+  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
+  if (t >= s.T) return;
+  const int64_t bytes = (int64_t)s.H * V::ELEM;
+  const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / V::ELEM;
+  const int32_t* p = pos + t * s.k;
+  const float* wt = w == nullptr ? nullptr : w + t * s.k;
+  unsigned char* o = out + t * ldo * V::ELEM;
+  for (int c = lane; c < chunks; c += s.lanes) {
+    float acc[V::N] = {};
+    for (int j0 = 0; j0 < s.k; j0 += 8) {
+      v4i y[8];
+      float wj[8];
+      bool on[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        on[i] = false;
+        if (j0 + i < s.k) {
+          const int at = p[j0 + i];
+          if (at >= 0 && at < s.rows) {
+            on[i] = true;
+            y[i] = load16(Y + at * bytes + 16 * (int64_t)c);
+            wj[i] = wt == nullptr ? 1.0f : wt[j0 + i];
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!on[i]) continue;
+        float f[V::N];
+        V::unpack(y[i], f);
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) acc[e] = fmaf(wj[i], f[e], acc[e]);
+      }
+    }
+    store16(o + 16 * (int64_t)c, V::pack(acc));
+  }
+  if (lane < tail) {
+    const int64_t b = 16 * (int64_t)chunks + lane * V::ELEM;
+    float acc = 0.f;
+    for (int j = 0; j < s.k; ++j) {
+      const int at = p[j];
+      if (at >= 0 && at < s.rows)
+        acc = fmaf(wt == nullptr ? 1.0f : wt[j], V::load1(Y + at * bytes + b), acc);
+    }
+    V::store1(o + b, acc);
+  }
+}
+
+// dY[row] = w dOut[t] (zeros for dropped rows), dw = <dOut[t], Y[row]> (0 for dropped
+// slots). Eight slots at a time: a thread keeps their partial dot products over its
+// channels, then the token's threads add theirs in a fixed order.
+template <bool BF16>
+__global__ __launch_bounds__(256) void kg_combine_bwd_kernel(const unsigned char* dOut,
+                                                             int64_t ldo, const unsigned char* Y,
+                                                             const int32_t* pos, const float* w,
+                                                             RowShape s, unsigned char* dY,
+                                                             float* dw) {
+  using V = Vec<BF16>;
+  __shared__ float part[4][8];
+  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
+  const int64_t t0 = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
+  const bool live = t0 < s.T;  // a workgroup of a token's 256 threads is live as a whole
+  const int64_t t = live ? t0 : 0;
+  const int64_t bytes = (int64_t)s.H * V::ELEM;
+  const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / V::ELEM;
+  const unsigned char* d = dOut + t * ldo * V::ELEM;
+  const int32_t* p = pos + t * s.k;
+  for (int j0 = 0; j0 < s.k; j0 += 8) {
+    float dot[8] = {}, wj[8];
+    int at[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      at[i] = 0;
+      wj[i] = 1.0f;
+      if (j0 + i < s.k) {
+        at[i] = p[j0 + i];
+        if (w != nullptr) wj[i] = w[t * s.k + j0 + i];
+      }
+    }
+    if (live) {
+      for (int c = lane; c < chunks; c += s.lanes) {
+        float g[V::N];
+        V::unpack(load16(d + 16 * (int64_t)c), g);
+        v4i y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (dw != nullptr && j0 + i < s.k && at[i] >= 0 && at[i] < s.rows)
+            y[i] = load16(Y + at[i] * bytes + 16 * (int64_t)c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (j0 + i >= s.k) continue;
+          const int64_t r = named_row(at[i], s.rows);
+          if (r < 0) continue;
+          float f[V::N];
+          if (at[i] < 0) {
+            store16(dY + r * bytes + 16 * (int64_t)c, v4i{0, 0, 0, 0});
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < V::N; ++e) f[e] = wj[i] * g[e];
+          store16(dY + r * bytes + 16 * (int64_t)c, V::pack(f));
+          if (dw != nullptr) {
+            V::unpack(y[i], f);
+#pragma unroll
+            for (int e = 0; e < V::N; ++e) dot[i] = fmaf(g[e], f[e], dot[i]);
+          }
+        }
+      }
+      if (lane < tail) {
+        const int64_t b = 16 * (int64_t)chunks + lane * V::ELEM;
+        const float g = V::load1(d + b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (j0 + i >= s.k) continue;
+          const int64_t r = named_row(at[i], s.rows);
+          if (r < 0) continue;
+          V::store1(dY + r * bytes + b, at[i] < 0 ? 0.f : wj[i] * g);
+          if (dw != nullptr && at[i] >= 0) dot[i] = fmaf(g, V::load1(Y + r * bytes + b), dot[i]);
+        }
+      }
+    }
+    if (dw == nullptr) continue;
+    const int in_wave = s.lanes < 64 ? s.lanes : 64;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      for (int o = 1; o < in_wave; o <<= 1) dot[i] += __shfl_xor(dot[i], o, 64);
+    if (s.lanes > 64) {  // the token's threads are the workgroup's first s.lanes / 64 waves ...
+      const int wave = threadIdx.x >> 6, first = wave & ~(s.lanes / 64 - 1);
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[wave][i] = dot[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dot[i] = 0.f;
+        for (int v = 0; v < s.lanes / 64; ++v) dot[i] += part[first + v][i];
+      }
+    }
+    if (live && lane == 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j0 + i < s.k) dw[t * s.k + j0 + i] = at[i] >= 0 && at[i] < s.rows ? dot[i] : 0.f;
+  }
+}
+
+static int key_bits(int G) {
+  int b = 1;
+  while ((1 << b) <= G) ++b;
+  return b;
+}
+
+static int64_t route_blocks(int64_t n) { return (n + kSortBlock - 1) / kSortBlock; }
+
+// Checks that the row kernels share, and their launch shape: threads per token are the
+// power of two (16 to 256) that covers the row's 16-byte units.
+static int row_shape(int64_t T, int k, int H, int elem, int64_t* grid, RowShape* s) {
+  if (T < 0 || k < 0 || H < 0) return KG_ERR_SHAPE;
+  if (H > (1 << 24) || k > 4096 || (k > 0 && T > (int64_t)(INT32_MAX - 1) / k) || T > INT32_MAX - 1)
+    return KG_ERR_UNSUPPORTED;
+  s->T = T;
+  s->rows = T * k;
+  s->k = k;
+  s->H = H;
+  const int64_t units = ((int64_t)H * elem + 15) / 16;
+  s->lanes = 16;
+  while (s->lanes < 256 && s->lanes < units) s->lanes *= 2;
+  const int per = 256 / s->lanes;
+  *grid = (T + per - 1) / per;
+  return KG_OK;
+}
+
+}  // namespace kg
+
+using namespace kg;
+
+extern "C" int64_t kg_route_workspace_bytes(int64_t T, int k, int G) {
+  if (T < 0 || k < 0 || G < 0 || G > kRouteMaxGroups || k > 4096 || T > INT32_MAX - 1 ||
+      (k > 0 && T > (int64_t)(INT32_MAX - 1) / k))
+    return -1;
+  const int64_t n = T * k;
+  return n <= kSoloSlots ? 0 : (route_blocks(n) + 1) * (G + 1) * 4;
+}
+
+extern "C" int kg_route(const int32_t* idx, int64_t T, int k, int G, int32_t* ks, int32_t* pos,
+                        int32_t* src, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (T < 0 || k < 0 || G < 0 || workspace_bytes < 0) return KG_ERR_SHAPE;
+  const int64_t need = kg_route_workspace_bytes(T, k, G);
+  if (need < 0) return KG_ERR_UNSUPPORTED;
+  const int64_t n = T * k;
+  if (G == 0 && n == 0) return KG_OK;
+  if ((G > 0 && ks == nullptr) || (n > 0 && (idx == nullptr || pos == nullptr)) ||
+      (need > 0 && workspace == nullptr))
+    return KG_ERR_NULL;
+  if (workspace_bytes < need) return KG_ERR_SHAPE;
+  if (((uintptr_t)idx | (uintptr_t)ks | (uintptr_t)pos | (uintptr_t)src |
+       (need > 0 ? (uintptr_t)workspace : 0)) & 3)
+    return KG_ERR_ALIGN;
+  const struct { const void* p; size_t n; } r[5] = {{idx, (size_t)n * 4}, {ks, (size_t)G * 4},
+      {pos, (size_t)n * 4}, {src, (size_t)n * 4}, {workspace, (size_t)need}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if (ranges_overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return KG_ERR_ALIAS;
+  const int bits = key_bits(G), keys = G + 1;
+  if (n <= kSoloSlots) {
+    const size_t lds = (size_t)(kSoloWaves + 1) * keys * 4;
+    if (lds > 65536 &&
+        hipFuncSetAttribute((const void*)kg_route_solo_kernel,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+      return KG_ERR_HIP;
+    return launch(kg_route_solo_kernel, 1, 64 * kSoloWaves, lds, stream, idx, (int)n, G, bits, ks,
+                  pos, src);
+  }
+  const int64_t blocks = route_blocks(n);
+  int32_t* counts = (int32_t*)workspace;
+  int32_t* totals = counts + blocks * keys;
+  int rc = launch(kg_route_count_kernel, blocks, kSortThreads, (size_t)keys * 4, stream, idx, n, G,
+                  counts);
+  if (rc == KG_OK)
+    rc = launch(kg_route_scan_kernel, (keys + 63) / 64, 64, 0, stream, counts, (int)blocks, G,
+                totals);
+  if (rc == KG_OK)
+    rc = launch(kg_route_rank_kernel, blocks, kSortThreads, (size_t)(kSortWaves + 1) * keys * 4,
+                stream, idx, n, G, bits, counts, totals, ks, pos, src);
+  return rc;
+}
+
+extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k, int H,
+                           int type, void* Xp, void* stream) {
+  if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
+  const int elem = type == KG_ROWS_BF16 ? 2 : 4;
+  RowShape s;
+  int64_t grid;
+  const int rc = row_shape(T, k, H, elem, &grid, &s);
+  if (rc != KG_OK) return rc;
+  if (ldx < H) return KG_ERR_SHAPE;
+  if (s.rows == 0 || H == 0) return KG_OK;
+  if (X == nullptr || pos == nullptr || Xp == nullptr) return KG_ERR_NULL;
+  if ((((uintptr_t)X | (uintptr_t)Xp) & (elem - 1)) || ((uintptr_t)pos & 3)) return KG_ERR_ALIGN;
+  const size_t out = (size_t)s.rows * H * elem;
+  if (ranges_overlap(X, ((size_t)(T - 1) * ldx + H) * elem, Xp, out) ||
+      ranges_overlap(pos, (size_t)s.rows * 4, Xp, out))
+    return KG_ERR_ALIAS;
+  auto fn = elem == 2 ? kg_dispatch_kernel<2> : kg_dispatch_kernel<4>;
+  return launch(fn, grid, 256, 0, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Xp);
+}
+
+extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k,
+                               int H, void* Q, float* sa, void* stream) {
+  RowShape s;
+  int64_t grid;
+  const int rc = row_shape(T, k, H, 2, &grid, &s);
+  if (rc != KG_OK) return rc;
+  if (ldx < H) return KG_ERR_SHAPE;
+  if (H % 16 != 0) return KG_ERR_ALIGN;
+  if (s.rows == 0 || H == 0) return KG_OK;
+  if (X == nullptr || pos == nullptr || Q == nullptr || sa == nullptr) return KG_ERR_NULL;
+  if (((uintptr_t)X & 1) || (((uintptr_t)pos | (uintptr_t)sa) & 3)) return KG_ERR_ALIGN;
+  const size_t nx = ((size_t)(T - 1) * ldx + H) * 2, nq = (size_t)s.rows * H;
+  const size_t ns = (size_t)((H + 127) / 128) * s.rows * 4, np = (size_t)s.rows * 4;
+  if (ranges_overlap(X, nx, Q, nq) || ranges_overlap(X, nx, sa, ns) ||
+      ranges_overlap(pos, np, Q, nq) || ranges_overlap(pos, np, sa, ns) ||
+      ranges_overlap(Q, nq, sa, ns))
+    return KG_ERR_ALIAS;
+  return launch(kg_dispatch_fp8_kernel, grid, 256, 0, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Q, sa);
+}
+
+extern "C" int kg_combine(const void* Y, const int32_t* pos, const float* w, void* out, int64_t ldo,
+                          int64_t T, int k, int H, int type, void* stream) {
+  if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
+  const int elem = type == KG_ROWS_BF16 ? 2 : 4;
+  RowShape s;
+  int64_t grid;
+  const int rc = row_shape(T, k, H, elem, &grid, &s);
+  if (rc != KG_OK) return rc;
+  if (ldo < H) return KG_ERR_SHAPE;
+  if (T == 0 || H == 0) return KG_OK;
+  if (out == nullptr || (s.rows > 0 && (Y == nullptr || pos == nullptr))) return KG_ERR_NULL;
+  if ((((uintptr_t)Y | (uintptr_t)out) & (elem - 1)) || (((uintptr_t)pos | (uintptr_t)w) & 3))
+    return KG_ERR_ALIGN;
+  const size_t no = ((size_t)(T - 1) * ldo + H) * elem;
+  if (ranges_overlap(Y, (size_t)s.rows * H * elem, out, no) ||
+      ranges_overlap(pos, (size_t)s.rows * 4, out, no) ||
+      ranges_overlap(w, (size_t)s.rows * 4, out, no))
+    return KG_ERR_ALIAS;
+  auto fn = elem == 2 ? kg_combine_kernel<true> : kg_combine_kernel<false>;
+  return launch(fn, grid, 256, 0, stream, (const unsigned char*)Y, pos, w, s,
+                (unsigned char*)out, ldo);
+}
+
+extern "C" int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, const int32_t* pos,
+                              const float* w, void* dY, float* dw, int64_t T, int k, int H,
+                              int type, void* stream) {
+  if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
+  const int elem = type == KG_ROWS_BF16 ? 2 : 4;
+  RowShape s;
+  int64_t grid;
+  const int rc = row_shape(T, k, H, elem, &grid, &s);
+  if (rc != KG_OK) return rc;
+  if (ldo < H) return KG_ERR_SHAPE;
+  if (s.rows == 0) return KG_OK;
+  if (pos == nullptr) return KG_ERR_NULL;
+  if (H > 0 && (dOut == nullptr || dY == nullptr || (dw != nullptr && Y == nullptr)))
+    return KG_ERR_NULL;
+  if ((((uintptr_t)dOut | (uintptr_t)Y | (uintptr_t)dY) & (elem - 1)) ||
+      (((uintptr_t)pos | (uintptr_t)w | (uintptr_t)dw) & 3))
+    return KG_ERR_ALIGN;
+  const size_t nd = ((size_t)(T - 1) * ldo + H) * elem, ny = (size_t)s.rows * H * elem;
+  const size_t np = (size_t)s.rows * 4;
+  const struct { const void* p; size_t n; } in[4] = {{dOut, nd}, {Y, ny}, {pos, np}, {w, np}};
+  for (int i = 0; i < 4; ++i)
+    if (ranges_overlap(in[i].p, in[i].n, dY, ny) || ranges_overlap(in[i].p, in[i].n, dw, np))
+      return KG_ERR_ALIAS;
+  if (ranges_overlap(dY, ny, dw, np)) return KG_ERR_ALIAS;
+  auto fn = elem == 2 ? kg_combine_bwd_kernel<true> : kg_combine_bwd_kernel<false>;
+  return launch(fn, grid, 256, 0, stream, (const unsigned char*)dOut, ldo, (const unsigned char*)Y, pos,
+                w, s, (unsigned char*)dY, dw);
+}

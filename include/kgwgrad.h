@@ -340,6 +340,163 @@ int kg_requant(const void* X, const float* xs, const int32_t* ks, int G, int H, 
 int kg_dgrad(const void* A, const float* sa, const void* W, const float* sw, void* D,
              const int32_t* ms, int G, int N, int K, int64_t M_total, int flags, void* stream);
 
+/*
+ * kg_fprop -- enqueue the forward product y = x . w^T of expert rows, the product whose
+ * gradients kg_dgrad (dx) and kg_wgrad (dw) compute. Expert g owns the contiguous rows
+ * [off[g], off[g+1]) of A, off[g+1] = off[g] + ms[g]; for such a row t and output n
+ *
+ *   D[t][n] = sum over kb of sa[kb][t] * sw[g][n/128][kb] *
+ *             sum_{k = 128 kb}^{min(K, 128 kb + 128) - 1} A[t][k] * W[g][n][k]
+ *
+ *   A   [M_total, K]                      fp8 e4m3fn bytes, row t at A + t * lda
+ *   sa  [ceil(K/128), M_total]            fp32, one scale per row per 128 channels
+ *   W   [G, N, K]                         fp8 e4m3fn bytes, K contiguous (the tensor that
+ *                                         kg_dgrad reads as its W [G, K, N])
+ *   sw  [G, ceil(N/128), ceil(K/128)]     fp32, one scale per 128 x 128 block of W
+ *   D   [M_total, N]                      fp32 (bf16 with KG_FLAG_D_BF16), row t at
+ *                                         element t * ldd
+ *   ms  [G] int32, device memory: rows per expert, in expert order (0 for any of them)
+ *   flags  KG_FLAG_FP8_MFMA and/or KG_FLAG_D_BF16, accuracy as for kg_dgrad
+ *
+ * K and lda are multiples of 16 (rows of whole 16-byte units), N is any size; A and W are
+ * 16-byte aligned, sa, sw and ms 4-byte aligned, D by its element (rows that start at
+ * 16-byte boundaries are stored faster). Errors before any launch: KG_ERR_DTYPE, KG_ERR_SHAPE
+ * (negative sizes, lda < K, ldd < N), KG_ERR_NULL, KG_ERR_ALIGN, KG_ERR_ALIAS (D overlapping
+ * an input), KG_ERR_UNSUPPORTED (G > 1024, N > 2^24, K or lda > 2^23, ldd > 2^30,
+ * M_total > 2^31 - 1), KG_ERR_HIP. An ms that holds a negative count or does not add up to
+ * M_total is reported by kg_status (KG_ERR_KSUM) and nothing is written. G, N or M_total
+ * == 0: KG_OK, no launch.
+ */
+int kg_fprop(const void* A, int64_t lda, const float* sa, const void* W, const float* sw, void* D,
+             int64_t ldd, const int32_t* ms, int G, int N, int K, int64_t M_total, int flags,
+             void* stream);
+
+/*
+ * kg_route -- enqueue the plan that puts tokens into expert order.
+ *
+ *   idx  [T, k] int32: the experts chosen for each token; an entry outside [0, G) is a
+ *        dropped slot (an expert held elsewhere, a full one)
+ *   ks   [G] int32 out: slots per expert, as kg_wgrad's ks and kg_fprop's ms
+ *   pos  [T, k] int32 out: the row of slot s = t * k + j in the order by (expert, s), the
+ *        dropped slots last; r for a kept slot, ~r (negative) for a dropped one
+ *   src  [T * k] int32 out, may be NULL: the slot s of row r, ~s for a dropped slot's row
+ *   workspace  device memory of kg_route_workspace_bytes(T, k, G) bytes (NULL where that is
+ *        0), 4-byte aligned; needs no initialisation. Calls that share one must not run
+ *        concurrently.
+ *
+ * The order is the same whatever the timing. Errors before any launch: KG_ERR_SHAPE (negative
+ * sizes, a workspace that is too small), KG_ERR_NULL, KG_ERR_ALIGN (4 bytes), KG_ERR_ALIAS,
+ * KG_ERR_UNSUPPORTED (G > 1024, k > 4096, T * k > 2^31 - 2), KG_ERR_HIP.
+ */
+int kg_route(const int32_t* idx, int64_t T, int k, int G, int32_t* ks, int32_t* pos, int32_t* src,
+             void* workspace, int64_t workspace_bytes, void* stream);
+/* Workspace of kg_route in bytes (0: none needed), or -1 for sizes it does not take. */
+int64_t kg_route_workspace_bytes(int64_t T, int k, int G);
+
+/* Element types of the row copies below (argument `type`). */
+#define KG_ROWS_BF16 0
+#define KG_ROWS_F32 1
+
+/*
+ * kg_dispatch, kg_dispatch_fp8 -- enqueue the copy of every token's row to its k expert rows.
+ *
+ *   X    [T, H] (bf16 or fp32; bf16 for kg_dispatch_fp8), row t at element t * ldx
+ *   pos  [T, k] int32 from kg_route
+ *   Xp   [T * k, H] out: X[t] at the rows of t's kept slots, zeros at the dropped slots'
+ *   Q    [T * k, H] out: the same rows as e4m3fn codes: for each row and 128 channels
+ *        (the last run may be shorter) s = amax / 448 (1 if amax is 0) and q = e4m3(x / s),
+ *        binary32 quotients rounded to nearest, as kg_requant's fp32 scales (amax skips NaNs)
+ *   sa   [ceil(H/128), T * k] fp32 out: those scales, as kg_fprop and kg_dgrad read them
+ *        (1 at the dropped slots' rows)
+ *
+ * Every row is written once if pos is a plan of kg_route; a value of pos that names no row
+ * (outside [0, T * k)) is passed over. The gradient of kg_dispatch is kg_combine with w
+ * NULL. Errors before any launch: KG_ERR_DTYPE, KG_ERR_SHAPE (negative sizes, ldx < H),
+ * KG_ERR_NULL, KG_ERR_ALIGN (tensors by their elements; H % 16 for kg_dispatch_fp8),
+ * KG_ERR_ALIAS, KG_ERR_UNSUPPORTED (H > 2^24, k > 4096, T * k > 2^31 - 2), KG_ERR_HIP.
+ */
+int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k, int H, int type,
+                void* Xp, void* stream);
+int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k, int H,
+                    void* Q, float* sa, void* stream);
+
+/*
+ * kg_combine -- enqueue out[t] = sum_j w[t][j] * Y[pos[t][j]] over t's kept slots, in fp32 in
+ * the order of j, rounded once to the output's type (zeros for a token without any).
+ *
+ *   Y    [T * k, H] (type: bf16 or fp32)
+ *   pos  [T, k] int32 from kg_route
+ *   w    [T, k] fp32, or NULL for weights of 1; a dropped slot's weight is not used
+ *   out  [T, H] of the same type, row t at element t * ldo
+ * Errors as kg_dispatch.
+ */
+int kg_combine(const void* Y, const int32_t* pos, const float* w, void* out, int64_t ldo,
+               int64_t T, int k, int H, int type, void* stream);
+
+/*
+ * kg_combine_bwd -- enqueue the gradients of kg_combine: for each slot with row r
+ *   dY[r] = w[t][j] * dOut[t] (rounded once; zeros for a dropped slot's row) and
+ *   dw[t][j] = sum_h dOut[t][h] * Y[r][h] in fp32, in an order that does not depend on timing
+ *   (0 for a dropped slot).
+ * w NULL: weights of 1; dw NULL: not computed, and Y is not read. Errors as kg_dispatch.
+ */
+int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, const int32_t* pos,
+                   const float* w, void* dY, float* dw, int64_t T, int k, int H, int type,
+                   void* stream);
+
+/* Kinds of an AdamW table (argument `kinds`, OR-ed). */
+#define KG_ADAMW_P_BF16 1 /* parameters are bf16, not fp32                                  */
+#define KG_ADAMW_G_BF16 2 /* gradients are bf16, not fp32                                   */
+#define KG_ADAMW_8BIT 4   /* states are e4m3 codes with fp32 scales per 128 elements        */
+
+/* One tensor of n consecutive elements. The states m and v are fp32; with KG_ADAMW_8BIT m
+   holds e4m3fn codes of the first moment and v of the square root of the second, each with
+   ceil(n/128) fp32 scales (value = code * scale); zeros in all of them are the start. copy
+   (may be NULL) receives the new parameters as bf16. */
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+  int64_t n;
+} kg_adamw_tensor;
+
+/*
+ * kg_adamw -- enqueue one AdamW step over all tensors of a table, in one launch:
+ *   g' = g * gscale;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2;
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, each operation rounded once. 8-bit states are rounded to nearest after the step
+ * (the parameters see the unrounded ones), with scale amax / 448 per block of 128
+ * elements; a nonzero sqrt(v) is never rounded to zero.
+ *
+ *   table  the image that kg_adamw_pack made on the host, copied to device memory by the
+ *          caller (8-byte aligned); valid as long as the tensors stay where they are
+ *   count, kinds  as given to kg_adamw_pack; items = kg_adamw_items(tensors, count)
+ *   step   1 for the first step; not used with dyn
+ *   gscale device fp32, or NULL for 1: a factor on every gradient (clipping, unscaling)
+ *   dyn    device fp32 {lr, 1 - beta1^step, 1 - beta2^step}, or NULL: read in the place of lr
+ *          and step, so that a captured graph can be replayed with new ones
+ *
+ * kg_adamw_pack (host only) returns KG_ERR_DTYPE, KG_ERR_SHAPE (a negative count or n, an
+ * image smaller than kg_adamw_table_bytes), KG_ERR_NULL, KG_ERR_ALIGN (each pointer by its
+ * element), KG_ERR_ALIAS (something a step writes overlaps anything else it touches) or
+ * KG_ERR_UNSUPPORTED. kg_adamw_items and kg_adamw_table_bytes return -1 for negative or too
+ * large sizes. kg_adamw returns KG_ERR_DTYPE, KG_ERR_SHAPE (negative sizes, step < 1, lr,
+ * eps or weight_decay < 0, beta outside [0, 1)), KG_ERR_NULL, KG_ERR_ALIGN,
+ * KG_ERR_UNSUPPORTED or KG_ERR_HIP; no tensors: KG_OK, no launch.
+ */
+int64_t kg_adamw_items(const kg_adamw_tensor* tensors, int count);
+int64_t kg_adamw_table_bytes(const kg_adamw_tensor* tensors, int count);
+int kg_adamw_pack(const kg_adamw_tensor* tensors, int count, int kinds, void* image,
+                  int64_t image_bytes);
+int kg_adamw(const void* table, int count, int64_t items, int kinds, double lr, double beta1,
+             double beta2, double eps, double weight_decay, int64_t step, const float* gscale,
+             const float* dyn, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
