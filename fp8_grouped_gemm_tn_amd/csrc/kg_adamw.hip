@@ -9,8 +9,8 @@
 //   p  = p * (1 - lr wd) - (m / (sqrt(v) * (1 - b2^t)^-1/2 + eps)) * (lr / (1 - b1^t))
 //
 // 8-bit states (KG_ADAMW_8BIT): each 128 consecutive elements of a tensor (the last block may
-// be shorter) share two fp32 scales. m is held as e4m3 codes of m * (448 / amax |m|) with
-// scale amax / 448; r = sqrt(v) as e4m3 codes of r * (448 / amax r) with scale amax / 448, so
+// be shorter) share two fp32 scales. With amax the block's largest |m|, m is held as e4m3
+// codes of m * (448 * fl(1 / amax)) with scale amax * fl(1 / 448); r = sqrt(v) likewise, so
 // that a block's v spans 2^36. A nonzero r never becomes zero (its code is at least the
 // smallest one): a lost r would divide the next step's m by eps alone. A block whose amax is
 // below 2^-118 (where 448 / amax would overflow) is held as zeros. p is updated with the new
@@ -159,8 +159,8 @@ __device__ __forceinline__ void store_codes(void* base, float* scales, int64_t a
   }
   const float amax = __uint_as_float(top);
   const bool kept = !(amax < 0x1p-118f);
-  const float inv = kept ? 448.0f / amax : 0.0f;
-  if (n > 0 && (threadIdx.x & 15) == 0) scales[at >> 7] = kept ? amax / 448.0f : 0.0f;
+  const float inv = kept ? 448.0f * (1.0f / amax) : 0.0f;
+  if (n > 0 && (threadIdx.x & 15) == 0) scales[at >> 7] = kept ? amax * (1.0f / 448.0f) : 0.0f;
   v2i w;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
