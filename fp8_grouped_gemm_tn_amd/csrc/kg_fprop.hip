@@ -133,104 +133,136 @@ __device__ __forceinline__ void store_run(void* D, int64_t at, int left, bool ve
 
 // ---------------------------------------------------------------------------- tiled kernel
 
-// BT tokens x BN outputs per workgroup of 8 waves (WT along the tokens); stages of one
-// 128-channel block: BN rows of W, BT rows of A, the BT token scales.
-template <int BT_, int BN_, int WT_>
+// BT tokens x BN outputs per workgroup of 8 waves (WT along the tokens, PER_CU such
+// workgroups per compute unit), two stages of one
+// 128-channel block in LDS: BN rows of W, BT rows of A, the BT token scales.
+template <int BT_, int BN_, int WT_, int PER_CU_>
 struct FCfg {
+  static constexpr int PER_CU = PER_CU_;  // workgroups per compute unit
   static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = 8 / WT_, THREADS = 512, TK = 128;
   static constexpr int TT = BT / WT / 16;  // 16-token tiles of a wave
   static constexpr int NI = BN / WN / 16;  // 16-output tiles of a wave
   static constexpr int NS = 2;
   static constexpr int OPW = BN * TK, OPT = BT * TK;
   static constexpr int SA_OFF = OPW + OPT;
-  static constexpr int SA_BYTES = (BT * 4 + 1023) / 1024 * 1024;
-  static constexpr int STAGE = SA_OFF + SA_BYTES;
-  static constexpr int LOADS_W = BN / 8, LOADS_T = BT / 8;  // 1 KB wave loads: 8 rows each
-  static constexpr int LOADS = LOADS_W + LOADS_T + SA_BYTES / 1024;
-  static constexpr int SLOTS = (LOADS + 7) / 8;
+  static constexpr int STAGE = SA_OFF + BT * 4;
+  static constexpr int LW = BN / 64, LT = BT / 64;  // a wave's 1 KB loads of W and of A
+  static constexpr int LOADS = LW + LT + 1;         // ... and one of token scales
   static_assert(NI % 2 == 0 && BN / WN <= 128 && 128 % (BN / WN) == 0,
                 "a wave's outputs lie in one weight-scale block");
+  static_assert(BT <= 512 && BT % 64 == 0 && BN % 64 == 0, "whole wave loads");
 };
 
-// Row r's 16-byte chunk c lies in slot c ^ fkey(r) of the row's 128 bytes. The 16-byte LDS
-// reads go 32 lanes at a time and are free of conflicts when their chunks are distinct
-// modulo 512 bytes: the 16 rows that two lane groups name (16 neighbouring ones for
-// tokens, frow's for W) share r mod 4 four at a time, and those four have distinct keys.
-__device__ __forceinline__ constexpr int fkey(int r) {
-  const int y = (r >> 2) & 7;
-  return 2 * ((y & 3) ^ (y >> 2));
+// LDS layout: a row's 128 channel bytes in order, but its 16-byte chunk c in slot c ^ key.
+// A 16-byte LDS read serves 16 lanes at a time (lanes 0-3, 12-15, 20-27, then the other 16 of
+// the lower half; the upper half alike), without conflicts if their chunks are distinct
+// modulo 256 bytes. With key = m & 7 for the row that MFMA row (or column) m reads they are:
+// tokens lie in that order, W's rows in frow's. (Measured: 0 conflict cycles, where keys
+// chosen for 32 lanes and 512 bytes cost one per access.)
+__device__ __forceinline__ constexpr int key_t(int r) { return r & 7; }
+__device__ __forceinline__ constexpr int key_w(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
+
+// 4 bytes per lane global -> LDS at `lds` + 4 * lane (see load16_lds).
+__device__ __forceinline__ void load4_lds(v4i r, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(r), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+               : "memory", "m0");
 }
 
+// This wave's loads of one tile. Load x of an operand takes its rows 8 (wave + 8 x) ..
+// 8 (wave + 8 x) + 7. Rows that the tile lacks, channels past K, and stages past the last
+// block read as zeros; every stage is LOADS loads of each wave, so waits can count them.
 template <class C>
-__device__ __forceinline__ void f_load_stage(const FParams& p, unsigned char* st, int64_t row0,
-                                             int rows, int g, int n0, int kb) {
-  const int w = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int k0 = kb * C::TK;
-  const int kin = min(C::TK, p.K - k0);       // channels of this block that exist
-  const int outs = min(C::BN, p.N - n0);      // outputs of this tile that exist
-  const v4i rw = make_rsrc(p.W + ((int64_t)g * p.N + n0) * p.K + k0,
-                           (uint32_t)((outs - 1) * p.K + kin));
-  const v4i rt = make_rsrc(p.A + row0 * p.lda + k0, (uint32_t)((rows - 1) * (int)p.lda + kin));
-  const v4i rs = make_rsrc(p.sa + (int64_t)kb * p.M_total + row0, (uint32_t)(rows * 4));
-  const uint32_t base = lds_addr(st);
-#pragma unroll
-  for (int s = 0; s < C::SLOTS; ++s) {
-    const int k = w + 8 * s;
-    if (k >= C::LOADS) break;
-    const uint32_t to = base + 1024 * k;
-    if (k < C::LOADS_W + C::LOADS_T) {
-      const bool is_w = k < C::LOADS_W;
-      const int r = 8 * (is_w ? k : k - C::LOADS_W) + (lane >> 3);
-      const int ch = (lane & 7) ^ fkey(r);
-      const uint32_t off = 16 * ch < kin ? (uint32_t)(r * (is_w ? p.K : (int)p.lda) + 16 * ch)
-                                         : kOobOffset;
-      load16_lds(is_w ? rw : rt, to, off);
+struct FLoads {
+  const unsigned char *W, *A;
+  const float* sa;
+  int64_t M_total;
+  int K, lda, nk, outs, rows, wave;
+  uint32_t offw, offt, offs, lds;
+  bool endw, endt;  // this lane's chunk lies past the last block's channels
+  __device__ __forceinline__ void setup(const FParams& p, const unsigned char* smem, int64_t row0,
+                                        int rows_, int g, int n0, int nk_) {
+    wave = uniform(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    W = p.W + ((int64_t)g * p.N + n0) * p.K;
+    A = p.A + row0 * p.lda;
+    sa = p.sa + row0;
+    M_total = p.M_total;
+    K = p.K, lda = (int)p.lda, nk = nk_;
+    outs = min(C::BN, p.N - n0), rows = rows_;
+    const int r = 8 * wave + (lane >> 3);
+    const int cw = (lane & 7) ^ key_w(r), ct = (lane & 7) ^ key_t(r);
+    offw = (uint32_t)(r * K + 16 * cw);
+    offt = (uint32_t)(r * lda + 16 * ct);
+    const int last = K - (nk - 1) * C::TK;
+    endw = 16 * cw >= last;
+    endt = 16 * ct >= last;
+    // the scales: 64 tokens per wave (with fewer than 512 tokens several waves load the same
+    // ones to the same place)
+    const int part = wave % (C::BT / 64);
+    offs = 256 * part + 4 * lane;
+    lds = lds_addr(smem);
+  }
+  __device__ __forceinline__ int channels(int kb) const { return min(C::TK, K - kb * C::TK); }
+  __device__ __forceinline__ void load(int kw, int kt, int x) const {
+    if (x < C::LW) {
+      const v4i r = make_rsrc(W + (int64_t)kw * C::TK,
+                              kw < nk ? (uint32_t)((outs - 1) * K + channels(kw)) : 0u);
+      load16_lds(r, lds + (kw & 1) * C::STAGE + 1024 * (wave + 8 * x),
+                 (offw + (uint32_t)(64 * x * K)) | (kw == nk - 1 && endw ? kOobOffset : 0u));
+    } else if (x < C::LW + C::LT) {
+      const int y = x - C::LW;
+      const v4i r = make_rsrc(A + (int64_t)kt * C::TK,
+                              kt < nk ? (uint32_t)((rows - 1) * lda + channels(kt)) : 0u);
+      load16_lds(r, lds + (kt & 1) * C::STAGE + C::OPW + 1024 * (wave + 8 * y),
+                 (offt + (uint32_t)(64 * y * lda)) | (kt == nk - 1 && endt ? kOobOffset : 0u));
     } else {
-      load16_lds(rs, to, 1024 * (k - C::LOADS_W - C::LOADS_T) + 16 * lane);
+      const v4i r = make_rsrc(sa + (int64_t)kt * M_total, kt < nk ? (uint32_t)(rows * 4) : 0u);
+      load4_lds(r, lds + (kt & 1) * C::STAGE + C::SA_OFF + 256 * (wave % (C::BT / 64)), offs);
     }
   }
+};
+
+// Waits for all but N of this wave's vector-memory operations and for all its LDS reads, then
+// for the workgroup's other waves.
+template <int N>
+__device__ __forceinline__ void f_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(N) & ~0xF00);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-template <class C, bool FAST>
-__device__ __forceinline__ void f_compute(const unsigned char* st, float swv,
-                                          v4f (&acc)[C::NI][C::TT]) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int q = lane >> 4, j = lane & 15;
-  const int wt = w % C::WT, wn = w / C::WT;
-  const int t0 = wt * C::TT * 16, n0 = wn * C::NI * 16;
-  const float* sS = (const float*)(st + C::SA_OFF);
-  auto frag = [&](int off, int r) {
-    const unsigned char* row = st + off + r * C::TK;
-    const int key = fkey(r);
-    Frag<FAST> f;
-    f.set(*(const v4i*)(row + 16 * (q ^ key)), *(const v4i*)(row + 16 * ((q + 4) ^ key)));
-    return f;
-  };
-  Frag<FAST> tf[C::TT];
-  float s[C::TT];
-#pragma unroll
-  for (int tt = 0; tt < C::TT; ++tt) {
-    tf[tt] = frag(C::OPW, t0 + 16 * tt + j);
-    s[tt] = sS[t0 + 16 * tt + j] * swv;
-  }
-#pragma unroll
-  for (int i = 0; i < C::NI; ++i) {
-    const Frag<FAST> wf = frag(0, n0 + frow(i, j));
-    v4f part[C::TT];
-#pragma unroll
-    for (int tt = 0; tt < C::TT; ++tt) part[tt] = block_sum(wf, tf[tt]);
-#pragma unroll
-    for (int tt = 0; tt < C::TT; ++tt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(s[tt], part[tt][r], acc[i][tt][r]);
-  }
-}
+// Weight scales through scalar loads: a vector load among the stages' would make the
+// compiler wait for them.
+typedef __attribute__((address_space(4))) const float ConstFloat;
 
+// The loop over the blocks. While block kb is computed, W's block kb + 1 loads into the other
+// W buffer and the tokens' block kb + 2 into the buffer that kb's came from: the token
+// fragments are read one block ahead, each right after its last MFMA of the block before, so
+// their buffer is free during the whole block. The waves meet twice per block: before the
+// next tokens are read (they and nothing later have to be there), and at the block's end
+// (the next W, and every wave's token reads). Each load has most of a block's time to arrive.
+//
+// A partial sum is scaled and added LAG MFMAs after it was issued, four fmas between two
+// MFMAs, so neither waits for the other; the empty asm keeps the compiler from moving the
+// sums to the end of the block (which spilled), sched_barrier keeps the interleaving.
+// The loads are spread over the block's first half: issued in one burst they block the
+// wave's own instruction stream until the memory pipeline takes them.
+//
+// On 32768 tokens of 8 experts, K 7168, N 4096 (fp8 MFMA, bf16 out, 256 x 256): 1480 us with
+// a burst of loads, a vector load of the weight scale and no fragments ahead; 1110 with the
+// scale through a scalar load and four waves loading; 870 in this form, 847 without LDS
+// conflicts and with the loads in the first half. 1.64 M cycles, MFMA busy for 0.95 M of
+// them; the clock falls to 1.75 GHz under this load (1.98 without the loads).
 template <class C, bool FAST, bool OUTB>
-__global__ __launch_bounds__(C::THREADS, 1) void kg_fprop_kernel(FParams p) {
+__global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   __shared__ int64_t wsum_k[kMaxWaves];
   __shared__ int32_t wsum_b[kMaxWaves];
+  constexpr int LAG = 3, S = C::NI * C::TT;
   Sched s = sched_carve(smem + C::NS * C::STAGE, p.G);
   if (sched_build<C::THREADS>(p.ms, p.G, C::BT, p.M_total, s, wsum_k, wsum_b) != KG_OK) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = KG_ERR_KSUM;
@@ -238,15 +270,20 @@ __global__ __launch_bounds__(C::THREADS, 1) void kg_fprop_kernel(FParams p) {
   }
   const int mt_total = s.boff[p.G], total = mt_total * p.tiles_n;
   const int grid = gridDim.x, b = blockIdx.x;
+  // XCD-contiguous runs when the items take several rounds, as in kg_dgrad
   const int slot = (grid % 8 == 0 && total > grid) ? (b % 8) * (grid / 8) + b / 8 : b;
   const int nk = (p.K + C::TK - 1) / C::TK, nsc = (p.N + 127) / 128;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, j = lane & 15;
   const int wt = w % C::WT, wn = w / C::WT;
+  const int c0 = 16 * (q ^ (j & 7)), c1 = 16 * ((q + 4) ^ (j & 7));
+  const unsigned char* fragw = smem + (wn * C::NI * 16 + frow(0, j)) * C::TK;
+  const unsigned char* fragt = smem + C::OPW + (wt * C::TT * 16 + j) * C::TK;
+  const unsigned char* scale = smem + C::SA_OFF + 4 * (wt * C::TT * 16 + j);
   for (int base = 0; base < total; base += grid) {
     const int idx = base + slot;
     if (idx >= total) break;
-    // panels of kPanelM m-tiles, m-tiles fastest, as in kg_dgrad
+    // panels of kPanelM m-tiles, m-tiles fastest, as in kg_dgrad (2 or 8: the same times)
     const int per_panel = kPanelM * p.tiles_n;
     const int panel = idx / per_panel, wi = idx - panel * per_panel;
     const int pm = min(kPanelM, mt_total - panel * kPanelM);
@@ -257,31 +294,84 @@ __global__ __launch_bounds__(C::THREADS, 1) void kg_fprop_kernel(FParams p) {
       if (s.boff[mid] <= mtg) lo_g = mid; else hi_g = mid;
     }
     const int g = uniform(lo_g);
-    const int64_t row0 = s.off[g] + (int64_t)(mtg - s.boff[g]) * C::BT;
+    // (rows fit 31 bits)
+    const int row0 = uniform((int)s.off[g] + (mtg - s.boff[g]) * C::BT);
     const int rows = uniform((int)min((int64_t)C::BT, s.off[g + 1] - row0));
     const int n0 = nt * C::BN;
-    const int nw = n0 + wn * C::NI * 16;  // this wave's outputs, one weight-scale block
-    const float* swg = p.sw + ((int64_t)g * nsc + min(nw / 128, nsc - 1)) * nk;
+    const int nw = n0 + wn * C::NI * 16;  // this wave's outputs, in one weight-scale block
+    const ConstFloat* swg =
+        (const ConstFloat*)p.sw + ((int64_t)g * nsc + min(nw / 128, nsc - 1)) * nk;
     v4f acc[C::NI][C::TT];
 #pragma unroll
     for (int i = 0; i < C::NI; ++i)
 #pragma unroll
       for (int tt = 0; tt < C::TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
-    __syncthreads();  // every wave is done with the previous item's stages
-    if (nk > 0) f_load_stage<C>(p, smem, row0, rows, g, n0, 0);
+    FLoads<C> L;
+    L.setup(p, smem, row0, rows, g, n0, nk);
+    Frag<FAST> tf[C::TT], wf[2];
+    float sc[C::TT];
+    auto read_t = [&](int kb, int tt) {
+      const unsigned char* r = fragt + (kb & 1) * C::STAGE + 16 * tt * C::TK;
+      tf[tt].set(*(const v4i*)(r + c0), *(const v4i*)(r + c1));
+      sc[tt] = *(const float*)(scale + (kb & 1) * C::STAGE + 64 * tt);
+    };
+    auto read_w = [&](int kb, int i) {
+      const unsigned char* r = fragw + (kb & 1) * C::STAGE + frow(i, 0) * C::TK;
+      wf[i & 1].set(*(const v4i*)(r + c0), *(const v4i*)(r + c1));
+    };
+    f_meet<0>();  // every wave is done with the previous item's stages
+    float swv = 0.f;
+    if (nk > 0) {
+      swv = swg[0];
+#pragma unroll
+      for (int x = C::LW; x < C::LOADS; ++x) L.load(0, 0, x);
+#pragma unroll
+      for (int x = 0; x < C::LW; ++x) L.load(0, 0, x);
+#pragma unroll
+      for (int x = C::LW; x < C::LOADS; ++x) L.load(0, 1, x);
+      f_meet<C::LT + 1>();
+#pragma unroll
+      for (int tt = 0; tt < C::TT; ++tt) read_t(0, tt);
+      f_meet<C::LT + 1>();
+    }
     for (int kb = 0; kb < nk; ++kb) {
-      // stage kb is in buffer kb % 2; stage kb + 1 loads into the other one meanwhile
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-      __syncthreads();
-      if (kb + 1 < nk)
-        f_load_stage<C>(p, smem + ((kb + 1) & 1) * C::STAGE, row0, rows, g, n0, kb + 1);
-      f_compute<C, FAST>(smem + (kb & 1) * C::STAGE, swg[kb], acc);
+      read_w(kb, 0);
+      float sx[C::TT];
+#pragma unroll
+      for (int tt = 0; tt < C::TT; ++tt) sx[tt] = sc[tt] * swv;
+      v4f part[LAG + 1];
+      auto add = [&](int u) {
+        const int i = u / C::TT, tt = u % C::TT;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][tt][r] = fmaf(sx[tt], part[u % (LAG + 1)][r], acc[i][tt][r]);
+        asm volatile("" : "+v"(acc[i][tt]));
+      };
+#pragma unroll
+      for (int u = 0; u < S; ++u) {
+        const int i = u / C::TT, tt = u % C::TT;
+        // the tokens' next block is there (of the loads, W's and theirs after it may not be)
+        if (u == S - C::TT) f_meet<C::LOADS>();
+        if (tt == 0 && i + 1 < C::NI) read_w(kb, i + 1);
+        part[u % (LAG + 1)] = block_sum(wf[i & 1], tf[tt]);
+        if (i == C::NI - 1) read_t(kb + 1, tt);  // (past the last block: not used)
+        if (u >= LAG) add(u - LAG);
+#pragma unroll
+        for (int x = 0; x < C::LOADS; ++x)
+          if (x * (S / 2) / C::LOADS == u) L.load(kb + 1, kb + 2, x);
+        if (u == S / 2) swv = swg[min(kb + 1, nk - 1)];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int u = S - LAG; u < S; ++u) add(u);
+      // W's next block is there, and the tokens' has been read
+      f_meet<C::LT + 1>();
     }
 #pragma unroll
     for (int tt = 0; tt < C::TT; ++tt) {
       const int r = (wt * C::TT + tt) * 16 + j;
       if (r >= rows) continue;
-      const int64_t at = (row0 + r) * p.ldd;
+      const int64_t at = (int64_t)(row0 + r) * p.ldd;
 #pragma unroll
       for (int i = 0; i < C::NI; i += 2) {
         const int n = nw + 16 * i + 8 * q;
@@ -289,13 +379,20 @@ __global__ __launch_bounds__(C::THREADS, 1) void kg_fprop_kernel(FParams p) {
       }
     }
   }
+  // no load into this workgroup's LDS outlives it
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 }
 
 // ------------------------------------------------------------------------ streaming kernel
 
-// A workgroup computes 32 outputs of one expert for all its rows, 16 TT at a time. Its 8
-// waves take the blocks of the contraction axis in turn, each adding up its blocks in
-// registers; the waves' sums are added in LDS in a fixed order. Grid: G x ceil(N / 32).
+// A workgroup computes 32 outputs of one expert for all its rows, 16 TT at a time: grid
+// G x ceil(N / 32). Its 8 waves take the blocks of the contraction axis in turn, each adding
+// up its blocks in registers, with the next block's operands on their way; the waves' sums
+// are added in LDS in a fixed order. A lane reads 32 neighbouring channels of a row, so a
+// row's 128 bytes go to four lanes of one load.
+//
+// Bound by W's bytes: 64 rows through 32 experts of 4096 x 7168 take 127 us (7.4 TB/s; 138
+// with one block's loads at a time). 64 outputs per workgroup: 139 us.
 constexpr int kStreamWaves = 8, kStreamN = 32;
 
 // Offsets by a scan of ms in every wave. Returns false if ms is inconsistent.
@@ -322,19 +419,13 @@ __device__ __forceinline__ bool find_rows(const FParams& p, int g, int64_t* row0
   return neg == 0 && sum == p.M_total;
 }
 
-// 16 bytes at p + off, zeros if they lie past `limit`.
-__device__ __forceinline__ v4i load_in(const unsigned char* p, int off, int limit) {
-  v4i x = {0, 0, 0, 0};
-  if (off < limit) x = *(const v4i*)(p + off);
-  return x;
-}
-
 template <int TT, bool FAST, bool OUTB>
 __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FParams p) {
-  __shared__ v4f sums[kStreamWaves][2 * TT][64];
+  constexpr int NJ = kStreamN / 16;
+  __shared__ v4f sums[kStreamWaves][NJ * TT][64];
   const int per = p.tiles_n;  // workgroups per expert
   const int g = blockIdx.x / per, n0 = (blockIdx.x - g * per) * kStreamN;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, j = lane & 15;
   int64_t row0;
   int rows;
@@ -342,75 +433,104 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = KG_ERR_KSUM;
     return;
   }
-  const int nk = (p.K + 127) / 128, nsc = (p.N + 127) / 128;
-  const float* swg = p.sw + ((int64_t)g * nsc + n0 / 128) * nk;
-  const unsigned char* wrow[2];
-  bool won[2];
+  const int nk = (p.K + 127) / 128, nfull = p.K / 128, nsc = (p.N + 127) / 128;
+  const ConstFloat* swg = (const ConstFloat*)p.sw + ((int64_t)g * nsc + n0 / 128) * nk;
+  // rows past the end name the last one: what they give is not stored
+  const unsigned char* wrow[NJ];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int n = n0 + frow(i, j);
-    won[i] = n < p.N;
-    wrow[i] = p.W + ((int64_t)g * p.N + (won[i] ? n : 0)) * p.K;
-  }
+  for (int i = 0; i < NJ; ++i)
+    wrow[i] = p.W + ((int64_t)g * p.N + min(n0 + frow(i, j), p.N - 1)) * p.K + 32 * q;
   for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
     const unsigned char* arow[TT];
-    bool aon[TT];
     const float* sa[TT];
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
-      const int r = r0 + 16 * tt + j;
-      aon[tt] = r < rows;
-      arow[tt] = p.A + (row0 + (aon[tt] ? r : 0)) * p.lda;
-      sa[tt] = p.sa + row0 + (aon[tt] ? r : 0);
+      const int64_t r = row0 + min(r0 + 16 * tt + j, rows - 1);
+      arow[tt] = p.A + r * p.lda + 32 * q;
+      sa[tt] = p.sa + r;
     }
-    v4f acc[2][TT];
+    v4f acc[NJ][TT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NJ; ++i)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int kb = w; kb < nk; kb += kStreamWaves) {
-      const int k0 = kb * 128 + 32 * q;  // a lane's 32 channels are neighbours
-      Frag<FAST> wf[2], tf[TT];
+    auto block = [&](const v4i (&wx)[NJ][2], const v4i (&tx)[TT][2], const float (&s)[TT], float swv) {
+      Frag<FAST> tf[TT];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int lim = won[i] ? p.K : 0;
-        wf[i].set(load_in(wrow[i], k0, lim), load_in(wrow[i], k0 + 16, lim));
-      }
-      const float swv = swg[kb];
-      float s[TT];
+      for (int tt = 0; tt < TT; ++tt) tf[tt].set(tx[tt][0], tx[tt][1]);
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        const int lim = aon[tt] ? p.K : 0;
-        tf[tt].set(load_in(arow[tt], k0, lim), load_in(arow[tt], k0 + 16, lim));
-        s[tt] = sa[tt][(int64_t)kb * p.M_total] * swv;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < NJ; ++i) {
+        Frag<FAST> wf;
+        wf.set(wx[i][0], wx[i][1]);
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
-          const v4f part = block_sum(wf[i], tf[tt]);
+          const v4f part = block_sum(wf, tf[tt]);
+          const float sx = s[tt] * swv;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(s[tt], part[r], acc[i][tt][r]);
+          for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(sx, part[r], acc[i][tt][r]);
         }
+      }
+    };
+    v4i wx[2][NJ][2], tx[2][TT][2];
+    float s[2][TT];
+    auto load = [&](int kb, int h) {
+#pragma unroll
+      for (int i = 0; i < NJ; ++i) {
+        wx[h][i][0] = *(const v4i*)(wrow[i] + kb * 128);
+        wx[h][i][1] = *(const v4i*)(wrow[i] + kb * 128 + 16);
+      }
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        tx[h][tt][0] = *(const v4i*)(arow[tt] + kb * 128);
+        tx[h][tt][1] = *(const v4i*)(arow[tt] + kb * 128 + 16);
+        s[h][tt] = sa[tt][(int64_t)kb * p.M_total];
+      }
+    };
+    int kb = w;
+    if (kb < nfull) load(kb, 0);
+    for (; kb < nfull; kb += 2 * kStreamWaves) {
+      const int k1 = kb + kStreamWaves, k2 = kb + 2 * kStreamWaves;
+      if (k1 < nfull) load(k1, 1);
+      block(wx[0], tx[0], s[0], swg[kb]);
+      if (k2 < nfull) load(k2, 0);
+      if (k1 < nfull) block(wx[1], tx[1], s[1], swg[k1]);
+    }
+    if (nfull < nk && w == nfull % kStreamWaves) {  // the last block's K % 128 channels
+      const int left = p.K - nfull * 128 - 32 * q;
+      const v4i zero = {0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < NJ; ++i)
+          wx[0][i][h] = 16 * h < left ? *(const v4i*)(wrow[i] + nfull * 128 + 16 * h) : zero;
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+          tx[0][tt][h] = 16 * h < left ? *(const v4i*)(arow[tt] + nfull * 128 + 16 * h) : zero;
+      }
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) s[0][tt] = sa[tt][(int64_t)nfull * p.M_total];
+      block(wx[0], tx[0], s[0], swg[nfull]);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NJ; ++i)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) sums[w][i * TT + tt][lane] = acc[i][tt];
     __syncthreads();
-    if (w < TT) {  // wave w joins and stores token tile w
+    // wave w joins and stores pair (w / TT) of output tiles of token tile w % TT
+    if (w < TT * NJ / 2) {
+      const int tt = w % TT, i0 = 2 * (w / TT);
       v4f x[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[i] = sums[0][i * TT + w][lane];
+        x[i] = sums[0][(i0 + i) * TT + tt][lane];
 #pragma unroll
         for (int v = 1; v < kStreamWaves; ++v) {
-          const v4f y = sums[v][i * TT + w][lane];
+          const v4f y = sums[v][(i0 + i) * TT + tt][lane];
 #pragma unroll
           for (int r = 0; r < 4; ++r) x[i][r] += y[r];
         }
       }
-      const int r = r0 + 16 * w + j, n = n0 + 8 * q;
+      const int r = r0 + 16 * tt + j, n = n0 + 16 * i0 + 8 * q;
       if (r < rows) store_run<OUTB>(p.D, (row0 + r) * p.ldd + n, p.N - n, p.vec, x[0], x[1]);
     }
     __syncthreads();
@@ -419,7 +539,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
 
 struct FLaunch {
   const void* fn;
-  int bt, bn, lds, id;
+  int bt, bn, lds, per_cu, id;
 };
 
 template <class C>
@@ -428,7 +548,7 @@ static FLaunch f_tiled(bool fast, bool outb, int id) {
                                 : (const void*)kg_fprop_kernel<C, true, false>)
                         : (outb ? (const void*)kg_fprop_kernel<C, false, true>
                                 : (const void*)kg_fprop_kernel<C, false, false>);
-  return FLaunch{fn, C::BT, C::BN, C::NS * C::STAGE, id};
+  return FLaunch{fn, C::BT, C::BN, C::NS * C::STAGE, C::PER_CU, id};
 }
 
 template <int TT>
@@ -437,7 +557,49 @@ static FLaunch f_stream(bool fast, bool outb) {
                                 : (const void*)kg_fprop_stream_kernel<TT, true, false>)
                         : (outb ? (const void*)kg_fprop_stream_kernel<TT, false, true>
                                 : (const void*)kg_fprop_stream_kernel<TT, false, false>);
-  return FLaunch{fn, 16 * TT, kStreamN, 0, -1};
+  return FLaunch{fn, 16 * TT, kStreamN, 0, 1, -1};
+}
+
+// The tiles that a launch takes: FastBig 256 x 256 for the fp8 MFMA, ExactBig 128 x 256 for
+// the bf16 MFMA (whose widened token fragments leave no room for 256 x 256: 1696 us spilled,
+// 1695 us here on the 32768-token problem above; 256 x 128 1707), Small 128 x 128 with two
+// workgroups per compute unit for either.
+using FastBig = FCfg<256, 256, 4, 1>;
+using ExactBig = FCfg<128, 256, 2, 1>;
+using Small = FCfg<128, 128, 4, 2>;
+
+// Which kernel and tile. The experts' sizes are known on the device only, so this goes by
+// M_total and G; every choice is right for every distribution of the rows.
+//  * Streaming up to 8 rows per expert on average, and up to 64 while M_total * N <= 2^19
+//    (few rows in all: a tile's time is then the latency of its blocks, 0.7 us each).
+//    K = 7168, N = 4096, streaming / Small: 32 experts of 2, 8, 16 rows 127/153, 164/167,
+//    231/170 us; 4 experts of 16, 32, 64 rows 27/41, 37/41, 71/42; 1 of 16, 64, 128 rows
+//    13/39, 23/39, 42/40.
+//    TT token tiles hold an expert's rows: the average, or twice it where several experts
+//    share M_total unevenly (4 experts of 16 rows, TT 1, 2, 4: 30, 27, 32 us).
+//  * Else the big or the small tile by their estimated rounds over the compute units times
+//    a round's time per block, in tenths of a microsecond: 15 and 12 (7 where the
+//    tiles are fewer than the compute units), exact products 18 and 23 (10). 32 experts of
+//    32, 64, 97, 128 rows, FastBig / Small: 211/171, 223/208, 233/241, 241/273 us; 4096
+//    rows, one expert, N = 7168, K = 2048: 67/84.
+static FLaunch f_choose(int64_t M, int G, int N, int cus, bool fast, bool outb) {
+  const int64_t avg = (M + G - 1) / G;
+  if (avg <= 8 || (avg <= 64 && M * N <= (1 << 19))) {
+    const int64_t rows = G == 1 ? avg : 2 * avg;
+    return rows <= 16 ? f_stream<1>(fast, outb) : rows <= 32 ? f_stream<2>(fast, outb)
+                                                             : f_stream<4>(fast, outb);
+  }
+  const int64_t live = G < M ? G : M;
+  auto cost = [&](int bt, int bn, int per_cu, int round, int first) {
+    const int64_t mt = M / bt + live / 2 > live ? M / bt + live / 2 : live;
+    const int64_t tiles = mt * ((N + bn - 1) / bn), at_once = (int64_t)cus * per_cu;
+    return tiles <= cus ? first : (tiles + at_once - 1) / at_once * round;
+  };
+  const int64_t small = cost(Small::BT, Small::BN, Small::PER_CU, fast ? 12 : 23, fast ? 7 : 10);
+  const int64_t big = fast ? cost(FastBig::BT, FastBig::BN, 1, 15, 15)
+                           : cost(ExactBig::BT, ExactBig::BN, 1, 18, 18);
+  if (small < big) return f_tiled<Small>(fast, outb, 0);
+  return fast ? f_tiled<FastBig>(true, outb, 1) : f_tiled<ExactBig>(false, outb, 2);
 }
 
 }  // namespace kg
@@ -489,35 +651,29 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
   p.N = N;
   p.K = K;
   p.vec = ((uintptr_t)D & 15) == 0 && ldd * el % 16 == 0;
-  const int64_t avg = (M_total + G - 1) / G;
-  const bool stream_w = avg <= 64;
-  FLaunch l;
+  FLaunch l = f_choose(M_total, G, N, cus, fast, outb);
+  p.tiles_n = (N + l.bn - 1) / l.bn;
   int64_t grid;
-  if (stream_w) {
-    l = avg <= 16 ? f_stream<1>(fast, outb) : avg <= 32 ? f_stream<2>(fast, outb)
-                                                        : f_stream<4>(fast, outb);
-    p.tiles_n = (N + l.bn - 1) / l.bn;
+  if (l.id < 0) {
     grid = (int64_t)G * p.tiles_n;
     if (grid > INT32_MAX) return KG_ERR_UNSUPPORTED;
   } else {
-    if (fast)
-      l = f_tiled<FCfg<256, 256, 4>>(fast, outb, 0);
-    else
-      l = f_tiled<FCfg<256, 128, 4>>(fast, outb, 1);
     l.lds += sched_bytes(G);
     static std::mutex mu;
-    static int set[64][2][2];  // the largest LDS size asked for so far
-    std::lock_guard<std::mutex> lk(mu);
-    if (set[dev][l.id][outb] < l.lds) {
-      if (hipFuncSetAttribute(l.fn, hipFuncAttributeMaxDynamicSharedMemorySize, l.lds) !=
-          hipSuccess)
-        return KG_ERR_HIP;
-      set[dev][l.id][outb] = l.lds;
+    static int set[64][3][2][2];  // the largest LDS size asked for so far
+    {
+      std::lock_guard<std::mutex> lk(mu);
+      if (set[dev][l.id][fast][outb] < l.lds) {
+        if (hipFuncSetAttribute(l.fn, hipFuncAttributeMaxDynamicSharedMemorySize, l.lds) !=
+            hipSuccess)
+          return KG_ERR_HIP;
+        set[dev][l.id][fast][outb] = l.lds;
+      }
     }
-    p.tiles_n = (N + l.bn - 1) / l.bn;
     const int64_t max_items = (M_total / l.bt + G) * (int64_t)p.tiles_n;
     if (max_items > INT32_MAX) return KG_ERR_UNSUPPORTED;
-    grid = max_items < cus ? max_items : cus;
+    const int64_t at_once = (int64_t)cus * l.per_cu;
+    grid = max_items < at_once ? max_items : at_once;
   }
   void* args[] = {&p};
   return hipLaunchKernel(l.fn, dim3((unsigned)grid), dim3(512), args, (size_t)l.lds,
