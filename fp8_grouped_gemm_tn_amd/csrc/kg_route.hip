@@ -31,10 +31,11 @@ constexpr int kRouteKeys = kRouteMaxGroups + 1;  // + the dropped slots
 // ------------------------------------------------------------------------------ sort plan
 
 // Waves of a sorting workgroup; each ranks a contiguous run of slots in order.
-constexpr int kSortWaves = 4, kSortThreads = 64 * kSortWaves;
-// Slots per workgroup of the two-pass plan.
-constexpr int kSortBlock = 2048;
-// Up to this many slots one workgroup of kSoloWaves waves does everything in one launch.
+constexpr int kSortWaves = 8, kSortThreads = 64 * kSortWaves;
+// The two-pass plan cuts the slots into at most kSortBlocks blocks of at least kSortBlock.
+constexpr int kSortBlocks = 256, kSortBlock = 2048;
+// Up to this many slots one workgroup of kSoloWaves waves does everything in one launch (256
+// experts: 4096 slots 7.6 us, 8192 slots 11.5 us against 9.4 in two passes).
 constexpr int kSoloWaves = 16;
 constexpr int kSoloSlots = 4096;
 
@@ -148,14 +149,14 @@ __global__ __launch_bounds__(64 * kSoloWaves) void kg_route_solo_kernel(
 
 // Pass 1: counts of every block of slots, counts[block][key].
 __global__ __launch_bounds__(kSortThreads) void kg_route_count_kernel(const int32_t* idx,
-                                                                     int64_t n, int G,
+                                                                     int64_t n, int per, int G,
                                                                      int32_t* counts) {
   extern __shared__ int sm[];
   const int keys = G + 1;
   for (int i = threadIdx.x; i < keys; i += kSortThreads) sm[i] = 0;
   __syncthreads();
-  const int64_t s0 = (int64_t)blockIdx.x * kSortBlock;
-  const int64_t s1 = s0 + kSortBlock < n ? s0 + kSortBlock : n;
+  const int64_t s0 = (int64_t)blockIdx.x * per;
+  const int64_t s1 = s0 + per < n ? s0 + per : n;
   for (int64_t s = s0 + threadIdx.x; s < s1; s += kSortThreads)
     atomicAdd(sm + slot_key(idx, s, G), 1);
   __syncthreads();
@@ -163,46 +164,50 @@ __global__ __launch_bounds__(kSortThreads) void kg_route_count_kernel(const int3
     counts[(int64_t)blockIdx.x * keys + i] = sm[i];
 }
 
-// Pass 2: for every key the exclusive scan of its counts over the blocks, in place, and its
-// total. One thread per key walks the blocks, a wave reads 64 neighbouring keys.
-__global__ __launch_bounds__(64) void kg_route_scan_kernel(int32_t* counts, int blocks, int G,
-                                                          int32_t* totals) {
-  const int keys = G + 1, e = blockIdx.x * 64 + threadIdx.x;
-  if (e >= keys) return;
-  int sum = 0;
-  for (int b = 0; b < blocks; ++b) {
-    const int64_t at = (int64_t)b * keys + e;
-    const int c = counts[at];
-    counts[at] = sum;
-    sum += c;
-  }
-  totals[e] = sum;
-}
-
-// Pass 3: every block ranks its slots behind its experts' earlier blocks.
+// Pass 2: every block adds up the counts (all of them for the experts' first rows, the earlier
+// blocks' for its own place in each) and ranks its slots. Reading counts in every block is at
+// most 256 x 256 x (G + 1) words from the L2, and saves a launch and its wait (131072 slots of
+// 256 experts 30 -> 11 us, 2 M slots 265 -> 34 us).
 __global__ __launch_bounds__(kSortThreads) void kg_route_rank_kernel(
-    const int32_t* idx, int64_t n, int G, int bits, const int32_t* counts, const int32_t* totals,
-    int32_t* ks, int32_t* pos, int32_t* src) {
+    const int32_t* __restrict__ idx, int64_t n, int per, int G, int bits,
+    const int32_t* __restrict__ counts, int blocks, int32_t* __restrict__ ks,
+    int32_t* __restrict__ pos, int32_t* __restrict__ src) {
   extern __shared__ int sm[];
   __shared__ int part[kSortWaves];
-  const int keys = G + 1, t = threadIdx.x, w = t >> 6;
+  const int keys = G + 1, t = threadIdx.x, w = t >> 6, me = blockIdx.x;
   int* hist = sm;                       // [kSortWaves][keys]
   int* total = sm + kSortWaves * keys;  // [keys]
-  for (int e = t; e < keys; e += kSortThreads) {
-    const int c = totals[e];
-    total[e] = c;
-    if (blockIdx.x == 0 && e < G) ks[e] = c;
-  }
   for (int i = t; i < kSortWaves * keys; i += kSortThreads) hist[i] = 0;
   __syncthreads();
-  const int64_t b0 = (int64_t)blockIdx.x * kSortBlock;
-  const int64_t b1 = b0 + kSortBlock < n ? b0 + kSortBlock : n;
-  constexpr int run = kSortBlock / kSortWaves;
+  const int64_t b0 = (int64_t)me * per;
+  const int64_t b1 = b0 + per < n ? b0 + per : n;
+  const int run = per / kSortWaves;
   const int64_t s0 = b0 + w * run < b1 ? b0 + w * run : b1, s1 = s0 + run < b1 ? s0 + run : b1;
   wave_count(idx, s0, s1, G, hist + w * keys);
+  constexpr int PER = (kRouteKeys + kSortThreads - 1) / kSortThreads;
+  int before[PER];
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int e = t + x * kSortThreads;
+    before[x] = 0;
+    if (e >= keys) continue;
+    int sum = 0;
+#pragma unroll 16
+    for (int b = 0; b < blocks; ++b) {
+      const int c = counts[(int64_t)b * keys + e];
+      sum += c;
+      before[x] += b < me ? c : 0;
+    }
+    total[e] = sum;
+    if (me == 0 && e < G) ks[e] = sum;
+  }
+  __syncthreads();
   scan_keys<kSortThreads>(total, G, part);
-  for (int e = t; e < keys; e += kSortThreads) {
-    int sum = total[e] + counts[(int64_t)blockIdx.x * keys + e];
+#pragma unroll
+  for (int x = 0; x < PER; ++x) {
+    const int e = t + x * kSortThreads;
+    if (e >= keys) continue;
+    int sum = total[e] + before[x];
     for (int i = 0; i < kSortWaves; ++i) {
       const int c = hist[i * keys + e];
       hist[i * keys + e] = sum;
@@ -223,7 +228,8 @@ struct RowShape {
   int64_t T;
   int64_t rows;  // T * k
   int k, H;
-  int lanes;  // threads per token: a power of two up to the workgroup's 256
+  int lanes;   // threads per token: a power of two up to the workgroup's 256
+  int slices;  // workgroups per token (the kernels that take one unit per thread)
 };
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t u) { return __uint_as_float(u << 16); }
@@ -275,6 +281,15 @@ struct Vec {
 
 __device__ __forceinline__ v4i load16(const unsigned char* p) { return *(const v4i_any*)p; }
 __device__ __forceinline__ void store16(unsigned char* p, const v4i& x) { *(v4i_any*)p = x; }
+// ... past the caches, for what is read or written once: the k copies of a row. (16384 tokens
+// of 8 slots, 7168 channels: fp8 rows 307 -> 192 us, bf16 rows 426 -> 383 us; the sums of k
+// rows, reading so, 415 -> 371 us.)
+__device__ __forceinline__ v4i load16_once(const unsigned char* p) {
+  return __builtin_nontemporal_load((const v4i_any*)p);
+}
+__device__ __forceinline__ void store16_once(unsigned char* p, const v4i& x) {
+  __builtin_nontemporal_store(x, (v4i_any*)p);
+}
 
 // The row that slot value `at` (of pos) names, or -1 for one outside [0, rows): a bad value
 // reads and writes nothing.
@@ -283,45 +298,75 @@ __device__ __forceinline__ int64_t named_row(int at, int64_t rows) {
   return r < rows ? r : -1;
 }
 
-// Xp[pos] = X[token], or zeros for dropped slots. A token's threads read its row once and
-// write it to its k rows.
+// This thread's token and 16-byte unit: a workgroup holds 256 / lanes tokens, or, with all 256
+// threads on one token, one of its `slices` runs of 256 units (and the token is the same for
+// the whole workgroup, so its k positions come through scalar loads).
+__device__ __forceinline__ bool my_unit(const RowShape& s, int64_t* t, int* c) {
+  if (s.lanes == 256) {
+    *t = blockIdx.x / (unsigned)s.slices;
+    *c = (int)(blockIdx.x - *t * s.slices) * 256 + threadIdx.x;
+  } else {
+    *t = (int64_t)blockIdx.x * (256 / s.lanes) + threadIdx.x / s.lanes;
+    *c = threadIdx.x & (s.lanes - 1);
+  }
+  return *t < s.T;
+}
+
+// Slots j0 .. j0 + 7 of token t (none past its k).
+struct Slots {
+  int at[8];
+  __device__ __forceinline__ Slots(const int32_t* pos, const RowShape& s, int64_t t, int j0) {
+    const int32_t* p = pos + t * s.k + j0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) at[i] = j0 + i < s.k ? p[i] : INT32_MAX;
+  }
+};
+
+// Xp[pos] = X[token], or zeros for dropped slots. A thread reads 16 bytes of its token's row
+// once and writes them to the k rows.
 template <int ELEM>
-__global__ __launch_bounds__(256) void kg_dispatch_kernel(const unsigned char* X, int64_t ldx,
-                                                          const int32_t* pos, RowShape s,
-                                                          unsigned char* Xp) {
-  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
-  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
-  if (t >= s.T) return;
+__global__ __launch_bounds__(256) void kg_dispatch_kernel(const unsigned char* __restrict__ X,
+                                                          int64_t ldx,
+                                                          const int32_t* __restrict__ pos,
+                                                          RowShape s,
+                                                          unsigned char* __restrict__ Xp) {
+  int64_t t;
+  int c;
+  if (!my_unit(s, &t, &c)) return;
   const int64_t bytes = (int64_t)s.H * ELEM;
   const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / ELEM;
   const unsigned char* x = X + t * ldx * ELEM;
-  const int32_t* p = pos + t * s.k;
-  for (int c = lane; c < chunks; c += s.lanes) {
+  if (c < chunks) {
     const v4i v = load16(x + 16 * (int64_t)c);
-    for (int j = 0; j < s.k; ++j) {
-      const int at = p[j];
-      const int64_t r = named_row(at, s.rows);
-      if (r >= 0) store16(Xp + r * bytes + 16 * (int64_t)c, at < 0 ? v4i{0, 0, 0, 0} : v);
+    for (int j0 = 0; j0 < s.k; j0 += 8) {
+      const Slots p(pos, s, t, j0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t r = named_row(p.at[i], s.rows);
+        if (r >= 0) store16_once(Xp + r * bytes + 16 * (int64_t)c, p.at[i] < 0 ? v4i{0, 0, 0, 0} : v);
+      }
     }
   }
-  if (lane < tail) {
-    const int64_t o = 16 * (int64_t)chunks + lane * ELEM;
+  if (c == chunks) {  // the row's last elements
     for (int j = 0; j < s.k; ++j) {
-      const int at = p[j];
+      const int at = pos[t * s.k + j];
       const int64_t r = named_row(at, s.rows);
       if (r < 0) continue;
-      if constexpr (ELEM == 2)
-        *(unsigned short*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const unsigned short*)(x + o);
-      else
-        *(uint32_t*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const uint32_t*)(x + o);
+      for (int e = 0; e < tail; ++e) {
+        const int64_t o = 16 * (int64_t)chunks + e * ELEM;
+        if constexpr (ELEM == 2)
+          *(unsigned short*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const unsigned short*)(x + o);
+        else
+          *(uint32_t*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const uint32_t*)(x + o);
+      }
     }
   }
 }
 
-// Largest of 16 neighbouring lanes' values.
-__device__ __forceinline__ float max16(float v) {
+// Largest of 8 neighbouring lanes' values.
+__device__ __forceinline__ float max8(float v) {
 #pragma unroll
-  for (int d = 1; d < 16; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  for (int d = 1; d < 8; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
   return v;
 }
 
@@ -336,33 +381,45 @@ __device__ __forceinline__ int codes4(float a, float b, float c, float d, float 
   return (int)(q ^ (((q & 0x7F7F7F7Fu) + 0x01010101u) & q & 0x80808080u));
 }
 
-// e4m3 rows: 16 lanes hold one 128-channel block, 8 channels each; its scale is
-// amax / 448 (1 for a block of zeros). The codes and the scale go to the token's k rows.
-__global__ __launch_bounds__(256) void kg_dispatch_fp8_kernel(const unsigned char* X, int64_t ldx,
-                                                              const int32_t* pos, RowShape s,
-                                                              unsigned char* Q, float* sa) {
-  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
-  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
-  if (t >= s.T) return;  // whole groups of 16 lanes or more: the shuffles below stay inside
-  const int chunks = s.H >> 3;  // 8 channels each; H is a multiple of 16
-  const int padded = (chunks + 15) & ~15;
+// e4m3 rows: 8 lanes hold one 128-channel block, 16 channels each; its scale is amax / 448 (1
+// for a block of zeros). The codes (16 bytes per thread) and the scale go to the token's k
+// rows. Here a unit is 16 channels.
+__global__ __launch_bounds__(256) void kg_dispatch_fp8_kernel(const unsigned char* __restrict__ X,
+                                                              int64_t ldx,
+                                                              const int32_t* __restrict__ pos,
+                                                              RowShape s,
+                                                              unsigned char* __restrict__ Q,
+                                                              float* __restrict__ sa) {
+  int64_t t;
+  int c;
+  if (!my_unit(s, &t, &c)) return;  // whole groups of 16 lanes or more: shuffles stay inside
+  const bool in = c < s.H >> 4;     // H is a multiple of 16
   const unsigned char* x = X + t * ldx * 2;
-  const int32_t* p = pos + t * s.k;
-  for (int c = lane; c < padded; c += s.lanes) {
-    float f[8] = {};
-    if (c < chunks) Vec<true>::unpack(load16(x + 16 * (int64_t)c), f);
-    float amax = 0.f;  // fmaxf passes over NaNs
+  float f[16] = {};
+  if (in) {
+    float a[8], b[8];
+    Vec<true>::unpack(load16(x + 32 * (int64_t)c), a);
+    Vec<true>::unpack(load16(x + 32 * (int64_t)c + 16), b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    amax = max16(amax);
-    const float sc = amax == 0.f ? 1.0f : amax / 448.0f;
-    const v2i q = {codes4(f[0], f[1], f[2], f[3], sc), codes4(f[4], f[5], f[6], f[7], sc)};
-    for (int j = 0; j < s.k; ++j) {
-      const int at = p[j];
-      const int64_t r = named_row(at, s.rows);
+    for (int i = 0; i < 8; ++i) f[i] = a[i], f[8 + i] = b[i];
+  }
+  float amax = 0.f;  // fmaxf passes over NaNs
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  amax = max8(amax);
+  if (!in) return;
+  const float sc = amax == 0.f ? 1.0f : amax / 448.0f;
+  v4i q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = codes4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], sc);
+  for (int j0 = 0; j0 < s.k; j0 += 8) {
+    const Slots p(pos, s, t, j0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = named_row(p.at[i], s.rows);
       if (r < 0) continue;
-      if (c < chunks) *(v2i_any*)(Q + r * s.H + 8 * (int64_t)c) = at < 0 ? v2i{0, 0} : q;
-      if ((c & 15) == 0) sa[(int64_t)(c >> 4) * s.rows + r] = at < 0 ? 1.0f : sc;
+      store16_once(Q + r * s.H + 16 * (int64_t)c, p.at[i] < 0 ? v4i{0, 0, 0, 0} : q);
+      if ((c & 7) == 0) sa[(int64_t)(c >> 3) * s.rows + r] = p.at[i] < 0 ? 1.0f : sc;
     }
   }
 }
@@ -370,40 +427,36 @@ __global__ __launch_bounds__(256) void kg_dispatch_fp8_kernel(const unsigned cha
 // out[t] = sum_j w[t][j] Y[pos[t][j]] in fp32, j in order, rounded once. Dropped slots are
 // left out, whatever their weight holds. Up to eight rows are read before the first is used.
 template <bool BF16>
-__global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* Y,
-                                                         const int32_t* pos, const float* w,
-                                                         RowShape s, unsigned char* out,
+__global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* __restrict__ Y,
+                                                         const int32_t* __restrict__ pos,
+                                                         const float* __restrict__ w, RowShape s,
+                                                         unsigned char* __restrict__ out,
                                                          int64_t ldo) {
   using V = Vec<BF16>;
-  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
-  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
-  if (t >= s.T) return;
+  int64_t t;
+  int c;
+  if (!my_unit(s, &t, &c)) return;
   const int64_t bytes = (int64_t)s.H * V::ELEM;
   const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / V::ELEM;
-  const int32_t* p = pos + t * s.k;
   const float* wt = w == nullptr ? nullptr : w + t * s.k;
   unsigned char* o = out + t * ldo * V::ELEM;
-  for (int c = lane; c < chunks; c += s.lanes) {
+  if (c < chunks) {
     float acc[V::N] = {};
     for (int j0 = 0; j0 < s.k; j0 += 8) {
+      const Slots p(pos, s, t, j0);
       v4i y[8];
       float wj[8];
-      bool on[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        on[i] = false;
-        if (j0 + i < s.k) {
-          const int at = p[j0 + i];
-          if (at >= 0 && at < s.rows) {
-            on[i] = true;
-            y[i] = load16(Y + at * bytes + 16 * (int64_t)c);
-            wj[i] = wt == nullptr ? 1.0f : wt[j0 + i];
-          }
+        wj[i] = 1.0f;
+        if (p.at[i] >= 0 && p.at[i] < s.rows) {
+          y[i] = load16_once(Y + p.at[i] * bytes + 16 * (int64_t)c);
+          if (wt != nullptr) wj[i] = wt[j0 + i];
         }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (!on[i]) continue;
+        if (!(p.at[i] >= 0 && p.at[i] < s.rows)) continue;
         float f[V::N];
         V::unpack(y[i], f);
 #pragma unroll
@@ -412,15 +465,17 @@ __global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* Y,
     }
     store16(o + 16 * (int64_t)c, V::pack(acc));
   }
-  if (lane < tail) {
-    const int64_t b = 16 * (int64_t)chunks + lane * V::ELEM;
-    float acc = 0.f;
-    for (int j = 0; j < s.k; ++j) {
-      const int at = p[j];
-      if (at >= 0 && at < s.rows)
-        acc = fmaf(wt == nullptr ? 1.0f : wt[j], V::load1(Y + at * bytes + b), acc);
+  if (c == chunks) {  // the row's last elements
+    for (int e = 0; e < tail; ++e) {
+      const int64_t b = 16 * (int64_t)chunks + e * V::ELEM;
+      float acc = 0.f;
+      for (int j = 0; j < s.k; ++j) {
+        const int at = pos[t * s.k + j];
+        if (at >= 0 && at < s.rows)
+          acc = fmaf(wt == nullptr ? 1.0f : wt[j], V::load1(Y + at * bytes + b), acc);
+      }
+      V::store1(o + b, acc);
     }
-    V::store1(o + b, acc);
   }
 }
 
@@ -428,11 +483,10 @@ __global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* Y,
 // slots). Eight slots at a time: a thread keeps their partial dot products over its
 // channels, then the token's threads add theirs in a fixed order.
 template <bool BF16>
-__global__ __launch_bounds__(256) void kg_combine_bwd_kernel(const unsigned char* dOut,
-                                                             int64_t ldo, const unsigned char* Y,
-                                                             const int32_t* pos, const float* w,
-                                                             RowShape s, unsigned char* dY,
-                                                             float* dw) {
+__global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
+    const unsigned char* __restrict__ dOut, int64_t ldo, const unsigned char* __restrict__ Y,
+    const int32_t* __restrict__ pos, const float* __restrict__ w, RowShape s,
+    unsigned char* __restrict__ dY, float* __restrict__ dw) {
   using V = Vec<BF16>;
   __shared__ float part[4][8];
   const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
@@ -463,7 +517,7 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(const unsigned char
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (dw != nullptr && j0 + i < s.k && at[i] >= 0 && at[i] < s.rows)
-            y[i] = load16(Y + at[i] * bytes + 16 * (int64_t)c);
+            y[i] = load16_once(Y + at[i] * bytes + 16 * (int64_t)c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (j0 + i >= s.k) continue;
@@ -476,7 +530,7 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(const unsigned char
           }
 #pragma unroll
           for (int e = 0; e < V::N; ++e) f[e] = wj[i] * g[e];
-          store16(dY + r * bytes + 16 * (int64_t)c, V::pack(f));
+          store16_once(dY + r * bytes + 16 * (int64_t)c, V::pack(f));
           if (dw != nullptr) {
             V::unpack(y[i], f);
 #pragma unroll
@@ -528,11 +582,19 @@ static int key_bits(int G) {
   return b;
 }
 
-static int64_t route_blocks(int64_t n) { return (n + kSortBlock - 1) / kSortBlock; }
+// Slots per block of the two-pass plan: whole runs of 64 for each wave.
+static int64_t route_block(int64_t n) {
+  int64_t per = (n + kSortBlocks - 1) / kSortBlocks;
+  per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
+  return per > kSortBlock ? per : kSortBlock;
+}
+static int64_t route_blocks(int64_t n) { return (n + route_block(n) - 1) / route_block(n); }
 
 // Checks that the row kernels share, and their launch shape: threads per token are the
-// power of two (16 to 256) that covers the row's 16-byte units.
-static int row_shape(int64_t T, int k, int H, int elem, int64_t* grid, RowShape* s) {
+// power of two (16 to 256) that covers the row's units (of `unit` bytes, the last one
+// partial); past 256 units a token takes several workgroups if `split`, else a loop.
+static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, int64_t* grid,
+                     RowShape* s) {
   if (T < 0 || k < 0 || H < 0) return KG_ERR_SHAPE;
   if (H > (1 << 24) || k > 4096 || (k > 0 && T > (int64_t)(INT32_MAX - 1) / k) || T > INT32_MAX - 1)
     return KG_ERR_UNSUPPORTED;
@@ -540,12 +602,13 @@ static int row_shape(int64_t T, int k, int H, int elem, int64_t* grid, RowShape*
   s->rows = T * k;
   s->k = k;
   s->H = H;
-  const int64_t units = ((int64_t)H * elem + 15) / 16;
+  const int64_t units = ((int64_t)H * elem + unit - 1) / unit;
   s->lanes = 16;
   while (s->lanes < 256 && s->lanes < units) s->lanes *= 2;
+  s->slices = split && units > 256 ? (int)((units + 255) / 256) : 1;
   const int per = 256 / s->lanes;
-  *grid = (T + per - 1) / per;
-  return KG_OK;
+  *grid = (T + per - 1) / per * s->slices;
+  return *grid <= INT32_MAX ? KG_OK : KG_ERR_UNSUPPORTED;
 }
 
 }  // namespace kg
@@ -557,7 +620,7 @@ extern "C" int64_t kg_route_workspace_bytes(int64_t T, int k, int G) {
       (k > 0 && T > (int64_t)(INT32_MAX - 1) / k))
     return -1;
   const int64_t n = T * k;
-  return n <= kSoloSlots ? 0 : (route_blocks(n) + 1) * (G + 1) * 4;
+  return n <= kSoloSlots ? 0 : route_blocks(n) * (G + 1) * 4;
 }
 
 extern "C" int kg_route(const int32_t* idx, int64_t T, int k, int G, int32_t* ks, int32_t* pos,
@@ -590,17 +653,13 @@ extern "C" int kg_route(const int32_t* idx, int64_t T, int k, int G, int32_t* ks
                   pos, src);
   }
   const int64_t blocks = route_blocks(n);
+  const int per = (int)route_block(n);
   int32_t* counts = (int32_t*)workspace;
-  int32_t* totals = counts + blocks * keys;
-  int rc = launch(kg_route_count_kernel, blocks, kSortThreads, (size_t)keys * 4, stream, idx, n, G,
-                  counts);
-  if (rc == KG_OK)
-    rc = launch(kg_route_scan_kernel, (keys + 63) / 64, 64, 0, stream, counts, (int)blocks, G,
-                totals);
-  if (rc == KG_OK)
-    rc = launch(kg_route_rank_kernel, blocks, kSortThreads, (size_t)(kSortWaves + 1) * keys * 4,
-                stream, idx, n, G, bits, counts, totals, ks, pos, src);
-  return rc;
+  const int rc = launch(kg_route_count_kernel, blocks, kSortThreads, (size_t)keys * 4, stream, idx,
+                        n, per, G, counts);
+  if (rc != KG_OK) return rc;
+  return launch(kg_route_rank_kernel, blocks, kSortThreads, (size_t)(kSortWaves + 1) * keys * 4,
+                stream, idx, n, per, G, bits, counts, (int)blocks, ks, pos, src);
 }
 
 extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k, int H,
@@ -609,7 +668,7 @@ extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
   int64_t grid;
-  const int rc = row_shape(T, k, H, elem, &grid, &s);
+  const int rc = row_shape(T, k, H, elem, 16, true, &grid, &s);
   if (rc != KG_OK) return rc;
   if (ldx < H) return KG_ERR_SHAPE;
   if (s.rows == 0 || H == 0) return KG_OK;
@@ -627,7 +686,7 @@ extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, i
                                int H, void* Q, float* sa, void* stream) {
   RowShape s;
   int64_t grid;
-  const int rc = row_shape(T, k, H, 2, &grid, &s);
+  const int rc = row_shape(T, k, H, 2, 32, true, &grid, &s);
   if (rc != KG_OK) return rc;
   if (ldx < H) return KG_ERR_SHAPE;
   if (H % 16 != 0) return KG_ERR_ALIGN;
@@ -649,7 +708,7 @@ extern "C" int kg_combine(const void* Y, const int32_t* pos, const float* w, voi
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
   int64_t grid;
-  const int rc = row_shape(T, k, H, elem, &grid, &s);
+  const int rc = row_shape(T, k, H, elem, 16, true, &grid, &s);
   if (rc != KG_OK) return rc;
   if (ldo < H) return KG_ERR_SHAPE;
   if (T == 0 || H == 0) return KG_OK;
@@ -673,7 +732,7 @@ extern "C" int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, cons
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
   int64_t grid;
-  const int rc = row_shape(T, k, H, elem, &grid, &s);
+  const int rc = row_shape(T, k, H, elem, 16, false, &grid, &s);
   if (rc != KG_OK) return rc;
   if (ldo < H) return KG_ERR_SHAPE;
   if (s.rows == 0) return KG_OK;

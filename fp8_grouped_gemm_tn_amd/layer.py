@@ -11,58 +11,78 @@ import ctypes
 from ._binding import (KG_ADAMW_8BIT, KG_ADAMW_G_BF16, KG_ADAMW_P_BF16, KG_ERR_SHAPE,
                        KG_FLAG_D_BF16, KG_OK, KG_ROWS_BF16, KG_ROWS_F32, KgError, _need, lib)
 
-
-def _on(stream):
-    import torch
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+torch = None  # imported with the first call, as the library itself is loaded
+_f32 = _bf16 = _int32 = None
 
 
-def _check(rc, what):
-    if rc != KG_OK:
-        raise KgError(rc, what)
+def _load():
+    """The loaded library, and torch with what the calls read of it."""
+    global torch, _f32, _bf16, _int32
+    if torch is None:
+        import torch as t
+        _f32, _bf16, _int32 = t.float32, t.bfloat16, t.int32
+        torch = t
+    return lib()
+
+
+def _on(ref, stream):
+    """hipStream_t: `stream`'s, or the current one. The call goes to the current GPU, so that
+    has to be `ref`'s."""
+    d = ref.device.index
+    if d != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on GPU {d}, which is not the current one")
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+
+
+def _fail(rc, what):
+    raise KgError(rc, what)
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _gpu(ref, **named):
+def _gpu(ref, *others):
     """Every given tensor is on `ref`'s GPU."""
-    _need(ref.is_cuda, "the tensors must be on a GPU")
-    for name, t in named.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+    if not ref.is_cuda:
+        raise ValueError("the tensors must be on a GPU")
+    d = ref.device
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"a tensor is on {t.device}, another on {d}")
 
 
 def _i32(t, shape, name):
-    import torch
-    _need(t.dtype == torch.int32 and t.shape == shape and t.is_contiguous(),
-          f"{name} must be a contiguous int32 {list(shape)} tensor")
+    if t.dtype is not _int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
 def _row_type(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _bf16:
         return KG_ROWS_BF16
-    _need(t.dtype == torch.float32, f"{name} must be bfloat16 or float32")
+    if t.dtype is not _f32:
+        raise ValueError(f"{name} must be bfloat16 or float32")
     return KG_ROWS_F32
 
 
 def _row_stride(t, name):
     """Row stride in elements of a 2-D tensor whose rows are contiguous (its width where it
     has at most one row, or no columns: torch gives those any stride)."""
-    _need(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1),
-          f"{name} must be 2-D with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld if rows > 1 and cols > 0 else cols
 
 
 def new_route_workspace(T, k, G, device):
     """The workspace of kg_route for T tokens of k slots and G experts (None where it needs
     none); keep it for later calls of at most these sizes."""
-    import torch
-    n = lib().kg_route_workspace_bytes(T, k, G)
+    n = _load().kg_route_workspace_bytes(T, k, G)
     if n < 0:
-        raise KgError(KG_ERR_SHAPE, "kg_route_workspace_bytes")
+        _fail(KG_ERR_SHAPE, "kg_route_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
@@ -70,46 +90,62 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
     """Plan that puts tokens into expert order: idx int32 [T, k] (an entry outside [0, G) is
     dropped), ks int32 [G] (out). pos int32 [T, k] and src int32 [T * k] are written (made if
     not given); ws: new_route_workspace (made if not given and needed). Returns (pos, src)."""
-    import torch
-    _need(idx.dim() == 2, "idx must be [T, k]")
-    T, k = idx.shape
-    _i32(idx, idx.shape, "idx")
-    _need(ks.dim() == 1, "ks must be [G]")
-    _i32(ks, ks.shape, "ks")
+    L = _load()
+    if idx.dim() != 2 or ks.dim() != 1:
+        raise ValueError("idx must be [T, k] and ks [G]")
+    T, k = shape = idx.shape
     G = ks.shape[0]
+    _i32(idx, shape, "idx")
+    _i32(ks, ks.shape, "ks")
     if pos is None:
         pos = torch.empty_like(idx)
     if src is None:
-        src = torch.empty(T * k, dtype=torch.int32, device=idx.device)
-    _i32(pos, idx.shape, "pos")
+        src = torch.empty(T * k, dtype=_int32, device=idx.device)
+    _i32(pos, shape, "pos")
     _i32(src, (T * k,), "src")
-    L = lib()
     if ws is None and L.kg_route_workspace_bytes(T, k, G) > 0:
         ws = new_route_workspace(T, k, G, idx.device)
+    at, size = None, 0
     if ws is not None:
-        _need(ws.dtype == torch.uint8 and ws.is_contiguous(), "ws must be contiguous uint8")
-    _gpu(idx, ks=ks, pos=pos, src=src, ws=ws)
-    _check(L.kg_route(idx.data_ptr(), T, k, G, ks.data_ptr(), pos.data_ptr(), src.data_ptr(),
-                      _at(ws), 0 if ws is None else ws.numel(), _on(stream)), "kg_route")
+        if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous uint8")
+        at, size = ws.data_ptr(), ws.numel()
+    _gpu(idx, ks, pos, src, ws)
+    rc = L.kg_route(idx.data_ptr(), T, k, G, ks.data_ptr(), pos.data_ptr(), src.data_ptr(), at,
+                    size, _on(idx, stream))
+    if rc:
+        _fail(rc, "kg_route")
     return pos, src
+
+
+def _positions(pos, T):
+    """k of pos [T, k]."""
+    if pos.dim() != 2 or pos.shape[0] != T:
+        raise ValueError("pos must be [T, k]")
+    _i32(pos, pos.shape, "pos")
+    return pos.shape[1]
+
+
+def _expert_rows(t, shape, dtype, name):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor")
 
 
 def kg_dispatch(X, pos, Xp=None, stream=None):
     """X [T, H] (bfloat16 or float32, rows contiguous) copied to Xp [T * k, H] (made if not
     given): every token's row to the rows that pos (kg_route) names, zeros for dropped slots."""
-    import torch
+    L = _load()
     ty, ldx = _row_type(X, "X"), _row_stride(X, "X")
     T, H = X.shape
-    _need(pos.dim() == 2 and pos.shape[0] == T, "pos must be [T, k]")
-    k = pos.shape[1]
-    _i32(pos, pos.shape, "pos")
+    k = _positions(pos, T)
     if Xp is None:
         Xp = torch.empty((T * k, H), dtype=X.dtype, device=X.device)
-    _need(Xp.dtype == X.dtype and Xp.shape == (T * k, H) and Xp.is_contiguous(),
-          "Xp must be a contiguous [T * k, H] tensor of X's dtype")
-    _gpu(X, pos=pos, Xp=Xp)
-    _check(lib().kg_dispatch(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, ty, Xp.data_ptr(),
-                             _on(stream)), "kg_dispatch")
+    _expert_rows(Xp, (T * k, H), X.dtype, "Xp")
+    _gpu(X, pos, Xp)
+    rc = L.kg_dispatch(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, ty, Xp.data_ptr(),
+                       _on(X, stream))
+    if rc:
+        _fail(rc, "kg_dispatch")
     return Xp
 
 
@@ -117,59 +153,51 @@ def kg_dispatch_fp8(X, pos, Q=None, sa=None, stream=None):
     """kg_dispatch as e4m3 codes: X bfloat16 [T, H], H a multiple of 16; Q 1-byte [T * k, H] and
     sa float32 [ceil(H / 128), T * k] as kg_fprop and kg_dgrad read them (made if not given).
     Returns (Q, sa)."""
-    import torch
-    _need(X.dtype == torch.bfloat16, "X must be bfloat16")
+    L = _load()
+    if X.dtype is not _bf16:
+        raise ValueError("X must be bfloat16")
     ldx = _row_stride(X, "X")
     T, H = X.shape
-    _need(pos.dim() == 2 and pos.shape[0] == T, "pos must be [T, k]")
-    k = pos.shape[1]
-    _i32(pos, pos.shape, "pos")
+    k = _positions(pos, T)
     if Q is None:
         Q = torch.empty((T * k, H), dtype=torch.uint8, device=X.device)
     if sa is None:
         sa = torch.empty((-(-H // 128), T * k), device=X.device)
-    _need(Q.element_size() == 1 and Q.shape == (T * k, H) and Q.is_contiguous(),
-          "Q must be a contiguous 1-byte [T * k, H] tensor")
-    _need(sa.dtype == torch.float32 and sa.shape == (-(-H // 128), T * k) and sa.is_contiguous(),
-          "sa must be a contiguous float32 [ceil(H / 128), T * k] tensor")
-    _gpu(X, pos=pos, Q=Q, sa=sa)
-    _check(lib().kg_dispatch_fp8(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, Q.data_ptr(),
-                                 sa.data_ptr(), _on(stream)), "kg_dispatch_fp8")
+    if Q.element_size() != 1 or Q.shape != (T * k, H) or not Q.is_contiguous():
+        raise ValueError("Q must be a contiguous 1-byte [T * k, H] tensor")
+    _expert_rows(sa, (-(-H // 128), T * k), _f32, "sa")
+    _gpu(X, pos, Q, sa)
+    rc = L.kg_dispatch_fp8(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, Q.data_ptr(),
+                           sa.data_ptr(), _on(X, stream))
+    if rc:
+        _fail(rc, "kg_dispatch_fp8")
     return Q, sa
-
-
-def _rows_of(Y, pos, name):
-    T, k = pos.shape
-    _need(Y.dim() == 2 and Y.shape[0] == T * k and Y.is_contiguous(),
-          f"{name} must be a contiguous [T * k, H] tensor")
-    return Y.shape[1]
-
-
-def _weights(w, pos, name):
-    import torch
-    _need(w.dtype == torch.float32 and w.shape == pos.shape and w.is_contiguous(),
-          f"{name} must be a contiguous float32 [T, k] tensor")
 
 
 def kg_combine(Y, pos, w=None, out=None, stream=None):
     """out[t] = sum_j w[t][j] Y[pos[t][j]] over the kept slots: Y [T * k, H] (bfloat16 or
     float32), pos int32 [T, k] from kg_route, w float32 [T, k] (None: ones), out [T, H] (rows
     contiguous; made if not given). With w None this is kg_dispatch's gradient."""
-    import torch
+    L = _load()
     ty = _row_type(Y, "Y")
-    _need(pos.dim() == 2, "pos must be [T, k]")
-    _i32(pos, pos.shape, "pos")
-    T, k = pos.shape
-    H = _rows_of(Y, pos, "Y")
+    T = pos.shape[0]
+    k = _positions(pos, T)
+    if Y.dim() != 2:
+        raise ValueError("Y must be [T * k, H]")
+    H = Y.shape[1]
+    _expert_rows(Y, (T * k, H), Y.dtype, "Y")
     if w is not None:
-        _weights(w, pos, "w")
+        _expert_rows(w, (T, k), _f32, "w")
     if out is None:
         out = torch.empty((T, H), dtype=Y.dtype, device=Y.device)
-    _need(out.dtype == Y.dtype and out.shape == (T, H), "out must be [T, H] of Y's dtype")
+    if out.dtype is not Y.dtype or out.shape != (T, H):
+        raise ValueError("out must be [T, H] of Y's dtype")
     ldo = _row_stride(out, "out")
-    _gpu(Y, pos=pos, w=w, out=out)
-    _check(lib().kg_combine(Y.data_ptr(), pos.data_ptr(), _at(w), out.data_ptr(), ldo, T, k, H, ty,
-                            _on(stream)), "kg_combine")
+    _gpu(Y, pos, w, out)
+    rc = L.kg_combine(Y.data_ptr(), pos.data_ptr(), _at(w), out.data_ptr(), ldo, T, k, H, ty,
+                      _on(Y, stream))
+    if rc:
+        _fail(rc, "kg_combine")
     return out
 
 
@@ -177,30 +205,29 @@ def kg_combine_bwd(dOut, Y, pos, w=None, dY=None, dw=None, need_dw=True, stream=
     """Gradients of kg_combine: dOut [T, H] (rows contiguous), Y [T * k, H], pos, w as given to
     it. Returns (dY [T * k, H], dw float32 [T, k]); with need_dw False dw is not computed (None)
     and Y is not read (it may be None)."""
-    import torch
+    L = _load()
     ty, ldo = _row_type(dOut, "dOut"), _row_stride(dOut, "dOut")
-    _need(pos.dim() == 2 and pos.shape[0] == dOut.shape[0], "pos must be [T, k]")
-    _i32(pos, pos.shape, "pos")
-    T, k = pos.shape
-    H = dOut.shape[1]
+    T, H = dOut.shape
+    k = _positions(pos, T)
     if w is not None:
-        _weights(w, pos, "w")
+        _expert_rows(w, (T, k), _f32, "w")
     if dY is None:
         dY = torch.empty((T * k, H), dtype=dOut.dtype, device=dOut.device)
-    _need(dY.dtype == dOut.dtype and dY.shape == (T * k, H) and dY.is_contiguous(),
-          "dY must be a contiguous [T * k, H] tensor of dOut's dtype")
+    _expert_rows(dY, (T * k, H), dOut.dtype, "dY")
     if need_dw:
-        _need(Y is not None and Y.dtype == dOut.dtype and _rows_of(Y, pos, "Y") == H,
-              "Y must be a contiguous [T * k, H] tensor of dOut's dtype")
+        if Y is None:
+            raise ValueError("dw needs Y")
+        _expert_rows(Y, (T * k, H), dOut.dtype, "Y")
         if dw is None:
             dw = torch.empty((T, k), device=dOut.device)
-        _weights(dw, pos, "dw")
+        _expert_rows(dw, (T, k), _f32, "dw")
     else:
         Y = dw = None
-    _gpu(dOut, Y=Y, pos=pos, w=w, dY=dY, dw=dw)
-    _check(lib().kg_combine_bwd(dOut.data_ptr(), ldo, _at(Y), pos.data_ptr(), _at(w),
-                                dY.data_ptr(), _at(dw), T, k, H, ty, _on(stream)),
-           "kg_combine_bwd")
+    _gpu(dOut, Y, pos, w, dY, dw)
+    rc = L.kg_combine_bwd(dOut.data_ptr(), ldo, _at(Y), pos.data_ptr(), _at(w), dY.data_ptr(),
+                          _at(dw), T, k, H, ty, _on(dOut, stream))
+    if rc:
+        _fail(rc, "kg_combine_bwd")
     return dY, dw
 
 
@@ -208,27 +235,28 @@ def kg_fprop(A, sa, W, sw, D, ms, flags=0, stream=None):
     """D = rows . W^T per expert: A fp8 codes [M_total, K] (rows contiguous), sa float32
     [ceil(K / 128), M_total], W fp8 codes [G, N, K], sw float32 [G, ceil(N / 128),
     ceil(K / 128)], ms int32 [G], D [M_total, N] (float32 or bfloat16, rows contiguous)."""
-    import torch
-    _need(W.dim() == 3 and W.element_size() == 1 and W.is_contiguous(),
-          "W must be contiguous fp8 codes [G, N, K]")
+    L = _load()
+    if W.dim() != 3 or W.element_size() != 1 or not W.is_contiguous():
+        raise ValueError("W must be contiguous fp8 codes [G, N, K]")
     G, N, K = W.shape
-    lda = _row_stride(A, "A")
+    lda, ldd = _row_stride(A, "A"), _row_stride(D, "D")
     M, nk = A.shape[0], -(-K // 128)
-    _need(A.shape[1] == K and A.element_size() == 1, "A must be fp8 codes [M_total, K]")
-    _need(sa.dtype == torch.float32 and sa.shape == (nk, M) and sa.is_contiguous(),
-          "sa must be contiguous float32 [ceil(K / 128), M_total]")
-    _need(sw.dtype == torch.float32 and sw.shape == (G, -(-N // 128), nk) and sw.is_contiguous(),
-          "sw must be contiguous float32 [G, ceil(N / 128), ceil(K / 128)]")
+    if A.shape[1] != K or A.element_size() != 1:
+        raise ValueError("A must be fp8 codes [M_total, K]")
+    _expert_rows(sa, (nk, M), _f32, "sa")
+    _expert_rows(sw, (G, -(-N // 128), nk), _f32, "sw")
     _i32(ms, (G,), "ms")
-    ldd = _row_stride(D, "D")
-    _need(D.shape == (M, N) and D.dtype in (torch.float32, torch.bfloat16),
-          "D must be a float32 or bfloat16 [M_total, N] tensor")
-    _gpu(D, A=A, sa=sa, W=W, sw=sw, ms=ms)
-    if D.dtype == torch.bfloat16:
+    if D.dtype is _bf16:
         flags |= KG_FLAG_D_BF16
-    _check(lib().kg_fprop(A.data_ptr(), lda, sa.data_ptr(), W.data_ptr(), sw.data_ptr(),
-                          D.data_ptr(), ldd, ms.data_ptr(), G, N, K, M, flags, _on(stream)),
-           "kg_fprop")
+    elif D.dtype is not _f32:
+        raise ValueError("D must be float32 or bfloat16")
+    if D.shape != (M, N):
+        raise ValueError("D must be [M_total, N]")
+    _gpu(D, A, sa, W, sw, ms)
+    rc = L.kg_fprop(A.data_ptr(), lda, sa.data_ptr(), W.data_ptr(), sw.data_ptr(), D.data_ptr(),
+                    ldd, ms.data_ptr(), G, N, K, M, flags, _on(D, stream))
+    if rc:
+        _fail(rc, "kg_fprop")
     return D
 
 
@@ -250,7 +278,7 @@ class AdamWTable:
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, m_scales=None, v_scales=None,
                  copies=None):
-        import torch
+        L = _load()
         n = len(params)
         self.count, self.kinds, self.items, self.table = n, 0, 0, None
         none = [None] * n
@@ -286,12 +314,13 @@ class AdamWTable:
             rows[i] = AdamWTensor(*(_at(col[i]) for col in lists), size)
         self.kinds = (KG_ADAMW_P_BF16 if p16 else 0) | (KG_ADAMW_G_BF16 if g16 else 0) | \
             (KG_ADAMW_8BIT if packed else 0)
-        L = lib()
         self.items, size = L.kg_adamw_items(rows, n), L.kg_adamw_table_bytes(rows, n)
         if size < 0:
-            raise KgError(KG_ERR_SHAPE, "kg_adamw_table_bytes")
+            _fail(KG_ERR_SHAPE, "kg_adamw_table_bytes")
         image = torch.empty(size, dtype=torch.uint8)
-        _check(L.kg_adamw_pack(rows, n, self.kinds, image.data_ptr(), size), "kg_adamw_pack")
+        rc = L.kg_adamw_pack(rows, n, self.kinds, image.data_ptr(), size)
+        if rc:
+            _fail(rc, "kg_adamw_pack")
         self.table = image.to(ref.device)
 
 
@@ -300,13 +329,16 @@ def kg_adamw(table, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step
     """One AdamW step over an AdamWTable's tensors, in place. step: 1 for the first. gscale:
     a one-element float32 GPU tensor that multiplies every gradient. dyn: float32 GPU tensor
     {lr, 1 - beta1^step, 1 - beta2^step}, read in the place of lr and step."""
-    import torch
-    if gscale is not None:
-        _need(gscale.dtype == torch.float32 and gscale.numel() == 1, "gscale must be one float32")
-    if dyn is not None:
-        _need(dyn.dtype == torch.float32 and dyn.numel() == 3 and dyn.is_contiguous(),
-              "dyn must be three contiguous float32")
-    if table.count and (gscale is not None or dyn is not None):
-        _gpu(table.table, gscale=gscale, dyn=dyn)
-    _check(lib().kg_adamw(_at(table.table), table.count, table.items, table.kinds, lr, beta1, beta2,
-                          eps, weight_decay, step, _at(gscale), _at(dyn), _on(stream)), "kg_adamw")
+    L = _load()
+    if gscale is not None and (gscale.dtype is not _f32 or gscale.numel() != 1):
+        raise ValueError("gscale must be one float32")
+    if dyn is not None and (dyn.dtype is not _f32 or dyn.shape != (3,) or not dyn.is_contiguous()):
+        raise ValueError("dyn must be three contiguous float32")
+    if table.table is None:  # no tensors
+        return
+    _gpu(table.table, gscale, dyn)
+    rc = L.kg_adamw(table.table.data_ptr(), table.count, table.items, table.kinds, lr, beta1,
+                    beta2, eps, weight_decay, step, _at(gscale), _at(dyn),
+                    _on(table.table, stream))
+    if rc:
+        _fail(rc, "kg_adamw")
