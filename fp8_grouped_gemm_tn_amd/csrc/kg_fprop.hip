@@ -239,24 +239,29 @@ __device__ __forceinline__ void f_meet() {
 // compiler wait for them.
 typedef __attribute__((address_space(4))) const float ConstFloat;
 
-// The loop over the blocks. While block kb is computed, W's block kb + 1 loads into the other
-// W buffer and the tokens' block kb + 2 into the buffer that kb's came from: the token
-// fragments are read one block ahead, each right after its last MFMA of the block before, so
-// their buffer is free during the whole block. The waves meet twice per block: before the
-// next tokens are read (they and nothing later have to be there), and at the block's end
-// (the next W, and every wave's token reads). Each load has most of a block's time to arrive.
+// The loop over the blocks. The token fragments are read one block ahead, each right after its
+// last MFMA of the block before, so the buffer that block kb's tokens came from is free during
+// block kb and their block kb + 2 loads into it. W's block kb has been read before the
+// block's last tile of outputs, and its block kb + 2 loads into that buffer from there. So
+// every load has a whole block's time or more to arrive. The waves meet twice per block: before
+// the next tokens are read, and at the block's end. (With one meeting, all loads awaited:
+// 33 -> 45 us on 256 tokens of one expert, nothing gained on large problems.)
 //
 // A partial sum is scaled and added LAG MFMAs after it was issued, four fmas between two
 // MFMAs, so neither waits for the other; the empty asm keeps the compiler from moving the
 // sums to the end of the block (which spilled), sched_barrier keeps the interleaving.
-// The loads are spread over the block's first half: issued in one burst they block the
-// wave's own instruction stream until the memory pipeline takes them.
+// The loads are spread over the block: issued in one burst they block the wave's own
+// instruction stream until the memory pipeline takes them.
 //
 // On 32768 tokens of 8 experts, K 7168, N 4096 (fp8 MFMA, bf16 out, 256 x 256): 1480 us with
 // a burst of loads, a vector load of the weight scale and no fragments ahead; 1110 with the
-// scale through a scalar load and four waves loading; 870 in this form, 847 without LDS
-// conflicts and with the loads in the first half. 1.64 M cycles, MFMA busy for 0.95 M of
-// them; the clock falls to 1.75 GHz under this load (1.98 without the loads).
+// scale through a scalar load and four waves loading; 870 with fragments ahead and counted
+// waits, 847 without LDS conflicts and with spread loads. 1.64 M cycles, MFMA busy for
+// 0.95 M of them, at 1.75 GHz, to which the clock falls under this load: without the loads
+// 1.50 M cycles at 1.92 GHz, without the meetings as well 1.32 M. Tried without gain: the
+// next tile's first loads before this one's stores (877), loads into the L2 two to four
+// blocks ahead (912), 32 x 32 MFMAs (924), raised wave priority (873), the last round's
+// tiles in quarters (840).
 template <class C, bool FAST, bool OUTB>
 __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -329,10 +334,12 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
       for (int x = 0; x < C::LW; ++x) L.load(0, 0, x);
 #pragma unroll
       for (int x = C::LW; x < C::LOADS; ++x) L.load(0, 1, x);
-      f_meet<C::LT + 1>();
+#pragma unroll
+      for (int x = 0; x < C::LW; ++x) L.load(1, 0, x);
+      f_meet<C::LOADS>();
 #pragma unroll
       for (int tt = 0; tt < C::TT; ++tt) read_t(0, tt);
-      f_meet<C::LT + 1>();
+      f_meet<C::LOADS>();
     }
     for (int kb = 0; kb < nk; ++kb) {
       read_w(kb, 0);
@@ -350,22 +357,27 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 #pragma unroll
       for (int u = 0; u < S; ++u) {
         const int i = u / C::TT, tt = u % C::TT;
-        // the tokens' next block is there (of the loads, W's and theirs after it may not be)
+        // the tokens' next block is there, W's block has been read (of the loads, W's next one
+        // and the tokens' next but one may be under way)
         if (u == S - C::TT) f_meet<C::LOADS>();
         if (tt == 0 && i + 1 < C::NI) read_w(kb, i + 1);
         part[u % (LAG + 1)] = block_sum(wf[i & 1], tf[tt]);
         if (i == C::NI - 1) read_t(kb + 1, tt);  // (past the last block: not used)
         if (u >= LAG) add(u - LAG);
 #pragma unroll
-        for (int x = 0; x < C::LOADS; ++x)
-          if (x * (S / 2) / C::LOADS == u) L.load(kb + 1, kb + 2, x);
+        for (int x = 0; x < C::LT + 1; ++x)
+          if (x * (S - C::TT) / (C::LT + 1) == u) L.load(0, kb + 2, C::LW + x);
+#pragma unroll
+        for (int x = 0; x < C::LW; ++x)
+          if (S - C::TT + x * C::TT / C::LW == u) L.load(kb + 2, 0, x);
         if (u == S / 2) swv = swg[min(kb + 1, nk - 1)];
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int u = S - LAG; u < S; ++u) add(u);
-      // W's next block is there, and the tokens' has been read
-      f_meet<C::LT + 1>();
+      // W's next block is there, and the tokens' has been read (the loads of the two after
+      // them may be under way)
+      f_meet<C::LOADS>();
     }
 #pragma unroll
     for (int tt = 0; tt < C::TT; ++tt) {
@@ -571,7 +583,7 @@ using Small = FCfg<128, 128, 4, 2>;
 // Which kernel and tile. The experts' sizes are known on the device only, so this goes by
 // M_total and G; every choice is right for every distribution of the rows.
 //  * Streaming up to 8 rows per expert on average, and up to 64 while M_total * N <= 2^19
-//    (few rows in all: a tile's time is then the latency of its blocks, 0.7 us each).
+//    (few rows in all: a tile's time is then the latency of its blocks, 0.6 us each).
 //    K = 7168, N = 4096, streaming / Small: 32 experts of 2, 8, 16 rows 127/153, 164/167,
 //    231/170 us; 4 experts of 16, 32, 64 rows 27/41, 37/41, 71/42; 1 of 16, 64, 128 rows
 //    13/39, 23/39, 42/40.
