@@ -281,9 +281,11 @@ struct Vec {
 
 __device__ __forceinline__ v4i load16(const unsigned char* p) { return *(const v4i_any*)p; }
 __device__ __forceinline__ void store16(unsigned char* p, const v4i& x) { *(v4i_any*)p = x; }
-// ... past the caches, for what is read or written once: the k copies of a row. (16384 tokens
-// of 8 slots, 7168 channels: fp8 rows 307 -> 192 us, bf16 rows 426 -> 383 us; the sums of k
-// rows, reading so, 415 -> 371 us.)
+// ... past the caches, for what is read or written once. (16384 tokens of 8 slots, 7168
+// channels, inputs not in the caches: bf16 rows 412 us, 5.1 TB/s, with a run of tokens per
+// XCD, 435 without; fp8 rows 285 us, 229 without the scales, whose 4-byte stores to
+// different lines cost as many L2 requests as the codes; sums of k rows 369 us, 5.7 TB/s,
+// 408 with outputs through the caches; gradients 782 us, 5.1 TB/s.)
 __device__ __forceinline__ v4i load16_once(const unsigned char* p) {
   return __builtin_nontemporal_load((const v4i_any*)p);
 }
@@ -300,11 +302,15 @@ __device__ __forceinline__ int64_t named_row(int at, int64_t rows) {
 
 // This thread's token and 16-byte unit: a workgroup holds 256 / lanes tokens, or, with all 256
 // threads on one token, one of its `slices` runs of 256 units (and the token is the same for
-// the whole workgroup, so its k positions come through scalar loads).
+// the whole workgroup, so its k positions come through scalar loads). Workgroups go to the 8
+// XCDs in turn; BY_XCD gives each XCD a run of tokens instead.
+template <bool BY_XCD = false>
 __device__ __forceinline__ bool my_unit(const RowShape& s, int64_t* t, int* c) {
   if (s.lanes == 256) {
-    *t = blockIdx.x / (unsigned)s.slices;
-    *c = (int)(blockIdx.x - *t * s.slices) * 256 + threadIdx.x;
+    const unsigned per = gridDim.x / 8, b = blockIdx.x;
+    const unsigned id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
+    *t = id / (unsigned)s.slices;
+    *c = (int)(id - *t * s.slices) * 256 + threadIdx.x;
   } else {
     *t = (int64_t)blockIdx.x * (256 / s.lanes) + threadIdx.x / s.lanes;
     *c = threadIdx.x & (s.lanes - 1);
@@ -332,7 +338,7 @@ __global__ __launch_bounds__(256) void kg_dispatch_kernel(const unsigned char* _
                                                           unsigned char* __restrict__ Xp) {
   int64_t t;
   int c;
-  if (!my_unit(s, &t, &c)) return;
+  if (!my_unit<true>(s, &t, &c)) return;
   const int64_t bytes = (int64_t)s.H * ELEM;
   const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / ELEM;
   const unsigned char* x = X + t * ldx * ELEM;
@@ -463,7 +469,7 @@ __global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* __
         for (int e = 0; e < V::N; ++e) acc[e] = fmaf(wj[i], f[e], acc[e]);
       }
     }
-    store16(o + 16 * (int64_t)c, V::pack(acc));
+    store16_once(o + 16 * (int64_t)c, V::pack(acc));
   }
   if (c == chunks) {  // the row's last elements
     for (int e = 0; e < tail; ++e) {
@@ -552,27 +558,34 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
       }
     }
     if (dw == nullptr) continue;
-    const int in_wave = s.lanes < 64 ? s.lanes : 64;
+    // The eight sums over the token's threads. In the first three steps a lane hands half of
+    // its sums over and keeps the other half, so ten shuffles add eight sums over a wave; then
+    // lanes 8 m + (0 .. 7) hold sum 4 * bit 0 + 2 * bit 1 + bit 2 of their number.
+    const int me = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      for (int o = 1; o < in_wave; o <<= 1) dot[i] += __shfl_xor(dot[i], o, 64);
-    if (s.lanes > 64) {  // the token's threads are the workgroup's first s.lanes / 64 waves ...
-      const int wave = threadIdx.x >> 6, first = wave & ~(s.lanes / 64 - 1);
-      __syncthreads();
-      if ((threadIdx.x & 63) == 0)
+    for (int step = 0; step < 3; ++step) {
+      const int half = 4 >> step;
+      const bool up = (me >> step) & 1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[wave][i] = dot[i];
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dot[i] = 0.f;
-        for (int v = 0; v < s.lanes / 64; ++v) dot[i] += part[first + v][i];
+      for (int i = 0; i < half; ++i) {
+        const float keep = up ? dot[half + i] : dot[i], give = up ? dot[i] : dot[half + i];
+        dot[i] = keep + __shfl_xor(give, 1 << step, 64);
       }
     }
-    if (live && lane == 0)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (j0 + i < s.k) dw[t * s.k + j0 + i] = at[i] >= 0 && at[i] < s.rows ? dot[i] : 0.f;
+    for (int o = 8; o < s.lanes && o < 64; o <<= 1) dot[0] += __shfl_xor(dot[0], o, 64);
+    const int mine = 4 * (me & 1) + 2 * ((me >> 1) & 1) + ((me >> 2) & 1);
+    if (s.lanes > 64) {  // a token's threads are s.lanes / 64 whole waves of the workgroup
+      const int wave = threadIdx.x >> 6, first = wave & ~(s.lanes / 64 - 1);
+      __syncthreads();
+      if (me < 8) part[wave][mine] = dot[0];
+      __syncthreads();
+      dot[0] = 0.f;
+      for (int v = 0; v < s.lanes / 64; ++v) dot[0] += part[first + v][mine];
+    }
+    if (live && lane < 8 && j0 + mine < s.k) {
+      const int j = p[j0 + mine];
+      dw[t * s.k + j0 + mine] = j >= 0 && j < s.rows ? dot[0] : 0.f;
+    }
   }
 }
 
