@@ -8,6 +8,8 @@ GPU, so the checks read each property of a tensor once.
 """
 import ctypes
 
+import numpy as np
+
 from ._binding import (KG_ADAMW_8BIT, KG_ADAMW_G_BF16, KG_ADAMW_P_BF16, KG_ERR_SHAPE,
                        KG_FLAG_D_BF16, KG_OK, KG_ROWS_BF16, KG_ROWS_F32, KgError, _need, lib)
 
@@ -32,6 +34,14 @@ def _on(ref, stream):
     if d != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on GPU {d}, which is not the current one")
     return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+
+
+def _made(shape, dtype, ref, stream):
+    """A new tensor on `ref`'s GPU for a call on `stream` (None: the current one)."""
+    t = torch.empty(shape, dtype=dtype, device=ref.device)
+    if stream is not None:
+        t.record_stream(stream)  # the memory is not handed on before the call is done with it
+    return t
 
 
 def _fail(rc, what):
@@ -98,13 +108,15 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
     _i32(idx, shape, "idx")
     _i32(ks, ks.shape, "ks")
     if pos is None:
-        pos = torch.empty_like(idx)
+        pos = _made(shape, _int32, idx, stream)
     if src is None:
-        src = torch.empty(T * k, dtype=_int32, device=idx.device)
+        src = _made((T * k,), _int32, idx, stream)
     _i32(pos, shape, "pos")
     _i32(src, (T * k,), "src")
-    if ws is None and L.kg_route_workspace_bytes(T, k, G) > 0:
-        ws = new_route_workspace(T, k, G, idx.device)
+    if ws is None:
+        n = L.kg_route_workspace_bytes(T, k, G)
+        if n > 0:
+            ws = _made((n,), torch.uint8, idx, stream)
     at, size = None, 0
     if ws is not None:
         if ws.dtype is not torch.uint8 or not ws.is_contiguous():
@@ -139,7 +151,7 @@ def kg_dispatch(X, pos, Xp=None, stream=None):
     T, H = X.shape
     k = _positions(pos, T)
     if Xp is None:
-        Xp = torch.empty((T * k, H), dtype=X.dtype, device=X.device)
+        Xp = _made((T * k, H), X.dtype, X, stream)
     _expert_rows(Xp, (T * k, H), X.dtype, "Xp")
     _gpu(X, pos, Xp)
     rc = L.kg_dispatch(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, ty, Xp.data_ptr(),
@@ -160,9 +172,9 @@ def kg_dispatch_fp8(X, pos, Q=None, sa=None, stream=None):
     T, H = X.shape
     k = _positions(pos, T)
     if Q is None:
-        Q = torch.empty((T * k, H), dtype=torch.uint8, device=X.device)
+        Q = _made((T * k, H), torch.uint8, X, stream)
     if sa is None:
-        sa = torch.empty((-(-H // 128), T * k), device=X.device)
+        sa = _made((-(-H // 128), T * k), _f32, X, stream)
     if Q.element_size() != 1 or Q.shape != (T * k, H) or not Q.is_contiguous():
         raise ValueError("Q must be a contiguous 1-byte [T * k, H] tensor")
     _expert_rows(sa, (-(-H // 128), T * k), _f32, "sa")
@@ -189,7 +201,7 @@ def kg_combine(Y, pos, w=None, out=None, stream=None):
     if w is not None:
         _expert_rows(w, (T, k), _f32, "w")
     if out is None:
-        out = torch.empty((T, H), dtype=Y.dtype, device=Y.device)
+        out = _made((T, H), Y.dtype, Y, stream)
     if out.dtype is not Y.dtype or out.shape != (T, H):
         raise ValueError("out must be [T, H] of Y's dtype")
     ldo = _row_stride(out, "out")
@@ -212,14 +224,14 @@ def kg_combine_bwd(dOut, Y, pos, w=None, dY=None, dw=None, need_dw=True, stream=
     if w is not None:
         _expert_rows(w, (T, k), _f32, "w")
     if dY is None:
-        dY = torch.empty((T * k, H), dtype=dOut.dtype, device=dOut.device)
+        dY = _made((T * k, H), dOut.dtype, dOut, stream)
     _expert_rows(dY, (T * k, H), dOut.dtype, "dY")
     if need_dw:
         if Y is None:
             raise ValueError("dw needs Y")
         _expert_rows(Y, (T * k, H), dOut.dtype, "Y")
         if dw is None:
-            dw = torch.empty((T, k), device=dOut.device)
+            dw = _made((T, k), _f32, dOut, stream)
         _expert_rows(dw, (T, k), _f32, "dw")
     else:
         Y = dw = None
@@ -292,36 +304,41 @@ class AdamWTable:
         if n == 0:
             return
         ref = lists[0][0]
-        _need(ref.is_cuda, "the tensors must be on a GPU")
-        f32, bf16 = torch.float32, torch.bfloat16
-        p16, g16 = ref.dtype == bf16, lists[1][0].dtype == bf16
+        _gpu(ref)
+        device = ref.device
+        p16, g16 = ref.dtype is _bf16, lists[1][0].dtype is _bf16
         names = ("params", "grads", "exp_avgs", "exp_avg_sqs", "m_scales", "v_scales", "copies")
-        kinds = (bf16 if p16 else f32, bf16 if g16 else f32, None if packed else f32,
-                 None if packed else f32, f32, f32, bf16)
-        rows = (AdamWTensor * n)()
-        for i in range(n):
-            size = lists[0][i].numel()
-            for name, kind, x in zip(names, kinds, (col[i] for col in lists)):
-                if x is None:
-                    continue
-                _need(x.device == ref.device and x.is_contiguous(),
-                      f"{name}[{i}] must be contiguous and on {ref.device}")
-                _need(x.dtype == kind if kind is not None else
-                      x.element_size() == 1 and x.dtype != torch.bool,
-                      f"{name}[{i}] must be {kind if kind is not None else 'e4m3 codes'}")
-                _need(x.numel() == (-(-size // 128) if name in ("m_scales", "v_scales") else size),
-                      f"{name}[{i}] has {x.numel()} elements for a parameter of {size}")
-            rows[i] = AdamWTensor(*(_at(col[i]) for col in lists), size)
+        kinds = (_bf16 if p16 else _f32, _bf16 if g16 else _f32, None if packed else _f32,
+                 None if packed else _f32, _f32, _f32, _bf16)
+        sizes = [x.numel() for x in lists[0]]
+        blocks = [-(-s // 128) for s in sizes]
+        rows = np.zeros((n, 8), np.int64)  # kg_adamw_tensor: seven pointers, n
+        rows[:, 7] = sizes
+        for col, (name, kind, xs) in enumerate(zip(names, kinds, lists)):
+            if xs is none:
+                continue
+            if kind is None:  # e4m3 codes
+                ok = all(x.element_size() == 1 and x.dtype is not torch.bool for x in xs)
+            else:
+                ok = all(x.dtype is kind for x in xs)
+            _need(ok, f"{name} must all be {'1-byte e4m3 codes' if kind is None else kind}")
+            _need(all(x.device == device and x.is_contiguous() for x in xs),
+                  f"{name} must be contiguous and on {device}")
+            _need([x.numel() for x in xs] == (blocks if name.endswith("scales") else sizes),
+                  f"{name} must have {'ceil(n / 128)' if name.endswith('scales') else 'n'} "
+                  "elements for a parameter of n")
+            rows[:, col] = [x.data_ptr() for x in xs]
+        at = rows.ctypes.data
         self.kinds = (KG_ADAMW_P_BF16 if p16 else 0) | (KG_ADAMW_G_BF16 if g16 else 0) | \
             (KG_ADAMW_8BIT if packed else 0)
-        self.items, size = L.kg_adamw_items(rows, n), L.kg_adamw_table_bytes(rows, n)
+        self.items, size = L.kg_adamw_items(at, n), L.kg_adamw_table_bytes(at, n)
         if size < 0:
             _fail(KG_ERR_SHAPE, "kg_adamw_table_bytes")
         image = torch.empty(size, dtype=torch.uint8)
-        rc = L.kg_adamw_pack(rows, n, self.kinds, image.data_ptr(), size)
+        rc = L.kg_adamw_pack(at, n, self.kinds, image.data_ptr(), size)
         if rc:
             _fail(rc, "kg_adamw_pack")
-        self.table = image.to(ref.device)
+        self.table = image.to(device)
 
 
 def kg_adamw(table, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, gscale=None,

@@ -315,3 +315,28 @@ def test_other_stream_and_graph():
         for a, b in zip(want, (ks, pos, src, Xp, Q, sa, out)):
             assert torch.equal(a, b)
         assert np.array_equal(pos.cpu().numpy(), plan_of(idx.cpu().numpy(), G)[1])
+
+
+def test_tensors_made_for_a_stream():
+    """With `stream` given, what a call makes (outputs, the plan's workspace) stays untouched by
+    later allocations of the current stream until that stream is done with it."""
+    T, k, G, H = 3000, 8, 64, 256
+    idx = torch.from_numpy(make_idx(T, k, G, "uniform", 4)).to(DEV)
+    X = torch.randn((T, H), device=DEV).to(BF16)
+    ks = torch.empty(G, dtype=torch.int32, device=DEV)
+    want = plan_of(idx.cpu().numpy(), G)
+    side = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                busy @ busy  # the side stream's work is late
+        pos, src = kg.kg_route(idx, ks, stream=side)
+        Xp = kg.kg_dispatch(X, pos, stream=side)
+        out = kg.kg_combine(Xp, pos, stream=side)
+        for _ in range(50):  # would land in memory that was freed too early
+            torch.full((2 ** 18,), 77, dtype=torch.int32, device=DEV)
+        side.synchronize()
+        assert np.array_equal(pos.cpu().numpy(), want[1]) and np.array_equal(src.cpu().numpy(), want[2])
+        assert torch.equal(out, (X.float() * k).to(BF16))
