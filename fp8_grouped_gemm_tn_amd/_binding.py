@@ -55,7 +55,8 @@ SIGNATURES = {
     "kg_route": (_i32, [_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp]),
     "kg_route_workspace_bytes": (_i64, [_i64, _i32, _i32]),
     "kg_dispatch": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
-    "kg_dispatch_fp8": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "kg_dispatch_fp8": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp]),
+    "kg_dispatch_fp8_workspace_bytes": (_i64, [_i64, _i32, _i32]),
     "kg_combine": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp]),
     "kg_combine_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp]),
     "kg_adamw_items": (_i64, [_vp, _i32]),

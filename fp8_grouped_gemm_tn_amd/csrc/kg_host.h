@@ -24,16 +24,23 @@ struct same {
   using type = T;
 };
 
-// Enqueues fn(args...) and returns KG_OK, or KG_ERR_HIP if this launch was refused (an
-// error that some earlier call left behind is not looked at and stays where it is).
+// Enqueues fn(args...) on grid_x by grid_y workgroups and returns KG_OK, or KG_ERR_HIP if this
+// launch was refused (an error that some earlier call left behind is not looked at and stays
+// where it is).
+template <typename... P>
+inline int launch2(void (*fn)(P...), int64_t grid_x, int grid_y, int block, size_t lds,
+                   void* stream, typename same<P>::type... args) {
+  void* ptrs[] = {(void*)&args...};
+  return hipLaunchKernel((const void*)fn, dim3((unsigned)grid_x, (unsigned)grid_y),
+                         dim3((unsigned)block), ptrs, lds, (hipStream_t)stream) == hipSuccess
+             ? KG_OK
+             : KG_ERR_HIP;
+}
+
 template <typename... P>
 inline int launch(void (*fn)(P...), int64_t grid, int block, size_t lds, void* stream,
                   typename same<P>::type... args) {
-  void* ptrs[] = {(void*)&args...};
-  return hipLaunchKernel((const void*)fn, dim3((unsigned)grid), dim3((unsigned)block), ptrs, lds,
-                         (hipStream_t)stream) == hipSuccess
-             ? KG_OK
-             : KG_ERR_HIP;
+  return launch2(fn, grid, 1, block, lds, stream, args...);
 }
 
 }  // namespace kg

@@ -283,8 +283,7 @@ __device__ __forceinline__ v4i load16(const unsigned char* p) { return *(const v
 __device__ __forceinline__ void store16(unsigned char* p, const v4i& x) { *(v4i_any*)p = x; }
 // ... past the caches, for what is read or written once. (16384 tokens of 8 slots, 7168
 // channels, inputs not in the caches: bf16 rows 412 us, 5.1 TB/s, with a run of tokens per
-// XCD, 435 without; fp8 rows 285 us, 229 without the scales, whose 4-byte stores to
-// different lines cost as many L2 requests as the codes; sums of k rows 369 us, 5.7 TB/s,
+// XCD, 435 without; fp8 rows 248 us, 4.9 TB/s; sums of k rows 369 us, 5.7 TB/s,
 // 408 with outputs through the caches; gradients 782 us, 5.1 TB/s.)
 __device__ __forceinline__ v4i load16_once(const unsigned char* p) {
   return __builtin_nontemporal_load((const v4i_any*)p);
@@ -369,6 +368,9 @@ __global__ __launch_bounds__(256) void kg_dispatch_kernel(const unsigned char* _
   }
 }
 
+// Scale blocks of a row, rounded up to whole 16-byte units.
+__host__ __device__ constexpr int padded_blocks(int H) { return ((H + 127) / 128 + 3) & ~3; }
+
 // Largest of 8 neighbouring lanes' values.
 __device__ __forceinline__ float max8(float v) {
 #pragma unroll
@@ -388,14 +390,22 @@ __device__ __forceinline__ int codes4(float a, float b, float c, float d, float 
 }
 
 // e4m3 rows: 8 lanes hold one 128-channel block, 16 channels each; its scale is amax / 448 (1
-// for a block of zeros). The codes (16 bytes per thread) and the scale go to the token's k
-// rows. Here a unit is 16 channels.
+// for a block of zeros). The codes (16 bytes per thread) go to the token's k rows. Here a unit
+// is 16 channels.
+// The scales belong to k rows of sa [blocks, rows], each a 4-byte store to a line of its own, and
+// as many L2 requests as the codes' 128-byte ones. So many of them go to token_sa [T, padded
+// blocks] once per token, each row's slot goes to slot_of, and kg_row_scales_kernel writes
+// sa along its rows. Measured with 8 slots, 7168 channels, one step / two: 1024 tokens 14.8 /
+// 16.7 us, 4096 tokens 47.8 / 48.6, 8192 tokens 138.5 / 124.7 (4.8 TB/s), 16384 tokens
+// 278 / 248.
 __global__ __launch_bounds__(256) void kg_dispatch_fp8_kernel(const unsigned char* __restrict__ X,
                                                               int64_t ldx,
                                                               const int32_t* __restrict__ pos,
                                                               RowShape s,
                                                               unsigned char* __restrict__ Q,
-                                                              float* __restrict__ sa) {
+                                                              float* __restrict__ sa,
+                                                              float* __restrict__ token_sa,
+                                                              int32_t* __restrict__ slot_of) {
   int64_t t;
   int c;
   if (!my_unit(s, &t, &c)) return;  // whole groups of 16 lanes or more: shuffles stay inside
@@ -425,8 +435,39 @@ __global__ __launch_bounds__(256) void kg_dispatch_fp8_kernel(const unsigned cha
       const int64_t r = named_row(p.at[i], s.rows);
       if (r < 0) continue;
       store16_once(Q + r * s.H + 16 * (int64_t)c, p.at[i] < 0 ? v4i{0, 0, 0, 0} : q);
-      if ((c & 7) == 0) sa[(int64_t)(c >> 3) * s.rows + r] = p.at[i] < 0 ? 1.0f : sc;
+      if (token_sa == nullptr) {
+        if ((c & 7) == 0) sa[(int64_t)(c >> 3) * s.rows + r] = p.at[i] < 0 ? 1.0f : sc;
+      } else if (c == 0) {
+        slot_of[r] = (int32_t)(t * s.k + j0 + i);
+      }
     }
+  }
+  if (token_sa != nullptr && (c & 7) == 0) token_sa[t * padded_blocks(s.H) + (c >> 3)] = sc;
+}
+
+// sa[kb][r] for kRowBlocks blocks of 256 rows per workgroup, from the token that row r's slot
+// belongs to. slot_of was not cleared: a row that no slot names is told by its slot's
+// position, and left alone as in the direct form.
+constexpr int kRowBlocks = 8;
+__global__ __launch_bounds__(256) void kg_row_scales_kernel(const int32_t* __restrict__ pos,
+                                                            const int32_t* __restrict__ slot_of,
+                                                            const float* __restrict__ token_sa,
+                                                            RowShape s, float* __restrict__ sa) {
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (r >= s.rows) return;
+  const int slot = slot_of[r];
+  if (slot < 0 || slot >= s.rows) return;
+  const int at = pos[slot];
+  if ((at < 0 ? ~at : at) != r) return;
+  const int kb0 = blockIdx.y * kRowBlocks, blocks = (s.H + 127) / 128;
+  const float* from = token_sa + (int64_t)(slot / s.k) * padded_blocks(s.H) + kb0;
+#pragma unroll
+  for (int h = 0; h < kRowBlocks; h += 4) {
+    if (kb0 + h >= blocks) break;
+    const v4f x = *(const v4f*)(from + h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (kb0 + h + i < blocks) sa[(int64_t)(kb0 + h + i) * s.rows + r] = at < 0 ? 1.0f : x[i];
   }
 }
 
@@ -589,6 +630,9 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
   }
 }
 
+// Scales (rows times blocks) from which kg_dispatch_fp8 writes them in a second step.
+constexpr int64_t kTwoStepScales = 1 << 21;
+
 static int key_bits(int G) {
   int b = 1;
   while ((1 << b) <= G) ++b;
@@ -695,24 +739,46 @@ extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64
   return launch(fn, grid, 256, 0, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Xp);
 }
 
-extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k,
-                               int H, void* Q, float* sa, void* stream) {
+extern "C" int64_t kg_dispatch_fp8_workspace_bytes(int64_t T, int k, int H) {
   RowShape s;
   int64_t grid;
+  if (row_shape(T, k, H, 2, 32, true, &grid, &s) != KG_OK) return -1;
+  if (s.rows * ((H + 127) / 128) < kTwoStepScales) return 0;
+  return T * padded_blocks(H) * 4 + s.rows * 4;
+}
+
+extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k,
+                               int H, void* Q, float* sa, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  RowShape s;
+  int64_t grid;
+  if (workspace_bytes < 0) return KG_ERR_SHAPE;
   const int rc = row_shape(T, k, H, 2, 32, true, &grid, &s);
   if (rc != KG_OK) return rc;
   if (ldx < H) return KG_ERR_SHAPE;
   if (H % 16 != 0) return KG_ERR_ALIGN;
   if (s.rows == 0 || H == 0) return KG_OK;
   if (X == nullptr || pos == nullptr || Q == nullptr || sa == nullptr) return KG_ERR_NULL;
-  if (((uintptr_t)X & 1) || (((uintptr_t)pos | (uintptr_t)sa) & 3)) return KG_ERR_ALIGN;
-  const size_t nx = ((size_t)(T - 1) * ldx + H) * 2, nq = (size_t)s.rows * H;
-  const size_t ns = (size_t)((H + 127) / 128) * s.rows * 4, np = (size_t)s.rows * 4;
-  if (ranges_overlap(X, nx, Q, nq) || ranges_overlap(X, nx, sa, ns) ||
-      ranges_overlap(pos, np, Q, nq) || ranges_overlap(pos, np, sa, ns) ||
-      ranges_overlap(Q, nq, sa, ns))
-    return KG_ERR_ALIAS;
-  return launch(kg_dispatch_fp8_kernel, grid, 256, 0, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Q, sa);
+  const int64_t need = kg_dispatch_fp8_workspace_bytes(T, k, H);
+  const bool two = workspace != nullptr && need > 0 && workspace_bytes >= need;
+  if (((uintptr_t)X & 1) || (((uintptr_t)pos | (uintptr_t)sa) & 3) ||
+      (two && ((uintptr_t)workspace & 15)))
+    return KG_ERR_ALIGN;
+  const size_t np = (size_t)s.rows * 4;
+  const struct { const void* p; size_t n; bool written; } r[5] = {
+      {X, ((size_t)(T - 1) * ldx + H) * 2, false}, {pos, np, false}, {Q, (size_t)s.rows * H, true},
+      {sa, (size_t)((H + 127) / 128) * s.rows * 4, true}, {two ? workspace : nullptr, (size_t)need, true}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if (r[j].written && ranges_overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return KG_ERR_ALIAS;
+  float* token_sa = two ? (float*)workspace : nullptr;
+  int32_t* slot_of = two ? (int32_t*)(token_sa + T * padded_blocks(H)) : nullptr;
+  const int e = launch(kg_dispatch_fp8_kernel, grid, 256, 0, stream, (const unsigned char*)X, ldx,
+                       pos, s, (unsigned char*)Q, sa, token_sa, slot_of);
+  if (e != KG_OK || !two) return e;
+  const int groups = ((H + 127) / 128 + kRowBlocks - 1) / kRowBlocks;
+  return launch2(kg_row_scales_kernel, (s.rows + 255) / 256, groups, 256, 0, stream, pos, slot_of,
+                 token_sa, s, sa);
 }
 
 extern "C" int kg_combine(const void* Y, const int32_t* pos, const float* w, void* out, int64_t ldo,

@@ -96,6 +96,15 @@ def new_route_workspace(T, k, G, device):
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
+def _workspace(ws):
+    """(address, bytes) of a workspace tensor or None."""
+    if ws is None:
+        return None, 0
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous uint8")
+    return ws.data_ptr(), ws.numel()
+
+
 def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
     """Plan that puts tokens into expert order: idx int32 [T, k] (an entry outside [0, G) is
     dropped), ks int32 [G] (out). pos int32 [T, k] and src int32 [T * k] are written (made if
@@ -117,11 +126,7 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
         n = L.kg_route_workspace_bytes(T, k, G)
         if n > 0:
             ws = _made((n,), torch.uint8, idx, stream)
-    at, size = None, 0
-    if ws is not None:
-        if ws.dtype is not torch.uint8 or not ws.is_contiguous():
-            raise ValueError("ws must be contiguous uint8")
-        at, size = ws.data_ptr(), ws.numel()
+    at, size = _workspace(ws)
     _gpu(idx, ks, pos, src, ws)
     rc = L.kg_route(idx.data_ptr(), T, k, G, ks.data_ptr(), pos.data_ptr(), src.data_ptr(), at,
                     size, _on(idx, stream))
@@ -161,9 +166,10 @@ def kg_dispatch(X, pos, Xp=None, stream=None):
     return Xp
 
 
-def kg_dispatch_fp8(X, pos, Q=None, sa=None, stream=None):
+def kg_dispatch_fp8(X, pos, Q=None, sa=None, ws=None, stream=None):
     """kg_dispatch as e4m3 codes: X bfloat16 [T, H], H a multiple of 16; Q 1-byte [T * k, H] and
-    sa float32 [ceil(H / 128), T * k] as kg_fprop and kg_dgrad read them (made if not given).
+    sa float32 [ceil(H / 128), T * k] as kg_fprop and kg_dgrad read them (made if not given);
+    ws: a uint8 workspace of kg_dispatch_fp8_workspace_bytes (made if not given and of use).
     Returns (Q, sa)."""
     L = _load()
     if X.dtype is not _bf16:
@@ -178,9 +184,14 @@ def kg_dispatch_fp8(X, pos, Q=None, sa=None, stream=None):
     if Q.element_size() != 1 or Q.shape != (T * k, H) or not Q.is_contiguous():
         raise ValueError("Q must be a contiguous 1-byte [T * k, H] tensor")
     _expert_rows(sa, (-(-H // 128), T * k), _f32, "sa")
-    _gpu(X, pos, Q, sa)
+    if ws is None:
+        n = L.kg_dispatch_fp8_workspace_bytes(T, k, H)
+        if n > 0:
+            ws = _made((n,), torch.uint8, X, stream)
+    at, size = _workspace(ws)
+    _gpu(X, pos, Q, sa, ws)
     rc = L.kg_dispatch_fp8(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, Q.data_ptr(),
-                           sa.data_ptr(), _on(X, stream))
+                           sa.data_ptr(), at, size, _on(X, stream))
     if rc:
         _fail(rc, "kg_dispatch_fp8")
     return Q, sa

@@ -418,7 +418,11 @@ int64_t kg_route_workspace_bytes(int64_t T, int k, int G);
 int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k, int H, int type,
                 void* Xp, void* stream);
 int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, int64_t T, int k, int H,
-                    void* Q, float* sa, void* stream);
+                    void* Q, float* sa, void* workspace, int64_t workspace_bytes, void* stream);
+/* Workspace with which kg_dispatch_fp8 writes many rows' scales faster, in bytes (0: it would
+   not use one; -1 for sizes it does not take). It may be NULL or smaller (then it is not
+   used), needs no initialisation and is 16-byte aligned. Results do not depend on it. */
+int64_t kg_dispatch_fp8_workspace_bytes(int64_t T, int k, int H);
 
 /*
  * kg_combine -- enqueue out[t] = sum_j w[t][j] * Y[pos[t][j]] over t's kept slots, in fp32 in

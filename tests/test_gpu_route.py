@@ -151,7 +151,8 @@ def e4m3_of(x):
 
 
 @pytest.mark.parametrize("T,k,G,H", [(1, 8, 16, 7168), (3, 2, 4, 16), (40, 3, 8, 144), (65, 8, 32, 2000),
-                                     (200, 2, 5, 128), (10, 1, 2, 4112)])
+                                     (200, 2, 5, 128), (10, 1, 2, 4112), (60000, 8, 40, 656),
+                                     (250000, 1, 7, 1040)])
 @pytest.mark.parametrize("kind", ["uniform", "wild"])
 def test_dispatch_fp8(T, k, G, H, kind):
     g = torch.Generator(DEV).manual_seed(H)
@@ -174,6 +175,33 @@ def test_dispatch_fp8(T, k, G, H, kind):
     assert np.array_equal(np.where(nan, 0x7F, want), got)
     want_s = np.where(kept[:, None], s[tok], np.float32(1)).T
     assert np.array_equal(sa.cpu().numpy().view(np.uint32), want_s.astype(np.float32).view(np.uint32))
+
+
+def test_fp8_scales_in_two_steps_and_in_one():
+    """With and without the workspace: the same bits, and rows that no slot names are left alone
+    whatever the workspace held."""
+    T, k, H = 60000, 4, 1168  # 10 blocks: 2.4 M scales
+    pos = torch.randperm(T * k, device=DEV).to(torch.int32).view(T, k)
+    pos[::3, 1] = ~pos[::3, 1]
+    pos[5, 0], pos[6, 2], pos[7, 3] = T * k, -2**31, 2**31 - 1
+    X = torch.randn((T, H), device=DEV).to(BF16)
+    L = kg.layer.lib()
+    n = L.kg_dispatch_fp8_workspace_bytes(T, k, H)
+    assert n > 0
+    got = []
+    for fill in (None, 0, 1, 0xFF):
+        Q = torch.full((T * k, H), 0x55, dtype=torch.uint8, device=DEV)
+        sa = torch.full((10, T * k), 9.0, device=DEV)
+        if fill is None:
+            st = torch.cuda.current_stream().cuda_stream
+            assert L.kg_dispatch_fp8(X.data_ptr(), H, pos.data_ptr(), T, k, H, Q.data_ptr(),
+                                     sa.data_ptr(), None, 0, st) == kg.KG_OK
+        else:
+            kg.kg_dispatch_fp8(X, pos, Q, sa, torch.full((n,), fill, dtype=torch.uint8, device=DEV))
+        got.append((Q, sa))
+    for Q, sa in got[1:]:
+        assert torch.equal(Q, got[0][0]) and torch.equal(sa, got[0][1])
+    assert int((got[0][1] == 9).all(0).sum()) == 3
 
 
 def test_special_values():

@@ -89,13 +89,22 @@ def test_route_workspace_sizes():
     assert 0 < need(16384, 8, 256) < need(1 << 20, 8, 256)
 
 
+def test_fp8_workspace_sizes():
+    need = B.lib().kg_dispatch_fp8_workspace_bytes
+    assert need(8, 8, 7168) == 0
+    assert need(-1, 8, 128) == need(8, 5000, 128) == -1
+    assert need(8192, 8, 7168) == 8192 * 56 * 4 + 65536 * 4
+    assert need(1024, 8, 7168) == 0
+    assert need(131072, 8, 144) == 131072 * 4 * 4 + 1048576 * 4
+
+
 def rows(fn, X=FAKE[0], ld=32, pos=FAKE[1], T=10, k=4, H=32, ty=0, out=FAKE[2], w=FAKE[3],
-         sa=FAKE[4], dw=FAKE[5], Y=FAKE[6]):
+         sa=FAKE[4], dw=FAKE[5], Y=FAKE[6], ws=None, wb=0):
     L = B.lib()
     if fn == "dispatch":
         return L.kg_dispatch(X, ld, pos, T, k, H, ty, out, None)
     if fn == "dispatch_fp8":
-        return L.kg_dispatch_fp8(X, ld, pos, T, k, H, out, sa, None)
+        return L.kg_dispatch_fp8(X, ld, pos, T, k, H, out, sa, ws, wb, None)
     if fn == "combine":
         return L.kg_combine(X, pos, w, out, ld, T, k, H, ty, None)
     return L.kg_combine_bwd(X, ld, Y, pos, w, out, dw, T, k, H, ty, None)
@@ -138,6 +147,10 @@ def test_row_refusals(fn, kw, code):
     ("dispatch_fp8", dict(sa=None), B.KG_ERR_NULL),
     ("dispatch_fp8", dict(sa=FAKE[2] + 4), B.KG_ERR_ALIAS),
     ("dispatch_fp8", dict(sa=FAKE[1]), B.KG_ERR_ALIAS),
+    ("dispatch_fp8", dict(wb=-1), B.KG_ERR_SHAPE),
+    ("dispatch_fp8", dict(T=1000000, ws=FAKE[7] + 8, wb=1 << 26), B.KG_ERR_ALIGN),
+    ("dispatch_fp8", dict(T=1000000, ws=FAKE[2] + 64, wb=1 << 26), B.KG_ERR_ALIAS),
+    ("dispatch_fp8", dict(T=1000000, ws=FAKE[0], wb=1 << 26), B.KG_ERR_ALIAS),
     ("combine", dict(w=FAKE[3] + 2), B.KG_ERR_ALIGN),
     ("combine", dict(w=FAKE[2]), B.KG_ERR_ALIAS),
     ("combine_bwd", dict(Y=None), B.KG_ERR_NULL),
