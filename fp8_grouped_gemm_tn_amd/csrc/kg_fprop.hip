@@ -47,7 +47,6 @@ struct FParams {
   int64_t M_total, lda, ldd;
   int G, N, K;
   int tiles_n;
-  int vec;  // D's rows start at 16-byte boundaries
 };
 
 // Row m (0 .. 15) of MFMA row tile i holds output row frow(i, m) of the wave's: pairs of
@@ -98,18 +97,21 @@ __device__ __forceinline__ v4f block_sum(const Frag<false>& w, const Frag<false>
   return s;
 }
 
-// Stores eight outputs [n, n + 8) of one token; `left` = N - n of them exist.
+// Stores eight outputs [n, n + 8) of one token; `left` = N - n of them exist. Rows of D may start
+// at any element: gfx950 takes 16-byte stores at any address.
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
 template <bool OUTB>
-__device__ __forceinline__ void store_run(void* D, int64_t at, int left, bool vec, const v4f& a,
+__device__ __forceinline__ void store_run(void* D, int64_t at, int left, const v4f& a,
                                           const v4f& b) {
   if constexpr (OUTB) {
     unsigned short* d = (unsigned short*)D + at;
     const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    v8bf h;
+    if (left >= 8) {
+      v8bf h;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (__bf16)x[i];  // to nearest, ties to even
-    if (vec && left >= 8) {
-      *(v4i*)d = __builtin_bit_cast(v4i, h);
+      for (int i = 0; i < 8; ++i) h[i] = (__bf16)x[i];  // to nearest, ties to even
+      *(v4i_any*)d = __builtin_bit_cast(v4i, h);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -117,9 +119,9 @@ __device__ __forceinline__ void store_run(void* D, int64_t at, int left, bool ve
     }
   } else {
     float* d = (float*)D + at;
-    if (vec && left >= 8) {
-      *(v4f*)d = a;
-      *(v4f*)(d + 4) = b;
+    if (left >= 8) {
+      *(v4f_any*)d = a;
+      *(v4f_any*)(d + 4) = b;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -387,7 +389,7 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 #pragma unroll
       for (int i = 0; i < C::NI; i += 2) {
         const int n = nw + 16 * i + 8 * q;
-        store_run<OUTB>(p.D, at + n, p.N - n, p.vec, acc[i][tt], acc[i + 1][tt]);
+        store_run<OUTB>(p.D, at + n, p.N - n, acc[i][tt], acc[i + 1][tt]);
       }
     }
   }
@@ -398,7 +400,7 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 // ------------------------------------------------------------------------ streaming kernel
 
 // A workgroup computes 32 outputs of one expert for all its rows, 16 TT at a time: grid
-// G x ceil(N / 32). Its 8 waves take the blocks of the contraction axis in turn, each adding
+// min(G, M_total) x ceil(N / 32), the experts without rows left out. Its 8 waves take the blocks of the contraction axis in turn, each adding
 // up its blocks in registers, with the next block's operands on their way; the waves' sums
 // are added in LDS in a fixed order. A lane reads 32 neighbouring channels of a row, so a
 // row's 128 bytes go to four lanes of one load.
@@ -407,28 +409,54 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 // with one block's loads at a time). 64 outputs per workgroup: 139 us.
 constexpr int kStreamWaves = 8, kStreamN = 32;
 
-// Offsets by a scan of ms in every wave. Returns false if ms is inconsistent.
-__device__ __forceinline__ bool find_rows(const FParams& p, int g, int64_t* row0, int* rows) {
-  const int lane = threadIdx.x & 63;
-  int64_t sum = 0, before = 0;
-  int mine = 0, neg = 0;
-  for (int i = lane; i < p.G; i += 64) {
-    const int v = p.ms[i];
+// The expert with rows that `nth` others with rows come before, its first row and their number, by
+// a scan of ms in every wave (a lane holds consecutive experts). rows = 0: there is none.
+// Returns false if ms is inconsistent.
+__device__ __forceinline__ bool find_rows(const FParams& p, int nth, int* g, int64_t* row0,
+                                          int* rows) {
+  const int lane = threadIdx.x & 63, per = (p.G + 63) / 64;
+  const int e0 = lane * per, e1 = min(p.G, e0 + per);
+  int64_t sum = 0;
+  int live = 0, neg = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int v = p.ms[e];
     neg |= v < 0;
     sum += v;
-    if (i < g) before += v;
-    if (i == g) mine = v;
+    live += v > 0;
   }
+  int64_t to = sum;  // rows and experts up to this lane's last one
+  int live_to = live;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    sum += __shfl_xor(sum, d, 64);
-    before += __shfl_xor(before, d, 64);
-    mine += __shfl_xor(mine, d, 64);
-    neg |= __shfl_xor(neg, d, 64);
+    const int64_t u = __shfl_up(to, d, 64);
+    const int v = __shfl_up(live_to, d, 64);
+    if (lane >= d) {
+      to += u;
+      live_to += v;
+    }
   }
-  *row0 = before;
-  *rows = uniform(mine);
-  return neg == 0 && sum == p.M_total;
+  const bool ok = __ballot(neg != 0) == 0 && __shfl(to, 63, 64) == p.M_total;
+  const uint64_t has = __ballot(live_to > nth);  // the first such lane has the expert
+  *rows = 0;
+  *g = 0;
+  *row0 = 0;
+  if (!ok || has == 0) return ok;
+  const int owner = __builtin_ctzll(has);
+  int64_t at = to - sum;
+  int mine = 0, mg = 0, left = nth - (live_to - live);
+  for (int e = e0; e < e1 && lane == owner; ++e) {
+    const int v = p.ms[e];
+    if (v > 0 && left-- == 0) {
+      mine = v;
+      mg = e;
+      break;
+    }
+    at += v;
+  }
+  *row0 = __shfl(at, owner, 64);
+  *rows = uniform(__shfl(mine, owner, 64));
+  *g = uniform(__shfl(mg, owner, 64));
+  return true;
 }
 
 template <int TT, bool FAST, bool OUTB>
@@ -436,12 +464,12 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
   constexpr int NJ = kStreamN / 16;
   __shared__ v4f sums[kStreamWaves][NJ * TT][64];
   const int per = p.tiles_n;  // workgroups per expert
-  const int g = blockIdx.x / per, n0 = (blockIdx.x - g * per) * kStreamN;
+  const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * kStreamN;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, j = lane & 15;
   int64_t row0;
-  int rows;
-  if (!find_rows(p, g, &row0, &rows)) {
+  int rows, g;
+  if (!find_rows(p, nth, &g, &row0, &rows)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = KG_ERR_KSUM;
     return;
   }
@@ -543,7 +571,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
         }
       }
       const int r = r0 + 16 * tt + j, n = n0 + 16 * i0 + 8 * q;
-      if (r < rows) store_run<OUTB>(p.D, (row0 + r) * p.ldd + n, p.N - n, p.vec, x[0], x[1]);
+      if (r < rows) store_run<OUTB>(p.D, (row0 + r) * p.ldd + n, p.N - n, x[0], x[1]);
     }
     __syncthreads();
   }
@@ -662,12 +690,11 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
   p.G = G;
   p.N = N;
   p.K = K;
-  p.vec = ((uintptr_t)D & 15) == 0 && ldd * el % 16 == 0;
   FLaunch l = f_choose(M_total, G, N, cus, fast, outb);
   p.tiles_n = (N + l.bn - 1) / l.bn;
   int64_t grid;
   if (l.id < 0) {
-    grid = (int64_t)G * p.tiles_n;
+    grid = (int64_t)(G < M_total ? G : M_total) * p.tiles_n;
     if (grid > INT32_MAX) return KG_ERR_UNSUPPORTED;
   } else {
     l.lds += sched_bytes(G);
