@@ -582,12 +582,10 @@ struct FLaunch {
   int bt, bn, lds, per_cu, id;
 };
 
-template <class C>
-static FLaunch f_tiled(bool fast, bool outb, int id) {
-  const void* fn = fast ? (outb ? (const void*)kg_fprop_kernel<C, true, true>
-                                : (const void*)kg_fprop_kernel<C, true, false>)
-                        : (outb ? (const void*)kg_fprop_kernel<C, false, true>
-                                : (const void*)kg_fprop_kernel<C, false, false>);
+template <class C, bool FAST>
+static FLaunch f_tiled(bool outb, int id) {
+  const void* fn = outb ? (const void*)kg_fprop_kernel<C, FAST, true>
+                        : (const void*)kg_fprop_kernel<C, FAST, false>;
   return FLaunch{fn, C::BT, C::BN, C::NS * C::STAGE, C::PER_CU, id};
 }
 
@@ -600,28 +598,33 @@ static FLaunch f_stream(bool fast, bool outb) {
   return FLaunch{fn, 16 * TT, kStreamN, 0, 1, -1};
 }
 
-// The tiles that a launch takes: FastBig 256 x 256 for the fp8 MFMA, ExactBig 128 x 256 for
-// the bf16 MFMA (whose widened token fragments leave no room for 256 x 256: 1696 us spilled,
-// 1695 us here on the 32768-token problem above; 256 x 128 1707), Small 128 x 128 with two
-// workgroups per compute unit for either.
-using FastBig = FCfg<256, 256, 4, 1>;
-using ExactBig = FCfg<128, 256, 2, 1>;
-using Small = FCfg<128, 128, 4, 2>;
+// A tile and what one block of it takes on every compute unit, in tenths of a microsecond:
+// `first` while there are no more tiles than compute units, else `round` for PER_CU of them.
+struct FTile {
+  FLaunch l;
+  int first, round;
+};
 
 // Which kernel and tile. The experts' sizes are known on the device only, so this goes by
 // M_total and G; every choice is right for every distribution of the rows.
 //  * Streaming up to 8 rows per expert on average, and up to 64 while M_total * N <= 2^19
-//    (few rows in all: a tile's time is then the latency of its blocks, 0.6 us each).
-//    K = 7168, N = 4096, streaming / Small: 32 experts of 2, 8, 16 rows 127/153, 164/167,
+//    (few rows in all: a tile's time is then the latency of its blocks). K = 7168,
+//    N = 4096, streaming / 128 x 128 tiles: 32 experts of 2, 8, 16 rows 127/153, 164/167,
 //    231/170 us; 4 experts of 16, 32, 64 rows 27/41, 37/41, 71/42; 1 of 16, 64, 128 rows
-//    13/39, 23/39, 42/40.
-//    TT token tiles hold an expert's rows: the average, or twice it where several experts
-//    share M_total unevenly (4 experts of 16 rows, TT 1, 2, 4: 30, 27, 32 us).
-//  * Else the big or the small tile by their estimated rounds over the compute units times
-//    a round's time per block, in tenths of a microsecond: 15 and 12 (7 where the
-//    tiles are fewer than the compute units), exact products 18 and 23 (10). 32 experts of
-//    32, 64, 97, 128 rows, FastBig / Small: 211/171, 223/208, 233/241, 241/273 us; 4096
-//    rows, one expert, N = 7168, K = 2048: 67/84.
+//    13/39, 23/39, 42/40. TT token tiles hold an expert's rows: the average, or twice it
+//    where several experts share M_total unevenly (4 experts of 16 rows, TT 1, 2, 4: 30,
+//    27, 32 us).
+//  * Else the tile with the least estimated time, rounds over the compute units times a
+//    block's time. The number of 16-byte operand reads per MFMA falls with the tile's size,
+//    the latency of a block and the rows that an expert's last tile leaves empty rise.
+//    fp8 MFMA, 64 x 64 / 64 x 128 / 128 x 128 / 256 x 256: 256 rows, N 4096, K 7168 25 / 27 /
+//    34 / 75 us; 512 rows, K 4096 29 / 18 / 23 / 47; 1024 rows 41 / 29 / 25 / 47; 32 experts
+//    of 32 and 97 rows, K 7168 195 / 187 / 173 / 196 and 328 / 259 / 240 / 212.
+//    Exact products, 64 x 64 / 64 x 128 / 128 x 128 / 128 x 256: 256 rows 36 / 47 / 61 / 95 us;
+//    1024 rows, K 4096 59 / 45 / 41 / 57; 32 experts of 16 and 64 rows, K 7168 214 / 171 /
+//    247 / 207 and 312 / 246 / 268 / 226; 32768 rows of 8 experts, K 7168 1.69 ms with
+//    128 x 256 (256 x 256, whose widened fragments spill, 1.70). Two 128 x 128 workgroups
+//    per compute unit spill too (61 -> 110 us on the 256 rows).
 static FLaunch f_choose(int64_t M, int G, int N, int cus, bool fast, bool outb) {
   const int64_t avg = (M + G - 1) / G;
   if (avg <= 8 || (avg <= 64 && M * N <= (1 << 19))) {
@@ -629,17 +632,35 @@ static FLaunch f_choose(int64_t M, int G, int N, int cus, bool fast, bool outb) 
     return rows <= 16 ? f_stream<1>(fast, outb) : rows <= 32 ? f_stream<2>(fast, outb)
                                                              : f_stream<4>(fast, outb);
   }
+  using Tile64 = FCfg<64, 64, 4, 2>;
+  using Tile64x128 = FCfg<64, 128, 2, 2>;
+  const FTile tiles[4] = {
+      {fast ? f_tiled<FCfg<256, 256, 4, 1>, true>(outb, 0)
+            : f_tiled<FCfg<128, 256, 2, 1>, false>(outb, 4), fast ? 15 : 18, fast ? 15 : 18},
+      {fast ? f_tiled<FCfg<128, 128, 4, 2>, true>(outb, 1)
+            : f_tiled<FCfg<128, 128, 4, 1>, false>(outb, 5), fast ? 7 : 12, 12},
+      {fast ? f_tiled<Tile64x128, true>(outb, 2) : f_tiled<Tile64x128, false>(outb, 6),
+       fast ? 5 : 8, fast ? 10 : 15},
+      {fast ? f_tiled<Tile64, true>(outb, 3) : f_tiled<Tile64, false>(outb, 7), fast ? 4 : 6,
+       fast ? 8 : 9}};
   const int64_t live = G < M ? G : M;
-  auto cost = [&](int bt, int bn, int per_cu, int round, int first) {
-    const int64_t mt = M / bt + live / 2 > live ? M / bt + live / 2 : live;
-    const int64_t tiles = mt * ((N + bn - 1) / bn), at_once = (int64_t)cus * per_cu;
-    return tiles <= cus ? first : (tiles + at_once - 1) / at_once * round;
-  };
-  const int64_t small = cost(Small::BT, Small::BN, Small::PER_CU, fast ? 12 : 23, fast ? 7 : 10);
-  const int64_t big = fast ? cost(FastBig::BT, FastBig::BN, 1, 15, 15)
-                           : cost(ExactBig::BT, ExactBig::BN, 1, 18, 18);
-  if (small < big) return f_tiled<Small>(fast, outb, 0);
-  return fast ? f_tiled<FastBig>(true, outb, 1) : f_tiled<ExactBig>(false, outb, 2);
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 4; ++i) {
+    const FLaunch& l = tiles[i].l;
+    // tiles along the rows, in tenths: one expert's are known; of several, each has a last
+    // one that is filled to some part
+    int64_t mt = live == 1 ? (M + l.bt - 1) / l.bt * 10 : 10 * M / l.bt + 6 * live;
+    if (mt < 10 * live) mt = 10 * live;
+    const int64_t n = (mt * ((N + l.bn - 1) / l.bn) + 9) / 10, at_once = (int64_t)cus * l.per_cu;
+    const int64_t t = n <= cus ? tiles[i].first : (n + at_once - 1) / at_once * tiles[i].round;
+    // ties go to the smaller tile, whose estimate errs less
+    if (t <= least) {
+      least = t;
+      best = i;
+    }
+  }
+  return tiles[best].l;
 }
 
 }  // namespace kg
@@ -699,14 +720,14 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
   } else {
     l.lds += sched_bytes(G);
     static std::mutex mu;
-    static int set[64][3][2][2];  // the largest LDS size asked for so far
+    static int set[64][8][2];  // the largest LDS size asked for so far
     {
       std::lock_guard<std::mutex> lk(mu);
-      if (set[dev][l.id][fast][outb] < l.lds) {
+      if (set[dev][l.id][outb] < l.lds) {
         if (hipFuncSetAttribute(l.fn, hipFuncAttributeMaxDynamicSharedMemorySize, l.lds) !=
             hipSuccess)
           return KG_ERR_HIP;
-        set[dev][l.id][fast][outb] = l.lds;
+        set[dev][l.id][outb] = l.lds;
       }
     }
     const int64_t max_items = (M_total / l.bt + G) * (int64_t)p.tiles_n;
