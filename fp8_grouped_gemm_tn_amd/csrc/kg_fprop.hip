@@ -241,6 +241,64 @@ __device__ __forceinline__ void f_meet() {
 // compiler wait for them.
 typedef __attribute__((address_space(4))) const float ConstFloat;
 
+// Exclusive scans over the experts, in LDS: off[g] rows and boff[g] tiles of `bt` rows before
+// expert g, g = 0 .. G. Returns false if ms holds a negative count or does not add up to
+// M_total. (kg_sched.h's scan also orders the experts by length, G^2 LDS reads, which a walk in
+// expert order does not need.)
+template <int THREADS>
+__device__ __forceinline__ bool f_offsets(const int32_t* ms, int G, int bt, int64_t M_total,
+                                          int* off, int* boff) {
+  constexpr int E = kMaxGroups / THREADS, W = THREADS / 64;
+  __shared__ int64_t rows_of[W];
+  __shared__ int tiles_of[W];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  int kv[E], bv[E], neg = 0, own_b = 0;
+  int64_t own = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int g = E * t + e;
+    kv[e] = g < G ? ms[g] : 0;
+    neg |= kv[e] < 0;
+    bv[e] = kv[e] > 0 ? kv[e] / bt + (kv[e] % bt != 0) : 0;
+    own += kv[e];
+    own_b += bv[e];
+  }
+  const int64_t to = wave_incl_scan<int64_t>(own);
+  const int to_b = wave_incl_scan<int>(own_b);
+  if (lane == 63) {
+    rows_of[w] = to;
+    tiles_of[w] = to_b;
+  }
+  const int any_neg = __syncthreads_or(neg);
+  int64_t total = 0, run = to - own;
+  int run_b = to_b - own_b;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    total += rows_of[i];
+    if (i < w) {
+      run += rows_of[i];
+      run_b += tiles_of[i];
+    }
+  }
+  if (any_neg || total != M_total) return false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int g = E * t + e;
+    if (g <= G) {  // (G < kMaxGroups: else the last entry is the next line's)
+      off[g] = (int)run;
+      boff[g] = run_b;
+    }
+    run += kv[e];
+    run_b += bv[e];
+  }
+  if (t == THREADS - 1 && G == kMaxGroups) {
+    off[G] = (int)run;
+    boff[G] = run_b;
+  }
+  __syncthreads();
+  return true;
+}
+
 // The loop over the blocks. The token fragments are read one block ahead, each right after its
 // last MFMA of the block before, so the buffer that block kb's tokens came from is free during
 // block kb and their block kb + 2 loads into it. W's block kb has been read before the
@@ -267,15 +325,14 @@ typedef __attribute__((address_space(4))) const float ConstFloat;
 template <class C, bool FAST, bool OUTB>
 __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  __shared__ int64_t wsum_k[kMaxWaves];
-  __shared__ int32_t wsum_b[kMaxWaves];
   constexpr int LAG = 3, S = C::NI * C::TT;
-  Sched s = sched_carve(smem + C::NS * C::STAGE, p.G);
-  if (sched_build<C::THREADS>(p.ms, p.G, C::BT, p.M_total, s, wsum_k, wsum_b) != KG_OK) {
+  int* off = (int*)(smem + C::NS * C::STAGE);  // [G + 1]
+  int* boff = off + p.G + 1;
+  if (!f_offsets<C::THREADS>(p.ms, p.G, C::BT, p.M_total, off, boff)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = KG_ERR_KSUM;
     return;
   }
-  const int mt_total = s.boff[p.G], total = mt_total * p.tiles_n;
+  const int mt_total = boff[p.G], total = mt_total * p.tiles_n;
   const int grid = gridDim.x, b = blockIdx.x;
   // XCD-contiguous runs when the items take several rounds, as in kg_dgrad
   const int slot = (grid % 8 == 0 && total > grid) ? (b % 8) * (grid / 8) + b / 8 : b;
@@ -298,12 +355,11 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
     int lo_g = 0, hi_g = p.G;  // expert of m-tile mtg: the last g with boff[g] <= mtg
     while (hi_g - lo_g > 1) {
       const int mid = (lo_g + hi_g) >> 1;
-      if (s.boff[mid] <= mtg) lo_g = mid; else hi_g = mid;
+      if (boff[mid] <= mtg) lo_g = mid; else hi_g = mid;
     }
     const int g = uniform(lo_g);
-    // (rows fit 31 bits)
-    const int row0 = uniform((int)s.off[g] + (mtg - s.boff[g]) * C::BT);
-    const int rows = uniform((int)min((int64_t)C::BT, s.off[g + 1] - row0));
+    const int row0 = uniform(off[g] + (mtg - boff[g]) * C::BT);
+    const int rows = uniform(min(C::BT, off[g + 1] - row0));
     const int n0 = nt * C::BN;
     const int nw = n0 + wn * C::NI * 16;  // this wave's outputs, in one weight-scale block
     const ConstFloat* swg =
@@ -718,7 +774,7 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
     grid = (int64_t)(G < M_total ? G : M_total) * p.tiles_n;
     if (grid > INT32_MAX) return KG_ERR_UNSUPPORTED;
   } else {
-    l.lds += sched_bytes(G);
+    l.lds += 2 * (G + 1) * 4;
     static std::mutex mu;
     static int set[64][8][2];  // the largest LDS size asked for so far
     {
