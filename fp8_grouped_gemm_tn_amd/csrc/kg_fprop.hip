@@ -382,9 +382,11 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
       const unsigned char* r = fragw + (kb & 1) * C::STAGE + frow(i, 0) * C::TK;
       wf[i & 1].set(*(const v4i*)(r + c0), *(const v4i*)(r + c1));
     };
-    f_meet<0>();  // every wave is done with the previous item's stages
     float swv = 0.f;
     if (nk > 0) {
+      // (behind the previous tile's last meeting, so every wave is done with its stages; its
+      // stores may be under way, and so may its last loads, which read nothing: a wave's
+      // operations end in order, and a place in LDS is always loaded by the same wave)
       swv = swg[0];
 #pragma unroll
       for (int x = C::LW; x < C::LOADS; ++x) L.load(0, 0, x);
