@@ -35,6 +35,9 @@ constexpr int kAdamThreads = 256;
 constexpr int kAdamPer = 8;  // consecutive elements per thread: 16 threads hold one block
 constexpr int kItem = kAdamThreads * kAdamPer;
 
+// A launch holds fewer than 2^32 threads: 3.4e10 elements.
+constexpr int64_t kMaxItems = ((int64_t)1 << 32) / kAdamThreads - 1;
+
 struct AdamDesc {
   kg_adamw_tensor t;
   int64_t first_item;
@@ -257,7 +260,7 @@ extern "C" int64_t kg_adamw_items(const kg_adamw_tensor* tensors, int count) {
   for (int i = 0; i < count; ++i) {
     if (tensors[i].n < 0) return -1;
     items += items_of(tensors[i].n);
-    if (items > INT32_MAX) return -1;
+    if (items > kMaxItems) return -1;
   }
   return items;
 }
@@ -341,7 +344,7 @@ extern "C" int kg_adamw(const void* table, int count, int64_t items, int kinds, 
   if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && eps >= 0 && lr >= 0 &&
         weight_decay >= 0))
     return KG_ERR_SHAPE;
-  if (items > INT32_MAX) return KG_ERR_UNSUPPORTED;
+  if (items > kMaxItems) return KG_ERR_UNSUPPORTED;
   if (count == 0 || items == 0) return KG_OK;
   if (table == nullptr) return KG_ERR_NULL;
   if (((uintptr_t)table & 7) || (((uintptr_t)gscale | (uintptr_t)dyn) & 3)) return KG_ERR_ALIGN;

@@ -684,8 +684,9 @@ struct FTile {
 //    128 x 256 (256 x 256, whose widened fragments spill, 1.70). Two 128 x 128 workgroups
 //    per compute unit spill too (61 -> 110 us on the 256 rows).
 static FLaunch f_choose(int64_t M, int G, int N, int cus, bool fast, bool outb) {
-  const int64_t avg = (M + G - 1) / G;
-  if (avg <= 8 || (avg <= 64 && M * N <= (1 << 19))) {
+  const int64_t avg = (M + G - 1) / G, live = G < M ? G : M;
+  const bool fits = live * ((N + kStreamN - 1) / kStreamN) < (1 << 23);  // 2^32 threads
+  if (fits && (avg <= 8 || (avg <= 64 && M * N <= (1 << 19)))) {
     const int64_t rows = G == 1 ? avg : 2 * avg;
     return rows <= 16 ? f_stream<1>(fast, outb) : rows <= 32 ? f_stream<2>(fast, outb)
                                                              : f_stream<4>(fast, outb);
@@ -701,7 +702,6 @@ static FLaunch f_choose(int64_t M, int G, int N, int cus, bool fast, bool outb) 
        fast ? 5 : 8, fast ? 10 : 15},
       {fast ? f_tiled<Tile64, true>(outb, 3) : f_tiled<Tile64, false>(outb, 7), fast ? 4 : 6,
        fast ? 8 : 9}};
-  const int64_t live = G < M ? G : M;
   int best = 0;
   int64_t least = INT64_MAX;
   for (int i = 0; i < 4; ++i) {
@@ -774,7 +774,6 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
   int64_t grid;
   if (l.id < 0) {
     grid = (int64_t)(G < M_total ? G : M_total) * p.tiles_n;
-    if (grid > INT32_MAX) return KG_ERR_UNSUPPORTED;
   } else {
     l.lds += 2 * (G + 1) * 4;
     static std::mutex mu;
@@ -789,7 +788,7 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
       }
     }
     const int64_t max_items = (M_total / l.bt + G) * (int64_t)p.tiles_n;
-    if (max_items > INT32_MAX) return KG_ERR_UNSUPPORTED;
+    if (max_items > INT32_MAX - 4096) return KG_ERR_UNSUPPORTED;  // (indexes pass it by a grid)
     const int64_t at_once = (int64_t)cus * l.per_cu;
     grid = max_items < at_once ? max_items : at_once;
   }

@@ -230,7 +230,14 @@ struct RowShape {
   int k, H;
   int lanes;   // threads per token: a power of two up to the workgroup's 256
   int slices;  // workgroups per token (the kernels that take one unit per thread)
+  int64_t groups;  // workgroups that have work
 };
+
+// A launch holds fewer than 2^32 threads in x: more workgroups go over y as well.
+constexpr int64_t kGroupsX = 1 << 23;
+__device__ __forceinline__ int64_t group_id() {
+  return (int64_t)blockIdx.y * kGroupsX + blockIdx.x;
+}
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t u) { return __uint_as_float(u << 16); }
 
@@ -305,13 +312,14 @@ __device__ __forceinline__ int64_t named_row(int at, int64_t rows) {
 // XCDs in turn; BY_XCD gives each XCD a run of tokens instead.
 template <bool BY_XCD = false>
 __device__ __forceinline__ bool my_unit(const RowShape& s, int64_t* t, int* c) {
+  const int64_t b = group_id();
   if (s.lanes == 256) {
-    const unsigned per = gridDim.x / 8, b = blockIdx.x;
-    const unsigned id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
-    *t = id / (unsigned)s.slices;
+    const int64_t per = s.groups / 8;
+    const int64_t id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
+    *t = id / s.slices;
     *c = (int)(id - *t * s.slices) * 256 + threadIdx.x;
   } else {
-    *t = (int64_t)blockIdx.x * (256 / s.lanes) + threadIdx.x / s.lanes;
+    *t = b * (256 / s.lanes) + threadIdx.x / s.lanes;
     *c = threadIdx.x & (s.lanes - 1);
   }
   return *t < s.T;
@@ -537,7 +545,7 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
   using V = Vec<BF16>;
   __shared__ float part[4][8];
   const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
-  const int64_t t0 = (int64_t)blockIdx.x * per + threadIdx.x / s.lanes;
+  const int64_t t0 = group_id() * per + threadIdx.x / s.lanes;
   const bool live = t0 < s.T;  // a workgroup of a token's 256 threads is live as a whole
   const int64_t t = live ? t0 : 0;
   const int64_t bytes = (int64_t)s.H * V::ELEM;
@@ -650,8 +658,7 @@ static int64_t route_blocks(int64_t n) { return (n + route_block(n) - 1) / route
 // Checks that the row kernels share, and their launch shape: threads per token are the
 // power of two (16 to 256) that covers the row's units (of `unit` bytes, the last one
 // partial); past 256 units a token takes several workgroups if `split`, else a loop.
-static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, int64_t* grid,
-                     RowShape* s) {
+static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, RowShape* s) {
   if (T < 0 || k < 0 || H < 0) return KG_ERR_SHAPE;
   if (H > (1 << 24) || k > 4096 || (k > 0 && T > (int64_t)(INT32_MAX - 1) / k) || T > INT32_MAX - 1)
     return KG_ERR_UNSUPPORTED;
@@ -664,8 +671,16 @@ static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, in
   while (s->lanes < 256 && s->lanes < units) s->lanes *= 2;
   s->slices = split && units > 256 ? (int)((units + 255) / 256) : 1;
   const int per = 256 / s->lanes;
-  *grid = (T + per - 1) / per * s->slices;
-  return *grid <= INT32_MAX ? KG_OK : KG_ERR_UNSUPPORTED;
+  s->groups = (T + per - 1) / per * s->slices;
+  return s->groups <= kGroupsX * 65535 ? KG_OK : KG_ERR_UNSUPPORTED;
+}
+
+// A row kernel on s.groups workgroups (those past them in the last line have no token).
+template <typename... P>
+static int launch_rows(void (*fn)(P...), const RowShape& s, void* stream,
+                       typename same<P>::type... args) {
+  const int64_t x = s.groups < kGroupsX ? s.groups : kGroupsX;
+  return launch2(fn, x, (int)((s.groups + x - 1) / x), 256, 0, stream, args...);
 }
 
 }  // namespace kg
@@ -724,8 +739,7 @@ extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64
   if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
-  int64_t grid;
-  const int rc = row_shape(T, k, H, elem, 16, true, &grid, &s);
+  const int rc = row_shape(T, k, H, elem, 16, true, &s);
   if (rc != KG_OK) return rc;
   if (ldx < H) return KG_ERR_SHAPE;
   if (s.rows == 0 || H == 0) return KG_OK;
@@ -736,13 +750,12 @@ extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64
       ranges_overlap(pos, (size_t)s.rows * 4, Xp, out))
     return KG_ERR_ALIAS;
   auto fn = elem == 2 ? kg_dispatch_kernel<2> : kg_dispatch_kernel<4>;
-  return launch(fn, grid, 256, 0, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Xp);
+  return launch_rows(fn, s, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Xp);
 }
 
 extern "C" int64_t kg_dispatch_fp8_workspace_bytes(int64_t T, int k, int H) {
   RowShape s;
-  int64_t grid;
-  if (row_shape(T, k, H, 2, 32, true, &grid, &s) != KG_OK) return -1;
+  if (row_shape(T, k, H, 2, 32, true, &s) != KG_OK) return -1;
   if (s.rows * ((H + 127) / 128) < kTwoStepScales) return 0;
   return T * padded_blocks(H) * 4 + s.rows * 4;
 }
@@ -751,9 +764,8 @@ extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, i
                                int H, void* Q, float* sa, void* workspace,
                                int64_t workspace_bytes, void* stream) {
   RowShape s;
-  int64_t grid;
   if (workspace_bytes < 0) return KG_ERR_SHAPE;
-  const int rc = row_shape(T, k, H, 2, 32, true, &grid, &s);
+  const int rc = row_shape(T, k, H, 2, 32, true, &s);
   if (rc != KG_OK) return rc;
   if (ldx < H) return KG_ERR_SHAPE;
   if (H % 16 != 0) return KG_ERR_ALIGN;
@@ -773,7 +785,7 @@ extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, i
       if (r[j].written && ranges_overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return KG_ERR_ALIAS;
   float* token_sa = two ? (float*)workspace : nullptr;
   int32_t* slot_of = two ? (int32_t*)(token_sa + T * padded_blocks(H)) : nullptr;
-  const int e = launch(kg_dispatch_fp8_kernel, grid, 256, 0, stream, (const unsigned char*)X, ldx,
+  const int e = launch_rows(kg_dispatch_fp8_kernel, s, stream, (const unsigned char*)X, ldx,
                        pos, s, (unsigned char*)Q, sa, token_sa, slot_of);
   if (e != KG_OK || !two) return e;
   const int groups = ((H + 127) / 128 + kRowBlocks - 1) / kRowBlocks;
@@ -786,8 +798,7 @@ extern "C" int kg_combine(const void* Y, const int32_t* pos, const float* w, voi
   if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
-  int64_t grid;
-  const int rc = row_shape(T, k, H, elem, 16, true, &grid, &s);
+  const int rc = row_shape(T, k, H, elem, 16, true, &s);
   if (rc != KG_OK) return rc;
   if (ldo < H) return KG_ERR_SHAPE;
   if (T == 0 || H == 0) return KG_OK;
@@ -800,7 +811,7 @@ extern "C" int kg_combine(const void* Y, const int32_t* pos, const float* w, voi
       ranges_overlap(w, (size_t)s.rows * 4, out, no))
     return KG_ERR_ALIAS;
   auto fn = elem == 2 ? kg_combine_kernel<true> : kg_combine_kernel<false>;
-  return launch(fn, grid, 256, 0, stream, (const unsigned char*)Y, pos, w, s,
+  return launch_rows(fn, s, stream, (const unsigned char*)Y, pos, w, s,
                 (unsigned char*)out, ldo);
 }
 
@@ -810,8 +821,7 @@ extern "C" int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, cons
   if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
-  int64_t grid;
-  const int rc = row_shape(T, k, H, elem, 16, false, &grid, &s);
+  const int rc = row_shape(T, k, H, elem, 16, false, &s);
   if (rc != KG_OK) return rc;
   if (ldo < H) return KG_ERR_SHAPE;
   if (s.rows == 0) return KG_OK;
@@ -829,6 +839,6 @@ extern "C" int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, cons
       return KG_ERR_ALIAS;
   if (ranges_overlap(dY, ny, dw, np)) return KG_ERR_ALIAS;
   auto fn = elem == 2 ? kg_combine_bwd_kernel<true> : kg_combine_bwd_kernel<false>;
-  return launch(fn, grid, 256, 0, stream, (const unsigned char*)dOut, ldo, (const unsigned char*)Y, pos,
+  return launch_rows(fn, s, stream, (const unsigned char*)dOut, ldo, (const unsigned char*)Y, pos,
                 w, s, (unsigned char*)dY, dw);
 }

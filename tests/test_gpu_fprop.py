@@ -212,6 +212,24 @@ def test_rows_and_weights_past_32_bit_offsets():
             check(D[r], A[r], sa[:, r], W[-1:], sw[-1:], last, flags)
 
 
+def test_many_outputs_of_few_rows():
+    """2^24 outputs of 40 experts with a row each: more workgroups than the streaming kernel's
+    launch would hold."""
+    G, N, K = 40, 1 << 24, 16
+    W = torch.randint(0, 0x40, (G, N, K), dtype=torch.uint8, device=DEV)
+    A = torch.randint(0, 0x40, (G, K), dtype=torch.uint8, device=DEV)
+    sa, sw = torch.rand((1, G), device=DEV), torch.rand((G, N // 128, 1), device=DEV)
+    m = torch.ones(G, dtype=torch.int32, device=DEV)
+    D = torch.full((G, N), float("nan"), dtype=BF16, device=DEV)
+    kg.kg_fprop(A, sa, W, sw, D, m, FAST)
+    assert kg.kg_status() == kg.KG_OK
+    for g in (0, 17, 39):
+        n = slice(N - 4096, N)
+        check(D[g:g + 1, n], A[g:g + 1], sa[:, g:g + 1], W[g:g + 1, n], sw[g:g + 1, -32:],
+              torch.ones(1, dtype=torch.int32), FAST)
+    assert torch.isfinite(D.float().sum())
+
+
 def test_other_stream_and_graph():
     A, sa, W, sw, m = make([200, 0, 150], 200, 512, 9)
     A = A.contiguous()

@@ -368,3 +368,18 @@ def test_tensors_made_for_a_stream():
         side.synchronize()
         assert np.array_equal(pos.cpu().numpy(), want[1]) and np.array_equal(src.cpu().numpy(), want[2])
         assert torch.equal(out, (X.float() * k).to(BF16))
+
+
+def test_more_workgroups_than_a_line_holds():
+    """300 million tokens of one slot: the launches need over 2^24 workgroups."""
+    T, H = 300_000_000, 8
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV).view(T, 1)
+    X = (torch.arange(T * H, device=DEV) & 0xFF).to(BF16).view(T, H)
+    Xp = kg.kg_dispatch(X, pos)
+    assert torch.equal(Xp.view(torch.int32), X.flip(0).view(torch.int32))
+    out = kg.kg_combine(Xp, pos)
+    assert torch.equal(out.view(torch.int32), X.view(torch.int32))
+    dY, dw = kg.kg_combine_bwd(X, Xp, pos)
+    assert torch.equal(dY.view(torch.int32), Xp.view(torch.int32))
+    want = X.float().square().sum(1)
+    assert torch.equal(dw.view(-1), want)  # whole numbers below 2^24

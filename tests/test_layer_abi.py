@@ -251,6 +251,7 @@ def adamw(tab=FAKE[0], count=1, items=1, kinds=0, lr=1e-3, b1=0.9, b2=0.99, eps=
     (dict(gscale=FAKE[1] + 2), B.KG_ERR_ALIGN),
     (dict(dyn=FAKE[1] + 1), B.KG_ERR_ALIGN),
     (dict(items=1 << 31), B.KG_ERR_UNSUPPORTED),
+    (dict(items=1 << 24), B.KG_ERR_UNSUPPORTED),
     (dict(count=0, items=0, tab=None), B.KG_OK),
     (dict(items=0), B.KG_OK),
 ])
