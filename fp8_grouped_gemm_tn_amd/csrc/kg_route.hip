@@ -228,8 +228,8 @@ struct RowShape {
   int64_t T;
   int64_t rows;  // T * k
   int k, H;
-  int lanes;   // threads per token: a power of two up to the workgroup's 256
-  int slices;  // workgroups per token (the kernels that take one unit per thread)
+  int lanes;  // threads of a run: a power of two up to the workgroup's 256
+  int runs;   // runs of `lanes` units per token (the kernels that take one unit per thread)
   int64_t groups;  // workgroups that have work
 };
 
@@ -291,7 +291,9 @@ __device__ __forceinline__ void store16(unsigned char* p, const v4i& x) { *(v4i_
 // ... past the caches, for what is read or written once. (16384 tokens of 8 slots, 7168
 // channels, inputs not in the caches: bf16 rows 412 us, 5.1 TB/s, with a run of tokens per
 // XCD, 435 without; fp8 rows 248 us, 4.9 TB/s; sums of k rows 369 us, 5.7 TB/s,
-// 408 with outputs through the caches; gradients 782 us, 5.1 TB/s.)
+// 408 with outputs through the caches; gradients 782 us, 5.1 TB/s. Rows that start inside a
+// line gain less: 2951 channels 160 us past the caches and 165 through them, 1122 channels
+// 373 and 361.)
 __device__ __forceinline__ v4i load16_once(const unsigned char* p) {
   return __builtin_nontemporal_load((const v4i_any*)p);
 }
@@ -306,23 +308,32 @@ __device__ __forceinline__ int64_t named_row(int at, int64_t rows) {
   return r < rows ? r : -1;
 }
 
-// This thread's token and 16-byte unit: a workgroup holds 256 / lanes tokens, or, with all 256
-// threads on one token, one of its `slices` runs of 256 units (and the token is the same for
-// the whole workgroup, so its k positions come through scalar loads). Workgroups go to the 8
-// XCDs in turn; BY_XCD gives each XCD a run of tokens instead.
+// This thread's token and unit of its row. A workgroup holds 256 / lanes runs of `lanes` units,
+// a token `runs` of them; with 64 lanes or more the token is the same for a whole wave, and its k
+// positions come through scalar loads. Workgroups go to the 8 XCDs in turn; BY_XCD gives each
+// XCD a run of tokens instead.
 template <bool BY_XCD = false>
 __device__ __forceinline__ bool my_unit(const RowShape& s, int64_t* t, int* c) {
-  const int64_t b = group_id();
-  if (s.lanes == 256) {
-    const int64_t per = s.groups / 8;
-    const int64_t id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
-    *t = id / s.slices;
-    *c = (int)(id - *t * s.slices) * 256 + threadIdx.x;
-  } else {
-    *t = b * (256 / s.lanes) + threadIdx.x / s.lanes;
-    *c = threadIdx.x & (s.lanes - 1);
-  }
-  return *t < s.T;
+  const int64_t b = group_id(), per = s.groups / 8;
+  const int64_t id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
+  int sub = threadIdx.x / s.lanes;
+  if (s.lanes >= 64) sub = uniform(sub);
+  const int64_t q = id * (256 / s.lanes) + sub;
+  // (T * runs stays below 2^32 where runs > 1: a run is 64 units or more)
+  const int64_t tok = s.runs == 1 ? q : (uint32_t)q / (uint32_t)s.runs;
+  *t = tok;
+  *c = (int)(q - tok * s.runs) * s.lanes + (threadIdx.x & (s.lanes - 1));
+  return tok < s.T;
+}
+
+// Byte offset of 16-byte unit c of a row of `bytes` >= 16: the last unit ends with the row, so
+// where the row is no whole number of units it overlaps the one before and writes the same values
+// there. (Rows of 1122 bf16 channels, 40482 tokens of 8 slots, copied and summed: 473 us with a
+// last unit in elements, 374 with this one; rows of 318, 19888 tokens of 4 slots, gradients
+// 106 / 52.)
+__device__ __forceinline__ int64_t unit_at(int c, int64_t bytes) {
+  const int64_t o = 16 * (int64_t)c;
+  return o < bytes - 16 ? o : bytes - 16;
 }
 
 // Slots j0 .. j0 + 7 of token t (none past its k).
@@ -347,30 +358,29 @@ __global__ __launch_bounds__(256) void kg_dispatch_kernel(const unsigned char* _
   int c;
   if (!my_unit<true>(s, &t, &c)) return;
   const int64_t bytes = (int64_t)s.H * ELEM;
-  const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / ELEM;
+  if (16 * (int64_t)c >= bytes) return;
   const unsigned char* x = X + t * ldx * ELEM;
-  if (c < chunks) {
-    const v4i v = load16(x + 16 * (int64_t)c);
+  if (bytes >= 16) {
+    const int64_t o = unit_at(c, bytes);
+    const v4i v = load16(x + o);
     for (int j0 = 0; j0 < s.k; j0 += 8) {
       const Slots p(pos, s, t, j0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t r = named_row(p.at[i], s.rows);
-        if (r >= 0) store16_once(Xp + r * bytes + 16 * (int64_t)c, p.at[i] < 0 ? v4i{0, 0, 0, 0} : v);
+        if (r >= 0) store16_once(Xp + r * bytes + o, p.at[i] < 0 ? v4i{0, 0, 0, 0} : v);
       }
     }
-  }
-  if (c == chunks) {  // the row's last elements
+  } else {
     for (int j = 0; j < s.k; ++j) {
       const int at = pos[t * s.k + j];
       const int64_t r = named_row(at, s.rows);
       if (r < 0) continue;
-      for (int e = 0; e < tail; ++e) {
-        const int64_t o = 16 * (int64_t)chunks + e * ELEM;
+      for (int e = 0; e < s.H; ++e) {
         if constexpr (ELEM == 2)
-          *(unsigned short*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const unsigned short*)(x + o);
+          ((unsigned short*)Xp)[r * s.H + e] = at < 0 ? 0 : ((const unsigned short*)x)[e];
         else
-          *(uint32_t*)(Xp + r * bytes + o) = at < 0 ? 0 : *(const uint32_t*)(x + o);
+          ((uint32_t*)Xp)[r * s.H + e] = at < 0 ? 0 : ((const uint32_t*)x)[e];
       }
     }
   }
@@ -492,10 +502,11 @@ __global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* __
   int c;
   if (!my_unit(s, &t, &c)) return;
   const int64_t bytes = (int64_t)s.H * V::ELEM;
-  const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / V::ELEM;
+  if (16 * (int64_t)c >= bytes) return;
   const float* wt = w == nullptr ? nullptr : w + t * s.k;
-  unsigned char* o = out + t * ldo * V::ELEM;
-  if (c < chunks) {
+  unsigned char* to = out + t * ldo * V::ELEM;
+  if (bytes >= 16) {
+    const int64_t o = unit_at(c, bytes);
     float acc[V::N] = {};
     for (int j0 = 0; j0 < s.k; j0 += 8) {
       const Slots p(pos, s, t, j0);
@@ -505,7 +516,7 @@ __global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* __
       for (int i = 0; i < 8; ++i) {
         wj[i] = 1.0f;
         if (p.at[i] >= 0 && p.at[i] < s.rows) {
-          y[i] = load16_once(Y + p.at[i] * bytes + 16 * (int64_t)c);
+          y[i] = load16_once(Y + p.at[i] * bytes + o);
           if (wt != nullptr) wj[i] = wt[j0 + i];
         }
       }
@@ -518,18 +529,16 @@ __global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* __
         for (int e = 0; e < V::N; ++e) acc[e] = fmaf(wj[i], f[e], acc[e]);
       }
     }
-    store16_once(o + 16 * (int64_t)c, V::pack(acc));
-  }
-  if (c == chunks) {  // the row's last elements
-    for (int e = 0; e < tail; ++e) {
-      const int64_t b = 16 * (int64_t)chunks + e * V::ELEM;
+    store16_once(to + o, V::pack(acc));
+  } else {
+    for (int e = 0; e < s.H; ++e) {
       float acc = 0.f;
       for (int j = 0; j < s.k; ++j) {
         const int at = pos[t * s.k + j];
         if (at >= 0 && at < s.rows)
-          acc = fmaf(wt == nullptr ? 1.0f : wt[j], V::load1(Y + at * bytes + b), acc);
+          acc = fmaf(wt == nullptr ? 1.0f : wt[j], V::load1(Y + at * bytes + e * V::ELEM), acc);
       }
-      V::store1(o + b, acc);
+      V::store1(to + e * V::ELEM, acc);
     }
   }
 }
@@ -549,7 +558,7 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
   const bool live = t0 < s.T;  // a workgroup of a token's 256 threads is live as a whole
   const int64_t t = live ? t0 : 0;
   const int64_t bytes = (int64_t)s.H * V::ELEM;
-  const int chunks = (int)(bytes >> 4), tail = (int)(bytes & 15) / V::ELEM;
+  const int units = (int)((bytes + 15) >> 4);
   const unsigned char* d = dOut + t * ldo * V::ELEM;
   const int32_t* p = pos + t * s.k;
   for (int j0 = 0; j0 < s.k; j0 += 8) {
@@ -564,15 +573,18 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
         if (w != nullptr) wj[i] = w[t * s.k + j0 + i];
       }
     }
-    if (live) {
-      for (int c = lane; c < chunks; c += s.lanes) {
+    if (live && bytes >= 16) {
+      for (int c = lane; c < units; c += s.lanes) {
+        const int64_t o = unit_at(c, bytes);
+        // elements that the unit before has counted
+        const int seen = (int)(16 * (int64_t)c - o) / V::ELEM;
         float g[V::N];
-        V::unpack(load16(d + 16 * (int64_t)c), g);
+        V::unpack(load16(d + o), g);
         v4i y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (dw != nullptr && j0 + i < s.k && at[i] >= 0 && at[i] < s.rows)
-            y[i] = load16_once(Y + at[i] * bytes + 16 * (int64_t)c);
+            y[i] = load16_once(Y + at[i] * bytes + o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (j0 + i >= s.k) continue;
@@ -580,21 +592,23 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
           if (r < 0) continue;
           float f[V::N];
           if (at[i] < 0) {
-            store16(dY + r * bytes + 16 * (int64_t)c, v4i{0, 0, 0, 0});
+            store16(dY + r * bytes + o, v4i{0, 0, 0, 0});
             continue;
           }
 #pragma unroll
           for (int e = 0; e < V::N; ++e) f[e] = wj[i] * g[e];
-          store16_once(dY + r * bytes + 16 * (int64_t)c, V::pack(f));
+          store16_once(dY + r * bytes + o, V::pack(f));
           if (dw != nullptr) {
             V::unpack(y[i], f);
 #pragma unroll
-            for (int e = 0; e < V::N; ++e) dot[i] = fmaf(g[e], f[e], dot[i]);
+            for (int e = 0; e < V::N; ++e)
+              if (e >= seen) dot[i] = fmaf(g[e], f[e], dot[i]);
           }
         }
       }
-      if (lane < tail) {
-        const int64_t b = 16 * (int64_t)chunks + lane * V::ELEM;
+    } else if (live && lane == 0) {
+      for (int e = 0; e < s.H; ++e) {
+        const int64_t b = e * V::ELEM;
         const float g = V::load1(d + b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -655,9 +669,11 @@ static int64_t route_block(int64_t n) {
 }
 static int64_t route_blocks(int64_t n) { return (n + route_block(n) - 1) / route_block(n); }
 
-// Checks that the row kernels share, and their launch shape: threads per token are the
-// power of two (16 to 256) that covers the row's units (of `unit` bytes, the last one
-// partial); past 256 units a token takes several workgroups if `split`, else a loop.
+// Checks that the row kernels share, and their launch shape. A token's row is cut into units of
+// `unit` bytes (the last one partial). `split`: runs of `lanes` units (16 to 256, a power of two,
+// the largest of those that leave the fewest threads without a unit), one unit per thread.
+// Else one run of threads loops over the token's units: as many as leave few idle in the last
+// turn, and at least 64 where there are that many units.
 static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, RowShape* s) {
   if (T < 0 || k < 0 || H < 0) return KG_ERR_SHAPE;
   if (H > (1 << 24) || k > 4096 || (k > 0 && T > (int64_t)(INT32_MAX - 1) / k) || T > INT32_MAX - 1)
@@ -667,12 +683,21 @@ static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, Ro
   s->k = k;
   s->H = H;
   const int64_t units = ((int64_t)H * elem + unit - 1) / unit;
-  s->lanes = 16;
-  while (s->lanes < 256 && s->lanes < units) s->lanes *= 2;
-  s->slices = split && units > 256 ? (int)((units + 255) / 256) : 1;
+  s->lanes = 256;
+  int64_t least = INT64_MAX;
+  for (int lanes = 256; lanes >= (units >= 64 ? 64 : 16); lanes /= 2) {
+    const int64_t threads = (units + lanes - 1) / lanes * lanes;
+    if (threads < least) {
+      least = threads;
+      s->lanes = lanes;
+    }
+  }
+  s->runs = split && units > 0 ? (int)((units + s->lanes - 1) / s->lanes) : 1;
   const int per = 256 / s->lanes;
-  s->groups = (T + per - 1) / per * s->slices;
-  return s->groups <= kGroupsX * 65535 ? KG_OK : KG_ERR_UNSUPPORTED;
+  s->groups = (T * s->runs + per - 1) / per;
+  return s->groups <= kGroupsX * 65535 && (s->runs == 1 || T * s->runs < ((int64_t)1 << 32) - 256)
+             ? KG_OK
+             : KG_ERR_UNSUPPORTED;
 }
 
 // A row kernel on s.groups workgroups (those past them in the last line have no token).
