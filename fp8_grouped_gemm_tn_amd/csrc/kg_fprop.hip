@@ -138,9 +138,17 @@ __device__ __forceinline__ void store_run(void* D, int64_t at, int left, const v
 // BT tokens x BN outputs per workgroup of 8 waves (WT along the tokens, PER_CU such
 // workgroups per compute unit), two stages of one
 // 128-channel block in LDS: BN rows of W, BT rows of A, the BT token scales.
-template <int BT_, int BN_, int WT_, int PER_CU_>
+// With ROTATE each tile begins at a block of its own and goes round: tiles that run side by side
+// would else all read the same channels of W's rows, and where the rows lie a multiple of 4096
+// bytes apart those are in few of the memory channels. (32 experts, 8 rows each, N 4096, K 4096:
+// 155 -> 93 us; 64 experts of 4 rows, N 1024, K 4096: 62 -> 46.) It is for such rows only: else
+// nothing is gained (K 3584 and 7168 within 1%), and where latency counts the extra
+// instructions cost (256 tokens of one expert, K 7168: 26.4 -> 28.9 us), and for few tokens:
+// tiles of other outputs no longer read the tokens' blocks at the same time.
+template <int BT_, int BN_, int WT_, int PER_CU_, bool ROTATE_ = false>
 struct FCfg {
   static constexpr int PER_CU = PER_CU_;  // workgroups per compute unit
+  static constexpr bool ROTATE = ROTATE_;
   static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = 8 / WT_, THREADS = 512, TK = 128;
   static constexpr int TT = BT / WT / 16;  // 16-token tiles of a wave
   static constexpr int NI = BN / WN / 16;  // 16-output tiles of a wave
@@ -181,17 +189,18 @@ struct FLoads {
   const float* sa;
   int64_t M_total;
   int K, lda, nk, outs, rows, wave;
+  int first;  // the block that the tile begins with
   uint32_t offw, offt, offs, lds;
   bool endw, endt;  // this lane's chunk lies past the last block's channels
   __device__ __forceinline__ void setup(const FParams& p, const unsigned char* smem, int64_t row0,
-                                        int rows_, int g, int n0, int nk_) {
+                                        int rows_, int g, int n0, int nk_, int first_) {
     wave = uniform(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     W = p.W + ((int64_t)g * p.N + n0) * p.K;
     A = p.A + row0 * p.lda;
     sa = p.sa + row0;
     M_total = p.M_total;
-    K = p.K, lda = (int)p.lda, nk = nk_;
+    K = p.K, lda = (int)p.lda, nk = nk_, first = first_;
     outs = min(C::BN, p.N - n0), rows = rows_;
     const int r = 8 * wave + (lane >> 3);
     const int cw = (lane & 7) ^ key_w(r), ct = (lane & 7) ^ key_t(r);
@@ -207,20 +216,28 @@ struct FLoads {
     lds = lds_addr(smem);
   }
   __device__ __forceinline__ int channels(int kb) const { return min(C::TK, K - kb * C::TK); }
+  // The block that the tile takes as its kb-th.
+  __device__ __forceinline__ int block(int kb) const {
+    if constexpr (!C::ROTATE) return kb;
+    const int k = kb + first;
+    return k >= nk ? k - nk : k;
+  }
   __device__ __forceinline__ void load(int kw, int kt, int x) const {
     if (x < C::LW) {
-      const v4i r = make_rsrc(W + (int64_t)kw * C::TK,
-                              kw < nk ? (uint32_t)((outs - 1) * K + channels(kw)) : 0u);
+      const int k = block(kw);
+      const v4i r = make_rsrc(W + (int64_t)k * C::TK,
+                              kw < nk ? (uint32_t)((outs - 1) * K + channels(k)) : 0u);
       load16_lds(r, lds + (kw & 1) * C::STAGE + 1024 * (wave + 8 * x),
-                 (offw + (uint32_t)(64 * x * K)) | (kw == nk - 1 && endw ? kOobOffset : 0u));
+                 (offw + (uint32_t)(64 * x * K)) | (k == nk - 1 && endw ? kOobOffset : 0u));
     } else if (x < C::LW + C::LT) {
-      const int y = x - C::LW;
-      const v4i r = make_rsrc(A + (int64_t)kt * C::TK,
-                              kt < nk ? (uint32_t)((rows - 1) * lda + channels(kt)) : 0u);
+      const int y = x - C::LW, k = block(kt);
+      const v4i r = make_rsrc(A + (int64_t)k * C::TK,
+                              kt < nk ? (uint32_t)((rows - 1) * lda + channels(k)) : 0u);
       load16_lds(r, lds + (kt & 1) * C::STAGE + C::OPW + 1024 * (wave + 8 * y),
-                 (offt + (uint32_t)(64 * y * lda)) | (kt == nk - 1 && endt ? kOobOffset : 0u));
+                 (offt + (uint32_t)(64 * y * lda)) | (k == nk - 1 && endt ? kOobOffset : 0u));
     } else {
-      const v4i r = make_rsrc(sa + (int64_t)kt * M_total, kt < nk ? (uint32_t)(rows * 4) : 0u);
+      const v4i r =
+          make_rsrc(sa + (int64_t)block(kt) * M_total, kt < nk ? (uint32_t)(rows * 4) : 0u);
       load4_lds(r, lds + (kt & 1) * C::STAGE + C::SA_OFF + 256 * (wave % (C::BT / 64)), offs);
     }
   }
@@ -370,7 +387,7 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 #pragma unroll
       for (int tt = 0; tt < C::TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
     FLoads<C> L;
-    L.setup(p, smem, row0, rows, g, n0, nk);
+    L.setup(p, smem, row0, rows, g, n0, nk, C::ROTATE && nk > 0 ? (nt + 5 * g) % nk : 0);
     Frag<FAST> tf[C::TT], wf[2];
     float sc[C::TT];
     auto read_t = [&](int kb, int tt) {
@@ -387,7 +404,7 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
       // (behind the previous tile's last meeting, so every wave is done with its stages; its
       // stores may be under way, and so may its last loads, which read nothing: a wave's
       // operations end in order, and a place in LDS is always loaded by the same wave)
-      swv = swg[0];
+      swv = swg[L.block(0)];
 #pragma unroll
       for (int x = C::LW; x < C::LOADS; ++x) L.load(0, 0, x);
 #pragma unroll
@@ -430,7 +447,7 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 #pragma unroll
         for (int x = 0; x < C::LW; ++x)
           if (S - C::TT + x * C::TT / C::LW == u) L.load(kb + 2, 0, x);
-        if (u == S / 2) swv = swg[min(kb + 1, nk - 1)];
+        if (u == S / 2) swv = swg[L.block(min(kb + 1, nk - 1))];
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -665,13 +682,16 @@ struct FTile {
 
 // Which kernel and tile. The experts' sizes are known on the device only, so this goes by
 // M_total and G; every choice is right for every distribution of the rows.
-//  * Streaming up to 8 rows per expert on average, and up to 64 while M_total * N <= 2^19
-//    (few rows in all: a tile's time is then the latency of its blocks). K = 7168,
-//    N = 4096, streaming / 128 x 128 tiles: 32 experts of 2, 8, 16 rows 127/153, 164/167,
-//    231/170 us; 4 experts of 16, 32, 64 rows 27/41, 37/41, 71/42; 1 of 16, 64, 128 rows
-//    13/39, 23/39, 42/40. TT token tiles hold an expert's rows: the average, or twice it
-//    where several experts share M_total unevenly (4 experts of 16 rows, TT 1, 2, 4: 30,
-//    27, 32 us).
+//  * Streaming where it takes few workgroups and passes, 3 per compute unit (a tile's time is
+//    then the latency of its blocks): streaming / 64 x 128 tiles with K 7168, N 4096: 1, 16, 64
+//    rows of one expert 12 / 42, 14 / 25, 24 / 25 us; 4 experts of 2 and 16 rows 20 / 26 and
+//    30 / 26, 8 of 2 rows 40 / 39; 4 of 4 rows, N 7168, K 2048 16 / 12. TT token tiles hold an
+//    expert's rows: the average, or twice it where several experts share M_total unevenly
+//    (4 experts of 16 rows, TT 1, 2, 4: 30, 27, 32 us).
+//  * Streaming as well for the fewest rows of long weight rows. 32 experts, N 4096, streaming /
+//    64 x 128 tiles, K 2048, 3584, 7168: fp8 MFMA, 1 row each 37 / 37, 50 / 52, 105 / 127 us, 2 rows
+//    50 / 45, 76 / 74, 131 / 141, 4 rows 57 / 47, 87 / 77, 164 / 155; exact, 1 row 51 / 46, 83 / 78,
+//    120 / 145, 2 rows 70 / 51, 96 / 79, 179 / 157. 256 experts of 1 row, N 2048, K 512: 101 / 35.
 //  * Else the tile with the least estimated time, rounds over the compute units times a
 //    block's time. The number of 16-byte operand reads per MFMA falls with the tile's size,
 //    the latency of a block and the rows that an expert's last tile leaves empty rise.
@@ -683,28 +703,34 @@ struct FTile {
 //    247 / 207 and 312 / 246 / 268 / 226; 32768 rows of 8 experts, K 7168 1.69 ms with
 //    128 x 256 (256 x 256, whose widened fragments spill, 1.70). Two 128 x 128 workgroups
 //    per compute unit spill too (61 -> 110 us on the 256 rows).
-static FLaunch f_choose(int64_t M, int G, int N, int cus, bool fast, bool outb) {
+static FLaunch f_choose(int64_t M, int G, int N, int K, int cus, bool fast, bool outb) {
   const int64_t avg = (M + G - 1) / G, live = G < M ? G : M;
-  const bool fits = live * ((N + kStreamN - 1) / kStreamN) < (1 << 23);  // 2^32 threads
-  if (fits && (avg <= 8 || (avg <= 64 && M * N <= (1 << 19)))) {
-    const int64_t rows = G == 1 ? avg : 2 * avg;
+  const int64_t groups = live * ((N + kStreamN - 1) / kStreamN), rows = G == 1 ? avg : 2 * avg;
+  if ((avg <= 64 && groups * ((rows + 15) / 16) <= 3 * cus) ||
+      (groups < (1 << 23) && M <= (fast ? 2 : 1) * (int64_t)G && K > 4096)) {
     return rows <= 16 ? f_stream<1>(fast, outb) : rows <= 32 ? f_stream<2>(fast, outb)
                                                              : f_stream<4>(fast, outb);
   }
   using Tile64 = FCfg<64, 64, 4, 2>;
   using Tile64x128 = FCfg<64, 128, 2, 2>;
+  using Tile64x128R = FCfg<64, 128, 2, 2, true>;
+  // (more tiles than compute units: 8 experts of 16 rows, N 2048, without / with: fp8 15 / 18 us,
+  // exact 21 / 27)
+  const bool rotate =
+      K % 4096 == 0 && live > 1 && avg <= 64 && live * ((N + 127) / 128) > cus;
   const FTile tiles[4] = {
       {fast ? f_tiled<FCfg<256, 256, 4, 1>, true>(outb, 0)
-            : f_tiled<FCfg<128, 256, 2, 1>, false>(outb, 4), fast ? 15 : 18, fast ? 15 : 18},
-      {fast ? f_tiled<FCfg<128, 128, 4, 2>, true>(outb, 1)
-            : f_tiled<FCfg<128, 128, 4, 1>, false>(outb, 5), fast ? 7 : 12, 12},
-      {fast ? f_tiled<Tile64x128, true>(outb, 2) : f_tiled<Tile64x128, false>(outb, 6),
+            : f_tiled<FCfg<128, 256, 2, 1>, false>(outb, 1), fast ? 15 : 18, fast ? 15 : 18},
+      {fast ? f_tiled<FCfg<128, 128, 4, 2>, true>(outb, 2)
+            : f_tiled<FCfg<128, 128, 4, 1>, false>(outb, 3), fast ? 7 : 12, 12},
+      {rotate ? (fast ? f_tiled<Tile64x128R, true>(outb, 4) : f_tiled<Tile64x128R, false>(outb, 5))
+              : (fast ? f_tiled<Tile64x128, true>(outb, 6) : f_tiled<Tile64x128, false>(outb, 7)),
        fast ? 5 : 8, fast ? 10 : 15},
-      {fast ? f_tiled<Tile64, true>(outb, 3) : f_tiled<Tile64, false>(outb, 7), fast ? 4 : 6,
+      {fast ? f_tiled<Tile64, true>(outb, 8) : f_tiled<Tile64, false>(outb, 9), fast ? 4 : 6,
        fast ? 8 : 9}};
-  int best = 0;
+  int best = rotate ? 2 : 0;
   int64_t least = INT64_MAX;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4 && !rotate; ++i) {
     const FLaunch& l = tiles[i].l;
     // tiles along the rows, in tenths: one expert's are known; of several, each has a last
     // one that is filled to some part
@@ -769,7 +795,7 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
   p.G = G;
   p.N = N;
   p.K = K;
-  FLaunch l = f_choose(M_total, G, N, cus, fast, outb);
+  FLaunch l = f_choose(M_total, G, N, K, cus, fast, outb);
   p.tiles_n = (N + l.bn - 1) / l.bn;
   int64_t grid;
   if (l.id < 0) {
@@ -777,7 +803,7 @@ extern "C" int kg_fprop(const void* A, int64_t lda, const float* sa, const void*
   } else {
     l.lds += 2 * (G + 1) * 4;
     static std::mutex mu;
-    static int set[64][8][2];  // the largest LDS size asked for so far
+    static int set[64][10][2];  // the largest LDS size asked for so far
     {
       std::lock_guard<std::mutex> lk(mu);
       if (set[dev][l.id][outb] < l.lds) {

@@ -259,3 +259,12 @@ def test_other_stream_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(D, want) and torch.equal(Ds, want_s)
     check(D, A, sa, W, sw, m, FAST)
+
+
+@pytest.mark.parametrize("G,N,K,avg", [(140, 130, 4096, 2), (140, 130, 4096, 40), (129, 257, 8192, 3)])
+@pytest.mark.parametrize("dt,flags", [(BF16, 0), (F32, FAST)])
+def test_rows_a_multiple_of_4096_bytes_apart(G, N, K, avg, dt, flags):
+    """Many experts with few rows: a tile's blocks are added from a start of its own, round the end."""
+    rng = np.random.default_rng(G + K)
+    ms = rng.poisson(avg * rng.dirichlet(np.ones(G)) * G).tolist()
+    run(ms, N, K, dt, flags, seed=avg)
