@@ -333,8 +333,8 @@ __device__ __forceinline__ bool f_offsets(const int32_t* ms, int G, int bt, int6
 // On 32768 tokens of 8 experts, K 7168, N 4096 (fp8 MFMA, bf16 out, 256 x 256): 1480 us with
 // a burst of loads, a vector load of the weight scale and no fragments ahead; 1110 with the
 // scale through a scalar load and four waves loading; 870 with fragments ahead and counted
-// waits, 847 without LDS conflicts and with spread loads. 1.64 M cycles, MFMA busy for
-// 0.95 M of them, at 1.75 GHz, to which the clock falls under this load: without the loads
+// waits, 847 without LDS conflicts and with spread loads (now 812 to 848 by card). 1.61 M cycles,
+// MFMA busy for 0.95 M of them, at 1.77 GHz, to which the clock falls under this load: without the loads
 // 1.50 M cycles at 1.92 GHz, without the meetings as well 1.32 M. Tried without gain: the
 // next tile's first loads before this one's stores (877), loads into the L2 two to four
 // blocks ahead (912), 32 x 32 MFMAs (924), raised wave priority (873), the last round's
