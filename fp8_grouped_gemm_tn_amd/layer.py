@@ -14,26 +14,31 @@ from ._binding import (KG_ADAMW_8BIT, KG_ADAMW_G_BF16, KG_ADAMW_P_BF16, KG_ERR_S
                        KG_FLAG_D_BF16, KG_OK, KG_ROWS_BF16, KG_ROWS_F32, KgError, _need, lib)
 
 torch = None  # imported with the first call, as the library itself is loaded
+_lib = None
 _f32 = _bf16 = _int32 = None
+_row_types = {}
+_current_gpu = _current_stream = None
 
 
 def _load():
-    """The loaded library, and torch with what the calls read of it."""
-    global torch, _f32, _bf16, _int32
-    if torch is None:
+    """The loaded library; sets what the calls read of torch."""
+    global torch, _lib, _f32, _bf16, _int32, _row_types, _current_gpu, _current_stream
+    if _lib is None:
         import torch as t
+        L = lib()
         _f32, _bf16, _int32 = t.float32, t.bfloat16, t.int32
-        torch = t
-    return lib()
+        _row_types = {t.bfloat16: KG_ROWS_BF16, t.float32: KG_ROWS_F32}
+        _current_gpu, _current_stream = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream
+        torch, _lib = t, L
+    return _lib
 
 
-def _on(ref, stream):
+def _on(gpu, stream):
     """hipStream_t: `stream`'s, or the current one. The call goes to the current GPU, so that
-    has to be `ref`'s."""
-    d = ref.device.index
-    if d != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on GPU {d}, which is not the current one")
-    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+    has to be `gpu`."""
+    if gpu != _current_gpu():
+        raise ValueError(f"the tensors are on GPU {gpu}, which is not the current one")
+    return _current_stream(gpu) if stream is None else stream.cuda_stream
 
 
 def _made(shape, dtype, ref, stream):
@@ -53,13 +58,14 @@ def _at(t):
 
 
 def _gpu(ref, *others):
-    """Every given tensor is on `ref`'s GPU."""
-    if not ref.is_cuda:
+    """The GPU that `ref` and every given tensor are on."""
+    gpu = ref.get_device()
+    if gpu < 0:
         raise ValueError("the tensors must be on a GPU")
-    d = ref.device
     for t in others:
-        if t is not None and t.device != d:
-            raise ValueError(f"a tensor is on {t.device}, another on {d}")
+        if t is not None and t.get_device() != gpu:
+            raise ValueError(f"a tensor is on {t.device}, another on {ref.device}")
+    return gpu
 
 
 def _i32(t, shape, name):
@@ -67,24 +73,24 @@ def _i32(t, shape, name):
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
-def _row_type(t, name):
-    if t.dtype is _bf16:
-        return KG_ROWS_BF16
-    if t.dtype is not _f32:
+def _row_type(dtype, name):
+    ty = _row_types.get(dtype)
+    if ty is None:
         raise ValueError(f"{name} must be bfloat16 or float32")
-    return KG_ROWS_F32
+    return ty
 
 
-def _row_stride(t, name):
-    """Row stride in elements of a 2-D tensor whose rows are contiguous (its width where it
-    has at most one row, or no columns: torch gives those any stride)."""
-    if t.dim() != 2:
+def _rows(t, name):
+    """(rows, columns, row stride in elements) of a 2-D tensor whose rows are contiguous (its
+    width where it has at most one row, or no columns: torch gives those any stride)."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    rows, cols = t.shape
+    rows, cols = shape
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return ld if rows > 1 and cols > 0 else cols
+    return rows, cols, ld if rows > 1 and cols > 0 else cols
 
 
 def new_route_workspace(T, k, G, device):
@@ -109,13 +115,14 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
     """Plan that puts tokens into expert order: idx int32 [T, k] (an entry outside [0, G) is
     dropped), ks int32 [G] (out). pos int32 [T, k] and src int32 [T * k] are written (made if
     not given); ws: new_route_workspace (made if not given and needed). Returns (pos, src)."""
-    L = _load()
-    if idx.dim() != 2 or ks.dim() != 1:
+    L = _lib or _load()
+    shape, experts = idx.shape, ks.shape
+    if len(shape) != 2 or len(experts) != 1:
         raise ValueError("idx must be [T, k] and ks [G]")
-    T, k = shape = idx.shape
-    G = ks.shape[0]
+    T, k = shape
+    G = experts[0]
     _i32(idx, shape, "idx")
-    _i32(ks, ks.shape, "ks")
+    _i32(ks, experts, "ks")
     if pos is None:
         pos = _made(shape, _int32, idx, stream)
     if src is None:
@@ -127,20 +134,21 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
         if n > 0:
             ws = _made((n,), torch.uint8, idx, stream)
     at, size = _workspace(ws)
-    _gpu(idx, ks, pos, src, ws)
+    gpu = _gpu(idx, ks, pos, src, ws)
     rc = L.kg_route(idx.data_ptr(), T, k, G, ks.data_ptr(), pos.data_ptr(), src.data_ptr(), at,
-                    size, _on(idx, stream))
+                    size, _on(gpu, stream))
     if rc:
         _fail(rc, "kg_route")
     return pos, src
 
 
 def _positions(pos, T):
-    """k of pos [T, k]."""
-    if pos.dim() != 2 or pos.shape[0] != T:
-        raise ValueError("pos must be [T, k]")
-    _i32(pos, pos.shape, "pos")
-    return pos.shape[1]
+    """k of the int32 [T, k] tensor pos."""
+    shape = pos.shape
+    if (len(shape) != 2 or shape[0] != T or pos.dtype is not _int32 or
+            not pos.is_contiguous()):
+        raise ValueError(f"pos must be a contiguous int32 [{T}, k] tensor")
+    return shape[1]
 
 
 def _expert_rows(t, shape, dtype, name):
@@ -151,16 +159,16 @@ def _expert_rows(t, shape, dtype, name):
 def kg_dispatch(X, pos, Xp=None, stream=None):
     """X [T, H] (bfloat16 or float32, rows contiguous) copied to Xp [T * k, H] (made if not
     given): every token's row to the rows that pos (kg_route) names, zeros for dropped slots."""
-    L = _load()
-    ty, ldx = _row_type(X, "X"), _row_stride(X, "X")
-    T, H = X.shape
+    L = _lib or _load()
+    dtype = X.dtype
+    ty, (T, H, ldx) = _row_type(dtype, "X"), _rows(X, "X")
     k = _positions(pos, T)
     if Xp is None:
-        Xp = _made((T * k, H), X.dtype, X, stream)
-    _expert_rows(Xp, (T * k, H), X.dtype, "Xp")
-    _gpu(X, pos, Xp)
+        Xp = _made((T * k, H), dtype, X, stream)
+    _expert_rows(Xp, (T * k, H), dtype, "Xp")
+    gpu = _gpu(X, pos, Xp)
     rc = L.kg_dispatch(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, ty, Xp.data_ptr(),
-                       _on(X, stream))
+                       _on(gpu, stream))
     if rc:
         _fail(rc, "kg_dispatch")
     return Xp
@@ -171,11 +179,10 @@ def kg_dispatch_fp8(X, pos, Q=None, sa=None, ws=None, stream=None):
     sa float32 [ceil(H / 128), T * k] as kg_fprop and kg_dgrad read them (made if not given);
     ws: a uint8 workspace of kg_dispatch_fp8_workspace_bytes (made if not given and of use).
     Returns (Q, sa)."""
-    L = _load()
+    L = _lib or _load()
     if X.dtype is not _bf16:
         raise ValueError("X must be bfloat16")
-    ldx = _row_stride(X, "X")
-    T, H = X.shape
+    T, H, ldx = _rows(X, "X")
     k = _positions(pos, T)
     if Q is None:
         Q = _made((T * k, H), torch.uint8, X, stream)
@@ -189,9 +196,9 @@ def kg_dispatch_fp8(X, pos, Q=None, sa=None, ws=None, stream=None):
         if n > 0:
             ws = _made((n,), torch.uint8, X, stream)
     at, size = _workspace(ws)
-    _gpu(X, pos, Q, sa, ws)
+    gpu = _gpu(X, pos, Q, sa, ws)
     rc = L.kg_dispatch_fp8(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, Q.data_ptr(),
-                           sa.data_ptr(), at, size, _on(X, stream))
+                           sa.data_ptr(), at, size, _on(gpu, stream))
     if rc:
         _fail(rc, "kg_dispatch_fp8")
     return Q, sa
@@ -201,24 +208,24 @@ def kg_combine(Y, pos, w=None, out=None, stream=None):
     """out[t] = sum_j w[t][j] Y[pos[t][j]] over the kept slots: Y [T * k, H] (bfloat16 or
     float32), pos int32 [T, k] from kg_route, w float32 [T, k] (None: ones), out [T, H] (rows
     contiguous; made if not given). With w None this is kg_dispatch's gradient."""
-    L = _load()
-    ty = _row_type(Y, "Y")
-    T = pos.shape[0]
+    L = _lib or _load()
+    dtype, shape = Y.dtype, Y.shape
+    ty = _row_type(dtype, "Y")
+    T = pos.shape[0] if pos.dim() else -1
     k = _positions(pos, T)
-    if Y.dim() != 2:
-        raise ValueError("Y must be [T * k, H]")
-    H = Y.shape[1]
-    _expert_rows(Y, (T * k, H), Y.dtype, "Y")
+    if len(shape) != 2 or shape[0] != T * k or not Y.is_contiguous():
+        raise ValueError(f"Y must be a contiguous [{T * k}, H] tensor")
+    H = shape[1]
     if w is not None:
         _expert_rows(w, (T, k), _f32, "w")
     if out is None:
-        out = _made((T, H), Y.dtype, Y, stream)
-    if out.dtype is not Y.dtype or out.shape != (T, H):
+        out = _made((T, H), dtype, Y, stream)
+    rows, cols, ldo = _rows(out, "out")
+    if out.dtype is not dtype or rows != T or cols != H:
         raise ValueError("out must be [T, H] of Y's dtype")
-    ldo = _row_stride(out, "out")
-    _gpu(Y, pos, w, out)
+    gpu = _gpu(Y, pos, w, out)
     rc = L.kg_combine(Y.data_ptr(), pos.data_ptr(), _at(w), out.data_ptr(), ldo, T, k, H, ty,
-                      _on(Y, stream))
+                      _on(gpu, stream))
     if rc:
         _fail(rc, "kg_combine")
     return out
@@ -228,27 +235,27 @@ def kg_combine_bwd(dOut, Y, pos, w=None, dY=None, dw=None, need_dw=True, stream=
     """Gradients of kg_combine: dOut [T, H] (rows contiguous), Y [T * k, H], pos, w as given to
     it. Returns (dY [T * k, H], dw float32 [T, k]); with need_dw False dw is not computed (None)
     and Y is not read (it may be None)."""
-    L = _load()
-    ty, ldo = _row_type(dOut, "dOut"), _row_stride(dOut, "dOut")
-    T, H = dOut.shape
+    L = _lib or _load()
+    dtype = dOut.dtype
+    ty, (T, H, ldo) = _row_type(dtype, "dOut"), _rows(dOut, "dOut")
     k = _positions(pos, T)
     if w is not None:
         _expert_rows(w, (T, k), _f32, "w")
     if dY is None:
-        dY = _made((T * k, H), dOut.dtype, dOut, stream)
-    _expert_rows(dY, (T * k, H), dOut.dtype, "dY")
+        dY = _made((T * k, H), dtype, dOut, stream)
+    _expert_rows(dY, (T * k, H), dtype, "dY")
     if need_dw:
         if Y is None:
             raise ValueError("dw needs Y")
-        _expert_rows(Y, (T * k, H), dOut.dtype, "Y")
+        _expert_rows(Y, (T * k, H), dtype, "Y")
         if dw is None:
             dw = _made((T, k), _f32, dOut, stream)
         _expert_rows(dw, (T, k), _f32, "dw")
     else:
         Y = dw = None
-    _gpu(dOut, Y, pos, w, dY, dw)
+    gpu = _gpu(dOut, Y, pos, w, dY, dw)
     rc = L.kg_combine_bwd(dOut.data_ptr(), ldo, _at(Y), pos.data_ptr(), _at(w), dY.data_ptr(),
-                          _at(dw), T, k, H, ty, _on(dOut, stream))
+                          _at(dw), T, k, H, ty, _on(gpu, stream))
     if rc:
         _fail(rc, "kg_combine_bwd")
     return dY, dw
@@ -258,13 +265,13 @@ def kg_fprop(A, sa, W, sw, D, ms, flags=0, stream=None):
     """D = rows . W^T per expert: A fp8 codes [M_total, K] (rows contiguous), sa float32
     [ceil(K / 128), M_total], W fp8 codes [G, N, K], sw float32 [G, ceil(N / 128),
     ceil(K / 128)], ms int32 [G], D [M_total, N] (float32 or bfloat16, rows contiguous)."""
-    L = _load()
+    L = _lib or _load()
     if W.dim() != 3 or W.element_size() != 1 or not W.is_contiguous():
         raise ValueError("W must be contiguous fp8 codes [G, N, K]")
     G, N, K = W.shape
-    lda, ldd = _row_stride(A, "A"), _row_stride(D, "D")
-    M, nk = A.shape[0], -(-K // 128)
-    if A.shape[1] != K or A.element_size() != 1:
+    (M, cols, lda), (rows, outs, ldd) = _rows(A, "A"), _rows(D, "D")
+    nk = -(-K // 128)
+    if cols != K or A.element_size() != 1:
         raise ValueError("A must be fp8 codes [M_total, K]")
     _expert_rows(sa, (nk, M), _f32, "sa")
     _expert_rows(sw, (G, -(-N // 128), nk), _f32, "sw")
@@ -273,11 +280,11 @@ def kg_fprop(A, sa, W, sw, D, ms, flags=0, stream=None):
         flags |= KG_FLAG_D_BF16
     elif D.dtype is not _f32:
         raise ValueError("D must be float32 or bfloat16")
-    if D.shape != (M, N):
+    if rows != M or outs != N:
         raise ValueError("D must be [M_total, N]")
-    _gpu(D, A, sa, W, sw, ms)
+    gpu = _gpu(D, A, sa, W, sw, ms)
     rc = L.kg_fprop(A.data_ptr(), lda, sa.data_ptr(), W.data_ptr(), sw.data_ptr(), D.data_ptr(),
-                    ldd, ms.data_ptr(), G, N, K, M, flags, _on(D, stream))
+                    ldd, ms.data_ptr(), G, N, K, M, flags, _on(gpu, stream))
     if rc:
         _fail(rc, "kg_fprop")
     return D
@@ -301,7 +308,7 @@ class AdamWTable:
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, m_scales=None, v_scales=None,
                  copies=None):
-        L = _load()
+        L = _lib or _load()
         n = len(params)
         self.count, self.kinds, self.items, self.table = n, 0, 0, None
         none = [None] * n
@@ -357,16 +364,16 @@ def kg_adamw(table, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step
     """One AdamW step over an AdamWTable's tensors, in place. step: 1 for the first. gscale:
     a one-element float32 GPU tensor that multiplies every gradient. dyn: float32 GPU tensor
     {lr, 1 - beta1^step, 1 - beta2^step}, read in the place of lr and step."""
-    L = _load()
+    L = _lib or _load()
     if gscale is not None and (gscale.dtype is not _f32 or gscale.numel() != 1):
         raise ValueError("gscale must be one float32")
     if dyn is not None and (dyn.dtype is not _f32 or dyn.shape != (3,) or not dyn.is_contiguous()):
         raise ValueError("dyn must be three contiguous float32")
     if table.table is None:  # no tensors
         return
-    _gpu(table.table, gscale, dyn)
+    gpu = _gpu(table.table, gscale, dyn)
     rc = L.kg_adamw(table.table.data_ptr(), table.count, table.items, table.kinds, lr, beta1,
                     beta2, eps, weight_decay, step, _at(gscale), _at(dyn),
-                    _on(table.table, stream))
+                    _on(gpu, stream))
     if rc:
         _fail(rc, "kg_adamw")
