@@ -664,12 +664,10 @@ static FLaunch f_tiled(bool outb, int id) {
   return FLaunch{fn, C::BT, C::BN, C::NS * C::STAGE, C::PER_CU, id};
 }
 
-template <int TT>
-static FLaunch f_stream(bool fast, bool outb) {
-  const void* fn = fast ? (outb ? (const void*)kg_fprop_stream_kernel<TT, true, true>
-                                : (const void*)kg_fprop_stream_kernel<TT, true, false>)
-                        : (outb ? (const void*)kg_fprop_stream_kernel<TT, false, true>
-                                : (const void*)kg_fprop_stream_kernel<TT, false, false>);
+template <int TT, bool FAST>
+static FLaunch f_stream(bool outb) {
+  const void* fn = outb ? (const void*)kg_fprop_stream_kernel<TT, FAST, true>
+                        : (const void*)kg_fprop_stream_kernel<TT, FAST, false>;
   return FLaunch{fn, 16 * TT, kStreamN, 0, 1, -1};
 }
 
@@ -685,9 +683,12 @@ struct FTile {
 //  * Streaming where it takes few workgroups and passes, 3 per compute unit (a tile's time is
 //    then the latency of its blocks): streaming / 64 x 128 tiles with K 7168, N 4096: 1, 16, 64
 //    rows of one expert 12 / 42, 14 / 25, 24 / 25 us; 4 experts of 2 and 16 rows 20 / 26 and
-//    30 / 26, 8 of 2 rows 40 / 39; 4 of 4 rows, N 7168, K 2048 16 / 12. TT token tiles hold an
-//    expert's rows: the average, or twice it where several experts share M_total unevenly
-//    (4 experts of 16 rows, TT 1, 2, 4: 30, 27, 32 us).
+//    30 / 26, 8 of 2 rows 40 / 39; 4 of 4 rows, N 7168, K 2048 16 / 12. TT token tiles hold the
+//    rows of a pass: the average, or twice it where several experts share M_total unevenly, up
+//    to 32 (TT 2 / 4: 3 experts of 20 rows, N 512, K 2048 6.8 / 7.6 us, exact 8.8 / 12.2; 2 of 20,
+//    N 2048, K 4096 11.2 / 12.8 and 11.1 / 18.7). 64 fit one expert's rows (N 4096, K 7168
+//    31.3 / 24.6), not in exact products, whose widened fragments spill (64 rows, N and K 1024
+//    7.8 / 9.9, N 4096, K 7168 32.4 / 30.5).
 //  * Streaming as well for the fewest rows of long weight rows. 32 experts, N 4096, streaming /
 //    64 x 128 tiles, K 2048, 3584, 7168: fp8 MFMA, 1 row each 37 / 37, 50 / 52, 105 / 127 us, 2 rows
 //    50 / 45, 76 / 74, 131 / 141, 4 rows 57 / 47, 87 / 77, 164 / 155; exact, 1 row 51 / 46, 83 / 78,
@@ -708,8 +709,9 @@ static FLaunch f_choose(int64_t M, int G, int N, int K, int cus, bool fast, bool
   const int64_t groups = live * ((N + kStreamN - 1) / kStreamN), rows = G == 1 ? avg : 2 * avg;
   if ((avg <= 64 && groups * ((rows + 15) / 16) <= 3 * cus) ||
       (groups < (1 << 23) && M <= (fast ? 2 : 1) * (int64_t)G && K > 4096)) {
-    return rows <= 16 ? f_stream<1>(fast, outb) : rows <= 32 ? f_stream<2>(fast, outb)
-                                                             : f_stream<4>(fast, outb);
+    if (rows <= 16) return fast ? f_stream<1, true>(outb) : f_stream<1, false>(outb);
+    if (fast && G == 1 && rows > 32) return f_stream<4, true>(outb);
+    return fast ? f_stream<2, true>(outb) : f_stream<2, false>(outb);
   }
   using Tile64 = FCfg<64, 64, 4, 2>;
   using Tile64x128 = FCfg<64, 128, 2, 2>;
