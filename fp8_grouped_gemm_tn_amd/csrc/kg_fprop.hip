@@ -334,8 +334,10 @@ __device__ __forceinline__ bool f_offsets(const int32_t* ms, int G, int bt, int6
 // a burst of loads, a vector load of the weight scale and no fragments ahead; 1110 with the
 // scale through a scalar load and four waves loading; 870 with fragments ahead and counted
 // waits, 847 without LDS conflicts and with spread loads (now 812 to 848 by card). 1.61 M cycles,
-// MFMA busy for 0.95 M of them, at 1.77 GHz, to which the clock falls under this load: without the loads
-// 1.50 M cycles at 1.92 GHz, without the meetings as well 1.32 M. Tried without gain: the
+// MFMA busy for 0.95 M of them, at 1.77 GHz, to which the clock falls under this load: without
+// the loads 1.50 M cycles at 1.92 GHz, without the meetings as well 1.32 M. (Operands of zeros:
+// 704 us, without loads 627, without meetings 649, without both 545, without W's LDS reads 614,
+// without the scaled sums 686.) Tried without gain: the
 // next tile's first loads before this one's stores (877), loads into the L2 two to four
 // blocks ahead (912), 32 x 32 MFMAs (924), raised wave priority (873), the last round's
 // tiles in quarters (840).
@@ -475,13 +477,14 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 // ------------------------------------------------------------------------ streaming kernel
 
 // A workgroup computes 32 outputs of one expert for all its rows, 16 TT at a time: grid
-// min(G, M_total) x ceil(N / 32), the experts without rows left out. Its 8 waves take the blocks of the contraction axis in turn, each adding
-// up its blocks in registers, with the next block's operands on their way; the waves' sums
-// are added in LDS in a fixed order. A lane reads 32 neighbouring channels of a row, so a
+// min(G, M_total) x ceil(N / 32), the experts without rows left out. Its 8 waves take the
+// blocks of the contraction axis in turn, each adding up its blocks in registers, with the next
+// block's operands on their way (two or three more: slower, 140 -> 165 us); the waves' sums are
+// added in LDS in a fixed order. A lane reads 32 neighbouring channels of a row, so a
 // row's 128 bytes go to four lanes of one load.
 //
-// Bound by W's bytes: 64 rows through 32 experts of 4096 x 7168 take 127 us (7.4 TB/s; 138
-// with one block's loads at a time). 64 outputs per workgroup: 139 us.
+// Bound by W's bytes: 64 rows through 32 experts of 4096 x 7168 take 124 to 140 us by card (up to
+// 7.4 TB/s; 138 where 127, with one block's loads at a time). 64 outputs per workgroup: 139 us.
 constexpr int kStreamWaves = 8, kStreamN = 32;
 
 // The expert with rows that `nth` others with rows come before, its first row and their number, by
@@ -534,7 +537,12 @@ __device__ __forceinline__ bool find_rows(const FParams& p, int nth, int* g, int
   return true;
 }
 
-template <int TT, bool FAST, bool OUTB>
+// AHEAD: a block's weight scale is loaded with its operands, not when it is used. With the fp8
+// MFMA and TT 1 that takes the registers beyond 128, so that a compute unit holds one workgroup,
+// not two: for at most one workgroup per compute unit (1 row, N 4096, K 7168: 11.7 -> 10.7 us; 4
+// experts of 2 rows 20.9 -> 23.0, the 64 rows above 140 -> 155). Exact products of many experts
+// gain (32 experts of 1 row: 132 -> 119 us).
+template <int TT, bool FAST, bool OUTB, bool AHEAD>
 __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FParams p) {
   constexpr int NJ = kStreamN / 16;
   __shared__ v4f sums[kStreamWaves][NJ * TT][64];
@@ -569,7 +577,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
     for (int i = 0; i < NJ; ++i)
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
-    auto block = [&](const v4i (&wx)[NJ][2], const v4i (&tx)[TT][2], const float (&s)[TT], float swv) {
+    auto block = [&](const v4i (&wx)[NJ][2], const v4i (&tx)[TT][2], const float (&s)[TT],
+                     float swv) {
       Frag<FAST> tf[TT];
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) tf[tt].set(tx[tt][0], tx[tt][1]);
@@ -587,8 +596,9 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
       }
     };
     v4i wx[2][NJ][2], tx[2][TT][2];
-    float s[2][TT];
+    float s[2][TT], sv[2];
     auto load = [&](int kb, int h) {
+      if constexpr (AHEAD) sv[h] = swg[kb];
 #pragma unroll
       for (int i = 0; i < NJ; ++i) {
         wx[h][i][0] = *(const v4i*)(wrow[i] + kb * 128);
@@ -606,9 +616,9 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
     for (; kb < nfull; kb += 2 * kStreamWaves) {
       const int k1 = kb + kStreamWaves, k2 = kb + 2 * kStreamWaves;
       if (k1 < nfull) load(k1, 1);
-      block(wx[0], tx[0], s[0], swg[kb]);
+      block(wx[0], tx[0], s[0], AHEAD ? sv[0] : swg[kb]);
       if (k2 < nfull) load(k2, 0);
-      if (k1 < nfull) block(wx[1], tx[1], s[1], swg[k1]);
+      if (k1 < nfull) block(wx[1], tx[1], s[1], AHEAD ? sv[1] : swg[k1]);
     }
     if (nfull < nk && w == nfull % kStreamWaves) {  // the last block's K % 128 channels
       const int left = p.K - nfull * 128 - 32 * q;
@@ -664,10 +674,10 @@ static FLaunch f_tiled(bool outb, int id) {
   return FLaunch{fn, C::BT, C::BN, C::NS * C::STAGE, C::PER_CU, id};
 }
 
-template <int TT, bool FAST>
+template <int TT, bool FAST, bool AHEAD>
 static FLaunch f_stream(bool outb) {
-  const void* fn = outb ? (const void*)kg_fprop_stream_kernel<TT, FAST, true>
-                        : (const void*)kg_fprop_stream_kernel<TT, FAST, false>;
+  const void* fn = outb ? (const void*)kg_fprop_stream_kernel<TT, FAST, true, AHEAD>
+                        : (const void*)kg_fprop_stream_kernel<TT, FAST, false, AHEAD>;
   return FLaunch{fn, 16 * TT, kStreamN, 0, 1, -1};
 }
 
@@ -688,7 +698,7 @@ struct FTile {
 //    to 32 (TT 2 / 4: 3 experts of 20 rows, N 512, K 2048 6.8 / 7.6 us, exact 8.8 / 12.2; 2 of 20,
 //    N 2048, K 4096 11.2 / 12.8 and 11.1 / 18.7). 64 fit one expert's rows (N 4096, K 7168
 //    31.3 / 24.6), not in exact products, whose widened fragments spill (64 rows, N and K 1024
-//    7.8 / 9.9, N 4096, K 7168 32.4 / 30.5).
+//    7.8 / 9.9, N 4096, K 7168 30.0 / 30.5).
 //  * Streaming as well for the fewest rows of long weight rows. 32 experts, N 4096, streaming /
 //    64 x 128 tiles, K 2048, 3584, 7168: fp8 MFMA, 1 row each 37 / 37, 50 / 52, 105 / 127 us, 2 rows
 //    50 / 45, 76 / 74, 131 / 141, 4 rows 57 / 47, 87 / 77, 164 / 155; exact, 1 row 51 / 46, 83 / 78,
@@ -709,9 +719,11 @@ static FLaunch f_choose(int64_t M, int G, int N, int K, int cus, bool fast, bool
   const int64_t groups = live * ((N + kStreamN - 1) / kStreamN), rows = G == 1 ? avg : 2 * avg;
   if ((avg <= 64 && groups * ((rows + 15) / 16) <= 3 * cus) ||
       (groups < (1 << 23) && M <= (fast ? 2 : 1) * (int64_t)G && K > 4096)) {
-    if (rows <= 16) return fast ? f_stream<1, true>(outb) : f_stream<1, false>(outb);
-    if (fast && G == 1 && rows > 32) return f_stream<4, true>(outb);
-    return fast ? f_stream<2, true>(outb) : f_stream<2, false>(outb);
+    if (rows <= 16 && fast)
+      return groups <= cus ? f_stream<1, true, true>(outb) : f_stream<1, true, false>(outb);
+    if (rows <= 16) return f_stream<1, false, true>(outb);
+    if (fast && G == 1 && rows > 32) return f_stream<4, true, true>(outb);
+    return fast ? f_stream<2, true, true>(outb) : f_stream<2, false, true>(outb);
   }
   using Tile64 = FCfg<64, 64, 4, 2>;
   using Tile64x128 = FCfg<64, 128, 2, 2>;
