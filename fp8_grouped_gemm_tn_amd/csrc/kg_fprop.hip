@@ -133,6 +133,19 @@ __device__ __forceinline__ void store_run(void* D, int64_t at, int left, const v
   }
 }
 
+// ... and four.
+template <bool OUTB>
+__device__ __forceinline__ void store_four(void* D, int64_t at, int left, const v4f& a) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= left) continue;
+    if constexpr (OUTB)
+      ((unsigned short*)D)[at + i] = __builtin_bit_cast(unsigned short, (__bf16)(float)a[i]);
+    else
+      ((float*)D)[at + i] = a[i];
+  }
+}
+
 // ---------------------------------------------------------------------------- tiled kernel
 
 // BT tokens x BN outputs per workgroup of 8 waves (WT along the tokens, PER_CU such
@@ -476,15 +489,15 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 
 // ------------------------------------------------------------------------ streaming kernel
 
-// A workgroup computes 32 outputs of one expert for all its rows, 16 TT at a time: grid
-// min(G, M_total) x ceil(N / 32), the experts without rows left out. Its 8 waves take the
+// A workgroup computes 16 NJ outputs of one expert for all its rows, 16 TT at a time: grid
+// min(G, M_total) x ceil(N / (16 NJ)), the experts without rows left out. Its 8 waves take the
 // blocks of the contraction axis in turn, each adding up its blocks in registers, with the next
 // block's operands on their way (two or three more: slower, 140 -> 165 us); the waves' sums are
 // added in LDS in a fixed order. A lane reads 32 neighbouring channels of a row, so a
 // row's 128 bytes go to four lanes of one load.
 //
 // Bound by W's bytes: 64 rows through 32 experts of 4096 x 7168 take 124 to 140 us by card (up to
-// 7.4 TB/s; 138 where 127, with one block's loads at a time). 64 outputs per workgroup: 139 us.
+// 7.4 TB/s; 138 where 127, with one block's loads at a time. 64 outputs per workgroup: 139 us.
 constexpr int kStreamWaves = 8, kStreamN = 32;
 
 // The expert with rows that `nth` others with rows come before, its first row and their number, by
@@ -537,17 +550,12 @@ __device__ __forceinline__ bool find_rows(const FParams& p, int nth, int* g, int
   return true;
 }
 
-// AHEAD: a block's weight scale is loaded with its operands, not when it is used. With the fp8
-// MFMA and TT 1 that takes the registers beyond 128, so that a compute unit holds one workgroup,
-// not two: for at most one workgroup per compute unit (1 row, N 4096, K 7168: 11.7 -> 10.7 us; 4
-// experts of 2 rows 20.9 -> 23.0, the 64 rows above 140 -> 155). Exact products of many experts
-// gain (32 experts of 1 row: 132 -> 119 us).
-template <int TT, bool FAST, bool OUTB, bool AHEAD>
+template <int TT, int NJ, bool FAST, bool OUTB>
 __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FParams p) {
-  constexpr int NJ = kStreamN / 16;
+  constexpr int N0 = 16 * NJ;  // outputs of a workgroup
   __shared__ v4f sums[kStreamWaves][NJ * TT][64];
   const int per = p.tiles_n;  // workgroups per expert
-  const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * kStreamN;
+  const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * N0;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, j = lane & 15;
   int64_t row0;
@@ -562,7 +570,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
   const unsigned char* wrow[NJ];
 #pragma unroll
   for (int i = 0; i < NJ; ++i)
-    wrow[i] = p.W + ((int64_t)g * p.N + min(n0 + frow(i, j), p.N - 1)) * p.K + 32 * q;
+    wrow[i] =
+        p.W + ((int64_t)g * p.N + min(n0 + (NJ == 1 ? j : frow(i, j)), p.N - 1)) * p.K + 32 * q;
   for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
     const unsigned char* arow[TT];
     const float* sa[TT];
@@ -598,7 +607,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
     v4i wx[2][NJ][2], tx[2][TT][2];
     float s[2][TT], sv[2];
     auto load = [&](int kb, int h) {
-      if constexpr (AHEAD) sv[h] = swg[kb];
+      sv[h] = swg[kb];
 #pragma unroll
       for (int i = 0; i < NJ; ++i) {
         wx[h][i][0] = *(const v4i*)(wrow[i] + kb * 128);
@@ -611,14 +620,26 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
         s[h][tt] = sa[tt][(int64_t)kb * p.M_total];
       }
     };
-    int kb = w;
-    if (kb < nfull) load(kb, 0);
-    for (; kb < nfull; kb += 2 * kStreamWaves) {
-      const int k1 = kb + kStreamWaves, k2 = kb + 2 * kStreamWaves;
-      if (k1 < nfull) load(k1, 1);
-      block(wx[0], tx[0], s[0], AHEAD ? sv[0] : swg[kb]);
-      if (k2 < nfull) load(k2, 0);
-      if (k1 < nfull) block(wx[1], tx[1], s[1], AHEAD ? sv[1] : swg[k1]);
+    // This wave's blocks w, w + 8, ... In the loop every load is unconditional, so the compiler
+    // knows how many are under way and waits for no more than it needs (loads under conditions:
+    // the 64 rows above 136 us, not 128).
+    const int nb = nfull > w ? (nfull - w + kStreamWaves - 1) / kStreamWaves : 0;
+    int n = 0, kb = w;
+    if (nb > 0) load(kb, 0);
+    for (; n + 2 < nb; n += 2, kb += 2 * kStreamWaves) {
+      load(kb + kStreamWaves, 1);
+      block(wx[0], tx[0], s[0], sv[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      load(kb + 2 * kStreamWaves, 0);
+      block(wx[1], tx[1], s[1], sv[1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (n + 1 < nb) {
+      load(kb + kStreamWaves, 1);
+      block(wx[0], tx[0], s[0], sv[0]);
+      block(wx[1], tx[1], s[1], sv[1]);
+    } else if (n < nb) {
+      block(wx[0], tx[0], s[0], sv[0]);
     }
     if (nfull < nk && w == nfull % kStreamWaves) {  // the last block's K % 128 channels
       const int left = p.K - nfull * 128 - 32 * q;
@@ -641,12 +662,13 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) sums[w][i * TT + tt][lane] = acc[i][tt];
     __syncthreads();
-    // wave w joins and stores pair (w / TT) of output tiles of token tile w % TT
-    if (w < TT * NJ / 2) {
-      const int tt = w % TT, i0 = 2 * (w / TT);
-      v4f x[2];
+    // wave w joins and stores one pair of output tiles (or the only one) of token tile w % TT
+    constexpr int PAIR = NJ == 1 ? 1 : 2;
+    if (w < TT * NJ / PAIR) {
+      const int tt = w % TT, i0 = PAIR * (w / TT);
+      v4f x[PAIR];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < PAIR; ++i) {
         x[i] = sums[0][(i0 + i) * TT + tt][lane];
 #pragma unroll
         for (int v = 1; v < kStreamWaves; ++v) {
@@ -655,8 +677,12 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
           for (int r = 0; r < 4; ++r) x[i][r] += y[r];
         }
       }
-      const int r = r0 + 16 * tt + j, n = n0 + 16 * i0 + 8 * q;
-      if (r < rows) store_run<OUTB>(p.D, (row0 + r) * p.ldd + n, p.N - n, x[0], x[1]);
+      const int r = r0 + 16 * tt + j, n = n0 + 16 * i0 + 4 * PAIR * q;
+      if (r < rows) {
+        const int64_t at = (row0 + r) * p.ldd + n;
+        if constexpr (PAIR == 2) store_run<OUTB>(p.D, at, p.N - n, x[0], x[1]);
+        else store_four<OUTB>(p.D, at, p.N - n, x[0]);
+      }
     }
     __syncthreads();
   }
@@ -674,11 +700,11 @@ static FLaunch f_tiled(bool outb, int id) {
   return FLaunch{fn, C::BT, C::BN, C::NS * C::STAGE, C::PER_CU, id};
 }
 
-template <int TT, bool FAST, bool AHEAD>
+template <int TT, int NJ, bool FAST>
 static FLaunch f_stream(bool outb) {
-  const void* fn = outb ? (const void*)kg_fprop_stream_kernel<TT, FAST, true, AHEAD>
-                        : (const void*)kg_fprop_stream_kernel<TT, FAST, false, AHEAD>;
-  return FLaunch{fn, 16 * TT, kStreamN, 0, 1, -1};
+  const void* fn = outb ? (const void*)kg_fprop_stream_kernel<TT, NJ, FAST, true>
+                        : (const void*)kg_fprop_stream_kernel<TT, NJ, FAST, false>;
+  return FLaunch{fn, 16 * TT, 16 * NJ, 0, 1, -1};
 }
 
 // A tile and what one block of it takes on every compute unit, in tenths of a microsecond:
@@ -692,17 +718,18 @@ struct FTile {
 // M_total and G; every choice is right for every distribution of the rows.
 //  * Streaming where it takes few workgroups and passes, 3 per compute unit (a tile's time is
 //    then the latency of its blocks): streaming / 64 x 128 tiles with K 7168, N 4096: 1, 16, 64
-//    rows of one expert 12 / 42, 14 / 25, 24 / 25 us; 4 experts of 2 and 16 rows 20 / 26 and
-//    30 / 26, 8 of 2 rows 40 / 39; 4 of 4 rows, N 7168, K 2048 16 / 12. TT token tiles hold the
-//    rows of a pass: the average, or twice it where several experts share M_total unevenly, up
-//    to 32 (TT 2 / 4: 3 experts of 20 rows, N 512, K 2048 6.8 / 7.6 us, exact 8.8 / 12.2; 2 of 20,
-//    N 2048, K 4096 11.2 / 12.8 and 11.1 / 18.7). 64 fit one expert's rows (N 4096, K 7168
-//    31.3 / 24.6), not in exact products, whose widened fragments spill (64 rows, N and K 1024
-//    7.8 / 9.9, N 4096, K 7168 30.0 / 30.5).
+//    rows of one expert 8 / 42, 10 / 25, 20 / 25 us; 4 experts of 2 and 16 rows 20 / 23 and
+//    27 / 23; 4 of 4 rows, N 7168, K 2048 14 / 12. A workgroup has 16 outputs where 32
+//    would leave half of the compute units idle (what one has under way bounds it: N 4096,
+//    K 7168, 1 row 8.1 us with 16 outputs, 10.5 with 32; 16 rows, N 8192 16.2 and 13.0),
+//    else 32. TT token tiles hold the rows of a pass: the average, or twice it where several
+//    experts share M_total unevenly, up to 32, or 64 of one expert (N 4096, K 7168, 64 rows: 19.8
+//    us, in passes of 32 22.4), not in exact products, whose widened fragments spill (23.6).
 //  * Streaming as well for the fewest rows of long weight rows. 32 experts, N 4096, streaming /
-//    64 x 128 tiles, K 2048, 3584, 7168: fp8 MFMA, 1 row each 37 / 37, 50 / 52, 105 / 127 us, 2 rows
-//    50 / 45, 76 / 74, 131 / 141, 4 rows 57 / 47, 87 / 77, 164 / 155; exact, 1 row 51 / 46, 83 / 78,
-//    120 / 145, 2 rows 70 / 51, 96 / 79, 179 / 157. 256 experts of 1 row, N 2048, K 512: 101 / 35.
+//    64 x 128 tiles, K 2048, 3584, 4096, 7168: fp8 MFMA, 1 row each 38 / 38, 52 / 55, 65 / 76,
+//    92 / 127 us, 2 rows 48 / 45, 73 / 74, 84 / 84, 136 / 146, 4 rows 55 / 47, 86 / 81, 93 / 90,
+//    146 / 152; exact, 1 row 48 / 45, 70 / 76, 76 / 76, 118 / 145, 2 rows 66 / 50, 89 / 80,
+//    98 / 89, 149 / 152. 256 experts of 1 row, N 2048, K 512: 102 / 37.
 //  * Else the tile with the least estimated time, rounds over the compute units times a
 //    block's time. The number of 16-byte operand reads per MFMA falls with the tile's size,
 //    the latency of a block and the rows that an expert's last tile leaves empty rise.
@@ -718,20 +745,21 @@ static FLaunch f_choose(int64_t M, int G, int N, int K, int cus, bool fast, bool
   const int64_t avg = (M + G - 1) / G, live = G < M ? G : M;
   const int64_t groups = live * ((N + kStreamN - 1) / kStreamN), rows = G == 1 ? avg : 2 * avg;
   if ((avg <= 64 && groups * ((rows + 15) / 16) <= 3 * cus) ||
-      (groups < (1 << 23) && M <= (fast ? 2 : 1) * (int64_t)G && K > 4096)) {
-    if (rows <= 16 && fast)
-      return groups <= cus ? f_stream<1, true, true>(outb) : f_stream<1, true, false>(outb);
-    if (rows <= 16) return f_stream<1, false, true>(outb);
-    if (fast && G == 1 && rows > 32) return f_stream<4, true, true>(outb);
-    return fast ? f_stream<2, true, true>(outb) : f_stream<2, false, true>(outb);
+      (groups < (1 << 23) && M <= (fast && K > 4096 ? 2 : 1) * (int64_t)G && K >= 3584)) {
+    if (fast && G == 1 && rows > 32) return f_stream<4, 1, true>(outb);
+    if (groups <= cus / 2) {
+      if (rows <= 16) return fast ? f_stream<1, 1, true>(outb) : f_stream<1, 1, false>(outb);
+      return fast ? f_stream<2, 1, true>(outb) : f_stream<2, 1, false>(outb);
+    }
+    if (rows <= 16) return fast ? f_stream<1, 2, true>(outb) : f_stream<1, 2, false>(outb);
+    return fast ? f_stream<2, 2, true>(outb) : f_stream<2, 2, false>(outb);
   }
   using Tile64 = FCfg<64, 64, 4, 2>;
   using Tile64x128 = FCfg<64, 128, 2, 2>;
   using Tile64x128R = FCfg<64, 128, 2, 2, true>;
   // (more tiles than compute units: 8 experts of 16 rows, N 2048, without / with: fp8 15 / 18 us,
   // exact 21 / 27)
-  const bool rotate =
-      K % 4096 == 0 && live > 1 && avg <= 64 && live * ((N + 127) / 128) > cus;
+  const bool rotate = K % 4096 == 0 && avg <= 64 && live * ((N + 127) / 128) > cus;
   const FTile tiles[4] = {
       {fast ? f_tiled<FCfg<256, 256, 4, 1>, true>(outb, 0)
             : f_tiled<FCfg<128, 256, 2, 1>, false>(outb, 1), fast ? 15 : 18, fast ? 15 : 18},

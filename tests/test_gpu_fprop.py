@@ -268,3 +268,13 @@ def test_rows_a_multiple_of_4096_bytes_apart(G, N, K, avg, dt, flags):
     rng = np.random.default_rng(G + K)
     ms = rng.poisson(avg * rng.dirichlet(np.ones(G)) * G).tolist()
     run(ms, N, K, dt, flags, seed=avg)
+
+
+@pytest.mark.parametrize("ms,N,K", [([5], 37, 3600), ([16], 16, 1168), ([33], 50, 2064), ([64], 130, 7184),
+                                    ([49], 4000, 1936), ([2, 0, 9], 90, 3088), ([30, 34], 70, 2320),
+                                    ([1] * 40, 3000, 3600), ([16], 33000, 272), ([3], 34000, 4096)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("flags", [0, FAST])
+def test_few_rows(ms, N, K, dt, flags):
+    """Streaming: several blocks per wave, 16 or 32 outputs per workgroup, passes over the rows."""
+    run(ms, N, K, dt, flags, seed=K)
