@@ -775,8 +775,8 @@ static FLaunch f_choose(int64_t M, int G, int N, int K, int cus, bool fast, bool
   for (int i = 0; i < 4 && !rotate; ++i) {
     const FLaunch& l = tiles[i].l;
     // tiles along the rows, in tenths: one expert's are known; of several, each has a last
-    // one that is filled to some part
-    int64_t mt = live == 1 ? (M + l.bt - 1) / l.bt * 10 : 10 * M / l.bt + 6 * live;
+    // one that is half filled on average
+    int64_t mt = live == 1 ? (M + l.bt - 1) / l.bt * 10 : 10 * M / l.bt + 5 * live;
     if (mt < 10 * live) mt = 10 * live;
     const int64_t n = (mt * ((N + l.bn - 1) / l.bn) + 9) / 10, at_once = (int64_t)cus * l.per_cu;
     const int64_t t = n <= cus ? tiles[i].first : (n + at_once - 1) / at_once * tiles[i].round;
