@@ -308,17 +308,17 @@ __device__ __forceinline__ int64_t named_row(int at, int64_t rows) {
   return r < rows ? r : -1;
 }
 
-// This thread's token and unit of its row. A workgroup holds 256 / lanes runs of `lanes` units,
+// This thread's token and unit of its row. A workgroup holds THREADS / lanes runs of `lanes` units,
 // a token `runs` of them; with 64 lanes or more the token is the same for a whole wave, and its k
 // positions come through scalar loads. Workgroups go to the 8 XCDs in turn; BY_XCD gives each
 // XCD a run of tokens instead.
-template <bool BY_XCD = false>
+template <bool BY_XCD = false, int THREADS = 256>
 __device__ __forceinline__ bool my_unit(const RowShape& s, int64_t* t, int* c) {
   const int64_t b = group_id(), per = s.groups / 8;
   const int64_t id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
   int sub = threadIdx.x / s.lanes;
   if (s.lanes >= 64) sub = uniform(sub);
-  const int64_t q = id * (256 / s.lanes) + sub;
+  const int64_t q = id * (THREADS / s.lanes) + sub;
   // (T * runs stays below 2^32 where runs > 1: a run is 64 units or more)
   const int64_t tok = s.runs == 1 ? q : (uint32_t)q / (uint32_t)s.runs;
   *t = tok;
@@ -543,51 +543,66 @@ __global__ __launch_bounds__(256) void kg_combine_kernel(const unsigned char* __
   }
 }
 
+// Scalar loads, for addresses that are the same in a whole wave.
+typedef __attribute__((address_space(4))) const int32_t ConstInt;
+typedef __attribute__((address_space(4))) const float ConstFloat;
+
 // dY[row] = w dOut[t] (zeros for dropped rows), dw = <dOut[t], Y[row]> (0 for dropped
-// slots). Eight slots at a time: a thread keeps their partial dot products over its
-// channels, then the token's threads add theirs in a fixed order.
-template <bool BF16>
-__global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
+// slots). S slots at a time: a thread keeps their partial dot products over its channels, then
+// the token's threads add theirs in a fixed order. Without dw the units of a token may lie in
+// several workgroups (s.runs > 1).
+// S = 8 reads dOut once. S = 1 is for few slots: s then counts slots as tokens of one slot,
+// `per_row` of them to a row of dOut, so that more compute units share the work (8 slots, 7168
+// bf16 channels, S 8 / 1: 1 token 17.4 / 4.4 us, 64 tokens 22 / 8.8, 200 tokens 24.3 / 24.4, 512
+// tokens 29.5 / 55; 1024 channels, 64 tokens 7.2 / 4.6, 512 tokens 7.9 / 8.7).
+// WAVE: whole waves work on one token (s.lanes >= 64), so its positions and weights are scalars.
+template <bool BF16, int S, int THREADS, bool WAVE>
+__global__ __launch_bounds__(THREADS) void kg_combine_bwd_kernel(
     const unsigned char* __restrict__ dOut, int64_t ldo, const unsigned char* __restrict__ Y,
-    const int32_t* __restrict__ pos, const float* __restrict__ w, RowShape s,
+    const int32_t* __restrict__ pos, const float* __restrict__ w, RowShape s, int per_row,
     unsigned char* __restrict__ dY, float* __restrict__ dw) {
   using V = Vec<BF16>;
-  __shared__ float part[4][8];
-  const int per = 256 / s.lanes, lane = threadIdx.x & (s.lanes - 1);
-  const int64_t t0 = group_id() * per + threadIdx.x / s.lanes;
-  const bool live = t0 < s.T;  // a workgroup of a token's 256 threads is live as a whole
-  const int64_t t = live ? t0 : 0;
+  __shared__ float part[THREADS / 64][S];
+  const int lane = threadIdx.x & (s.lanes - 1);
+  int64_t t;
+  int first;
+  const bool live = my_unit<false, THREADS>(s, &t, &first);
+  if (!live) t = 0;  // (its threads take part in the sums of others)
+  if constexpr (WAVE) t = uniform((int)t);
   const int64_t bytes = (int64_t)s.H * V::ELEM;
   const int units = (int)((bytes + 15) >> 4);
-  const unsigned char* d = dOut + t * ldo * V::ELEM;
-  const int32_t* p = pos + t * s.k;
-  for (int j0 = 0; j0 < s.k; j0 += 8) {
-    float dot[8] = {}, wj[8];
-    int at[8];
+  const unsigned char* d = dOut + (S == 1 ? (uint32_t)t / (uint32_t)per_row : t) * ldo * V::ELEM;
+  for (int j0 = 0; j0 < s.k; j0 += S) {
+    float dot[S] = {}, wj[S];
+    int at[S];
+    int kept = 0;  // bit i: slot j0 + i has a row
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      at[i] = 0;
-      wj[i] = 1.0f;
-      if (j0 + i < s.k) {
-        at[i] = p[j0 + i];
-        if (w != nullptr) wj[i] = w[t * s.k + j0 + i];
+    for (int i = 0; i < S; ++i) {
+      const bool on = j0 + i < s.k;
+      const int64_t slot = t * s.k + j0 + i;
+      if constexpr (WAVE) {
+        at[i] = on ? ((const ConstInt*)pos)[slot] : INT32_MAX;
+        wj[i] = on && w != nullptr ? ((const ConstFloat*)w)[slot] : 1.0f;
+      } else {
+        at[i] = on ? pos[slot] : INT32_MAX;
+        wj[i] = on && w != nullptr ? w[slot] : 1.0f;
       }
+      kept |= (at[i] >= 0 && at[i] < s.rows) << i;
     }
     if (live && bytes >= 16) {
-      for (int c = lane; c < units; c += s.lanes) {
+      for (int c = first; c < units; c += s.lanes * s.runs) {
         const int64_t o = unit_at(c, bytes);
         // elements that the unit before has counted
         const int seen = (int)(16 * (int64_t)c - o) / V::ELEM;
         float g[V::N];
         V::unpack(load16(d + o), g);
-        v4i y[8];
+        v4i y[S];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (dw != nullptr && j0 + i < s.k && at[i] >= 0 && at[i] < s.rows)
+        for (int i = 0; i < S; ++i)
+          if (dw != nullptr && (kept >> i & 1))
             y[i] = load16_once(Y + at[i] * bytes + o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (j0 + i >= s.k) continue;
+        for (int i = 0; i < S; ++i) {
           const int64_t r = named_row(at[i], s.rows);
           if (r < 0) continue;
           float f[V::N];
@@ -611,8 +626,7 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
         const int64_t b = e * V::ELEM;
         const float g = V::load1(d + b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (j0 + i >= s.k) continue;
+        for (int i = 0; i < S; ++i) {
           const int64_t r = named_row(at[i], s.rows);
           if (r < 0) continue;
           V::store1(dY + r * bytes + b, at[i] < 0 ? 0.f : wj[i] * g);
@@ -621,36 +635,40 @@ __global__ __launch_bounds__(256) void kg_combine_bwd_kernel(
       }
     }
     if (dw == nullptr) continue;
-    // The eight sums over the token's threads. In the first three steps a lane hands half of
-    // its sums over and keeps the other half, so ten shuffles add eight sums over a wave; then
-    // lanes 8 m + (0 .. 7) hold sum 4 * bit 0 + 2 * bit 1 + bit 2 of their number.
     const int me = threadIdx.x & 63;
+    int mine = 0;  // the sum that this lane ends with
+    if constexpr (S == 8) {
+      // In the first three steps a lane hands half of its sums over and keeps the other half,
+      // so ten shuffles add eight sums over a wave; then lanes 8 m + (0 .. 7) hold sum
+      // 4 * bit 0 + 2 * bit 1 + bit 2 of their number.
 #pragma unroll
-    for (int step = 0; step < 3; ++step) {
-      const int half = 4 >> step;
-      const bool up = (me >> step) & 1;
+      for (int step = 0; step < 3; ++step) {
+        const int half = 4 >> step;
+        const bool up = (me >> step) & 1;
 #pragma unroll
-      for (int i = 0; i < half; ++i) {
-        const float keep = up ? dot[half + i] : dot[i], give = up ? dot[i] : dot[half + i];
-        dot[i] = keep + __shfl_xor(give, 1 << step, 64);
+        for (int i = 0; i < half; ++i) {
+          const float keep = up ? dot[half + i] : dot[i], give = up ? dot[i] : dot[half + i];
+          dot[i] = keep + __shfl_xor(give, 1 << step, 64);
+        }
       }
+      mine = 4 * (me & 1) + 2 * ((me >> 1) & 1) + ((me >> 2) & 1);
     }
-    for (int o = 8; o < s.lanes && o < 64; o <<= 1) dot[0] += __shfl_xor(dot[0], o, 64);
-    const int mine = 4 * (me & 1) + 2 * ((me >> 1) & 1) + ((me >> 2) & 1);
+    for (int o = S; o < s.lanes && o < 64; o <<= 1) dot[0] += __shfl_xor(dot[0], o, 64);
     if (s.lanes > 64) {  // a token's threads are s.lanes / 64 whole waves of the workgroup
-      const int wave = threadIdx.x >> 6, first = wave & ~(s.lanes / 64 - 1);
+      const int wave = threadIdx.x >> 6, begin = wave & ~(s.lanes / 64 - 1);
       __syncthreads();
-      if (me < 8) part[wave][mine] = dot[0];
+      if (me < S) part[wave][mine] = dot[0];
       __syncthreads();
       dot[0] = 0.f;
-      for (int v = 0; v < s.lanes / 64; ++v) dot[0] += part[first + v][mine];
+      for (int v = 0; v < s.lanes / 64; ++v) dot[0] += part[begin + v][mine];
     }
-    if (live && lane < 8 && j0 + mine < s.k) {
-      const int j = p[j0 + mine];
-      dw[t * s.k + j0 + mine] = j >= 0 && j < s.rows ? dot[0] : 0.f;
-    }
+    if (live && lane < S && j0 + mine < s.k)
+      dw[t * s.k + j0 + mine] = (kept >> mine & 1) ? dot[0] : 0.f;
   }
 }
+
+// Slots up to which kg_combine_bwd takes them one by one.
+constexpr int64_t kSingleSlots = 1024;
 
 // Scales (rows times blocks) from which kg_dispatch_fp8 writes them in a second step.
 constexpr int64_t kTwoStepScales = 1 << 21;
@@ -670,11 +688,14 @@ static int64_t route_block(int64_t n) {
 static int64_t route_blocks(int64_t n) { return (n + route_block(n) - 1) / route_block(n); }
 
 // Checks that the row kernels share, and their launch shape. A token's row is cut into units of
-// `unit` bytes (the last one partial). `split`: runs of `lanes` units (16 to 256, a power of two,
-// the largest of those that leave the fewest threads without a unit), one unit per thread.
-// Else one run of threads loops over the token's units: as many as leave few idle in the last
-// turn, and at least 64 where there are that many units.
-static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, RowShape* s) {
+// `unit` bytes (the last one partial).
+//  SPLIT: runs of `lanes` units (16 to 256, a power of two, the largest of those that leave the
+//    fewest threads without a unit), one unit per thread.
+//  LOOP: one run of threads loops over the token's units: as many as leave few idle in the last
+//    turn, and at least 64 where there are that many units.
+//  WIDE: as LOOP, with as many threads as there are units, up to the 1024 of its workgroups.
+enum RowForm { SPLIT, LOOP, WIDE };
+static int row_shape(int64_t T, int k, int H, int elem, int unit, RowForm form, RowShape* s) {
   if (T < 0 || k < 0 || H < 0) return KG_ERR_SHAPE;
   if (H > (1 << 24) || k > 4096 || (k > 0 && T > (int64_t)(INT32_MAX - 1) / k) || T > INT32_MAX - 1)
     return KG_ERR_UNSUPPORTED;
@@ -683,29 +704,41 @@ static int row_shape(int64_t T, int k, int H, int elem, int unit, bool split, Ro
   s->k = k;
   s->H = H;
   const int64_t units = ((int64_t)H * elem + unit - 1) / unit;
-  s->lanes = 256;
+  const int most = form == WIDE ? 1024 : 256;
+  s->lanes = most;
   int64_t least = INT64_MAX;
-  for (int lanes = 256; lanes >= (units >= 64 ? 64 : 16); lanes /= 2) {
+  for (int lanes = most; lanes >= (units >= 64 ? 64 : 16); lanes /= 2) {
     const int64_t threads = (units + lanes - 1) / lanes * lanes;
-    if (threads < least) {
+    if (form == WIDE ? lanes >= units : threads < least) {
       least = threads;
       s->lanes = lanes;
     }
   }
-  s->runs = split && units > 0 ? (int)((units + s->lanes - 1) / s->lanes) : 1;
-  const int per = 256 / s->lanes;
+  s->runs = form == SPLIT && units > 0 ? (int)((units + s->lanes - 1) / s->lanes) : 1;
+  const int per = most / s->lanes;
   s->groups = (T * s->runs + per - 1) / per;
   return s->groups <= kGroupsX * 65535 && (s->runs == 1 || T * s->runs < ((int64_t)1 << 32) - 256)
              ? KG_OK
              : KG_ERR_UNSUPPORTED;
 }
 
+// (without dw the positions come in vector loads: 4096 tokens of 2 slots, 1024 channels 8.7 us,
+// with scalar ones 10.8)
+template <bool BF16>
+static auto combine_bwd_kernel(const RowShape& s, bool need_dw, bool single) {
+  if (s.lanes < 64 || !need_dw)
+    return single ? kg_combine_bwd_kernel<BF16, 1, 1024, false>
+                  : kg_combine_bwd_kernel<BF16, 8, 256, false>;
+  return single ? kg_combine_bwd_kernel<BF16, 1, 1024, true>
+                : kg_combine_bwd_kernel<BF16, 8, 256, true>;
+}
+
 // A row kernel on s.groups workgroups (those past them in the last line have no token).
 template <typename... P>
-static int launch_rows(void (*fn)(P...), const RowShape& s, void* stream,
+static int launch_rows(void (*fn)(P...), const RowShape& s, int threads, void* stream,
                        typename same<P>::type... args) {
   const int64_t x = s.groups < kGroupsX ? s.groups : kGroupsX;
-  return launch2(fn, x, (int)((s.groups + x - 1) / x), 256, 0, stream, args...);
+  return launch2(fn, x, (int)((s.groups + x - 1) / x), threads, 0, stream, args...);
 }
 
 }  // namespace kg
@@ -764,7 +797,7 @@ extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64
   if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
-  const int rc = row_shape(T, k, H, elem, 16, true, &s);
+  const int rc = row_shape(T, k, H, elem, 16, SPLIT, &s);
   if (rc != KG_OK) return rc;
   if (ldx < H) return KG_ERR_SHAPE;
   if (s.rows == 0 || H == 0) return KG_OK;
@@ -775,12 +808,12 @@ extern "C" int kg_dispatch(const void* X, int64_t ldx, const int32_t* pos, int64
       ranges_overlap(pos, (size_t)s.rows * 4, Xp, out))
     return KG_ERR_ALIAS;
   auto fn = elem == 2 ? kg_dispatch_kernel<2> : kg_dispatch_kernel<4>;
-  return launch_rows(fn, s, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Xp);
+  return launch_rows(fn, s, 256, stream, (const unsigned char*)X, ldx, pos, s, (unsigned char*)Xp);
 }
 
 extern "C" int64_t kg_dispatch_fp8_workspace_bytes(int64_t T, int k, int H) {
   RowShape s;
-  if (row_shape(T, k, H, 2, 32, true, &s) != KG_OK) return -1;
+  if (row_shape(T, k, H, 2, 32, SPLIT, &s) != KG_OK) return -1;
   if (s.rows * ((H + 127) / 128) < kTwoStepScales) return 0;
   return T * padded_blocks(H) * 4 + s.rows * 4;
 }
@@ -790,7 +823,7 @@ extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, i
                                int64_t workspace_bytes, void* stream) {
   RowShape s;
   if (workspace_bytes < 0) return KG_ERR_SHAPE;
-  const int rc = row_shape(T, k, H, 2, 32, true, &s);
+  const int rc = row_shape(T, k, H, 2, 32, SPLIT, &s);
   if (rc != KG_OK) return rc;
   if (ldx < H) return KG_ERR_SHAPE;
   if (H % 16 != 0) return KG_ERR_ALIGN;
@@ -810,7 +843,7 @@ extern "C" int kg_dispatch_fp8(const void* X, int64_t ldx, const int32_t* pos, i
       if (r[j].written && ranges_overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return KG_ERR_ALIAS;
   float* token_sa = two ? (float*)workspace : nullptr;
   int32_t* slot_of = two ? (int32_t*)(token_sa + T * padded_blocks(H)) : nullptr;
-  const int e = launch_rows(kg_dispatch_fp8_kernel, s, stream, (const unsigned char*)X, ldx,
+  const int e = launch_rows(kg_dispatch_fp8_kernel, s, 256, stream, (const unsigned char*)X, ldx,
                        pos, s, (unsigned char*)Q, sa, token_sa, slot_of);
   if (e != KG_OK || !two) return e;
   const int groups = ((H + 127) / 128 + kRowBlocks - 1) / kRowBlocks;
@@ -823,7 +856,7 @@ extern "C" int kg_combine(const void* Y, const int32_t* pos, const float* w, voi
   if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
-  const int rc = row_shape(T, k, H, elem, 16, true, &s);
+  const int rc = row_shape(T, k, H, elem, 16, SPLIT, &s);
   if (rc != KG_OK) return rc;
   if (ldo < H) return KG_ERR_SHAPE;
   if (T == 0 || H == 0) return KG_OK;
@@ -836,7 +869,7 @@ extern "C" int kg_combine(const void* Y, const int32_t* pos, const float* w, voi
       ranges_overlap(w, (size_t)s.rows * 4, out, no))
     return KG_ERR_ALIAS;
   auto fn = elem == 2 ? kg_combine_kernel<true> : kg_combine_kernel<false>;
-  return launch_rows(fn, s, stream, (const unsigned char*)Y, pos, w, s,
+  return launch_rows(fn, s, 256, stream, (const unsigned char*)Y, pos, w, s,
                 (unsigned char*)out, ldo);
 }
 
@@ -846,8 +879,13 @@ extern "C" int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, cons
   if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
-  const int rc = row_shape(T, k, H, elem, 16, false, &s);
+  int rc = row_shape(T, k, H, elem, 16, dw == nullptr ? SPLIT : LOOP, &s);
   if (rc != KG_OK) return rc;
+  const bool single = dw != nullptr && s.rows <= kSingleSlots;
+  if (single) {
+    rc = row_shape(s.rows, 1, H, elem, 16, WIDE, &s);
+    if (rc != KG_OK) return rc;
+  }
   if (ldo < H) return KG_ERR_SHAPE;
   if (s.rows == 0) return KG_OK;
   if (pos == nullptr) return KG_ERR_NULL;
@@ -863,7 +901,8 @@ extern "C" int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, cons
     if (ranges_overlap(in[i].p, in[i].n, dY, ny) || ranges_overlap(in[i].p, in[i].n, dw, np))
       return KG_ERR_ALIAS;
   if (ranges_overlap(dY, ny, dw, np)) return KG_ERR_ALIAS;
-  auto fn = elem == 2 ? kg_combine_bwd_kernel<true> : kg_combine_bwd_kernel<false>;
-  return launch_rows(fn, s, stream, (const unsigned char*)dOut, ldo, (const unsigned char*)Y, pos,
-                w, s, (unsigned char*)dY, dw);
+  auto fn = elem == 2 ? combine_bwd_kernel<true>(s, dw != nullptr, single)
+                      : combine_bwd_kernel<false>(s, dw != nullptr, single);
+  return launch_rows(fn, s, single ? 1024 : 256, stream, (const unsigned char*)dOut, ldo,
+                     (const unsigned char*)Y, pos, w, s, k, (unsigned char*)dY, dw);
 }

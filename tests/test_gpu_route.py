@@ -383,3 +383,25 @@ def test_more_workgroups_than_a_line_holds():
     assert torch.equal(dY.view(torch.int32), Xp.view(torch.int32))
     want = X.float().square().sum(1)
     assert torch.equal(dw.view(-1), want)  # whole numbers below 2^24
+
+
+@pytest.mark.parametrize("T,k,G,H", [(400, 3, 20, 7), (200, 9, 12, 1235), (90, 17, 20, 40), (1100, 1, 3, 100),
+                                     (900, 2, 8, 129), (130, 8, 16, 2500), (128, 8, 16, 520), (1, 1025, 9, 66)])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("kind", ["uniform", "wild"])
+def test_gradients_on_both_sides_of_the_slots_taken_one_by_one(T, k, G, H, dt, kind):
+    test_dispatch_combine_and_gradients(T, k, G, H, dt, kind)
+
+
+@pytest.mark.parametrize("H", [40, 520])
+def test_gradients_of_many_slots_pass_over_bad_positions(H):
+    T, k = 300, 4
+    pos = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k)
+    bad = pos.clone()
+    bad[1, 0], bad[2, 1], bad[299, 3], bad[4, 1] = T * k, 2**31 - 1, -2**31, ~(T * k)
+    ok = (bad == pos).view(-1)
+    X, Y = torch.randn((T, H), device=DEV), torch.randn((T * k, H), device=DEV)
+    dY, dw = kg.kg_combine_bwd(X, Y, bad, None, torch.full((T * k, H), 9.0, device=DEV))
+    assert (dY[~ok] == 9).all() and (dw.view(-1)[~ok] == 0).all()
+    assert torch.equal(dY[ok], X.repeat_interleave(k, 0)[ok])
+    assert (dw.view(-1)[ok] != 0).all()
