@@ -553,8 +553,8 @@ typedef __attribute__((address_space(4))) const float ConstFloat;
 // several workgroups (s.runs > 1).
 // S = 8 reads dOut once. S = 1 is for few slots: s then counts slots as tokens of one slot,
 // `per_row` of them to a row of dOut, so that more compute units share the work (8 slots, 7168
-// bf16 channels, S 8 / 1: 1 token 17.4 / 4.4 us, 64 tokens 22 / 8.8, 200 tokens 24.3 / 24.4, 512
-// tokens 29.5 / 55; 1024 channels, 64 tokens 7.2 / 4.6, 512 tokens 7.9 / 8.7).
+// bf16 channels, S 8 / 1: 16 tokens 12.4 / 4.7 us, 64 tokens 12.7 / 8.0, 128 tokens 15.5 / 15.7, 256
+// tokens 18.6 / 29.0; 2048 channels 6.6 / 4.5, 6.9 / 4.6, 7.1 / 4.9, 7.9 / 8.7).
 // WAVE: whole waves work on one token (s.lanes >= 64), so its positions and weights are scalars.
 template <bool BF16, int S, int THREADS, bool WAVE>
 __global__ __launch_bounds__(THREADS) void kg_combine_bwd_kernel(
