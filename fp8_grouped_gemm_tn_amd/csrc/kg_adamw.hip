@@ -44,6 +44,15 @@ struct AdamDesc {
 };
 static_assert(sizeof(AdamDesc) == 72, "descriptor layout");
 
+template <bool PACKED>
+struct DescFor {
+  typedef const AdamDesc type;
+};
+template <>
+struct DescFor<true> {
+  typedef const AdamDesc& type;
+};
+
 struct AdamArgs {
   float b1, c1, b2, c2, eps, lr, wd, decay, rate, rbc2;
   const float* gscale;
@@ -191,7 +200,10 @@ template <bool PB, bool GB, bool PACKED>
 __global__ __launch_bounds__(kAdamThreads) void kg_adamw_kernel(const AdamDesc* table,
                                                                 const int32_t* owner, AdamArgs a) {
 #pragma clang fp contract(off)
-  const AdamDesc& d = table[owner[blockIdx.x]];
+  // fp32 states: the descriptor is read as a whole ahead of the stores, not again after them (160
+  // tensors of up to 40000 elements 6.5 -> 6.0 us; 1% slower on large ones). 8-bit states lose by
+  // it (eight tensors of 29.4 M elements 664 -> 699 us).
+  typename DescFor<PACKED>::type d = table[owner[blockIdx.x]];
   const int64_t at =
       ((int64_t)blockIdx.x - d.first_item) * kItem + threadIdx.x * kAdamPer;
   const int64_t left = d.t.n - at;
