@@ -553,8 +553,9 @@ typedef __attribute__((address_space(4))) const float ConstFloat;
 // several workgroups (s.runs > 1).
 // S = 8 reads dOut once. S = 1 is for few slots: s then counts slots as tokens of one slot,
 // `per_row` of them to a row of dOut, so that more compute units share the work (8 slots, 7168
-// bf16 channels, S 8 / 1: 16 tokens 12.4 / 4.7 us, 64 tokens 12.7 / 8.0, 128 tokens 15.5 / 15.7, 256
-// tokens 18.6 / 29.0; 2048 channels 6.6 / 4.5, 6.9 / 4.6, 7.1 / 4.9, 7.9 / 8.7).
+// bf16 channels, S 8 / 1: 16 tokens 12.4 / 4.7 us, 64 tokens 12.7 / 8.0, 128 tokens 15.5 / 15.7,
+// 256 tokens 18.6 / 29.0; 2048 channels 6.6 / 4.5, 6.9 / 4.6, 7.1 / 4.9, 7.9 / 8.7; 777 tokens of
+// 2 slots, 1235 channels 8.9 / 8.2).
 // WAVE: whole waves work on one token (s.lanes >= 64), so its positions and weights are scalars.
 template <bool BF16, int S, int THREADS, bool WAVE>
 __global__ __launch_bounds__(THREADS) void kg_combine_bwd_kernel(
@@ -667,8 +668,8 @@ __global__ __launch_bounds__(THREADS) void kg_combine_bwd_kernel(
   }
 }
 
-// Slots up to which kg_combine_bwd takes them one by one.
-constexpr int64_t kSingleSlots = 1024;
+// kg_combine_bwd takes slots one by one while the card holds all the workgroups at once.
+constexpr int64_t kSingleGroups = 512;
 
 // Scales (rows times blocks) from which kg_dispatch_fp8 writes them in a second step.
 constexpr int64_t kTwoStepScales = 1 << 21;
@@ -880,13 +881,12 @@ extern "C" int kg_combine_bwd(const void* dOut, int64_t ldo, const void* Y, cons
   if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
   const int elem = type == KG_ROWS_BF16 ? 2 : 4;
   RowShape s;
-  int rc = row_shape(T, k, H, elem, 16, dw == nullptr ? SPLIT : LOOP, &s);
+  const int rc = row_shape(T, k, H, elem, 16, dw == nullptr ? SPLIT : LOOP, &s);
   if (rc != KG_OK) return rc;
-  const bool single = dw != nullptr && s.rows <= kSingleSlots;
-  if (single) {
-    rc = row_shape(s.rows, 1, H, elem, 16, WIDE, &s);
-    if (rc != KG_OK) return rc;
-  }
+  RowShape one;
+  const bool single = dw != nullptr && row_shape(s.rows, 1, H, elem, 16, WIDE, &one) == KG_OK &&
+                      one.groups <= kSingleGroups;
+  if (single) s = one;
   if (ldo < H) return KG_ERR_SHAPE;
   if (s.rows == 0) return KG_OK;
   if (pos == nullptr) return KG_ERR_NULL;

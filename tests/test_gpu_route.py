@@ -405,3 +405,10 @@ def test_gradients_of_many_slots_pass_over_bad_positions(H):
     assert (dY[~ok] == 9).all() and (dw.view(-1)[~ok] == 0).all()
     assert torch.equal(dY[ok], X.repeat_interleave(k, 0)[ok])
     assert (dw.view(-1)[ok] != 0).all()
+
+
+@pytest.mark.parametrize("T,k,G,H", [(64, 8, 16, 7000), (65, 8, 16, 7000), (2100, 2, 8, 1100), (4200, 2, 8, 1100),
+                                     (3000, 11, 40, 30), (1, 4096, 9, 66), (5000, 9, 3, 20)])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_gradients_of_many_slots(T, k, G, H, dt):
+    test_dispatch_combine_and_gradients(T, k, G, H, dt, "wild")
