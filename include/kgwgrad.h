@@ -376,7 +376,8 @@ int kg_fprop(const void* A, int64_t lda, const float* sa, const void* W, const f
  *
  *   idx  [T, k] int32: the experts chosen for each token; an entry outside [0, G) is a
  *        dropped slot (an expert held elsewhere, a full one)
- *   ks   [G] int32 out: slots per expert, as kg_wgrad's ks and kg_fprop's ms
+ *   ks   [G] int32 out: kept slots per expert, as kg_wgrad's ks and kg_fprop's ms (which
+ *        add up to the rows that a product is given: with dropped slots, the first ones)
  *   pos  [T, k] int32 out: the row of slot s = t * k + j in the order by (expert, s), the
  *        dropped slots last; r for a kept slot, ~r (negative) for a dropped one
  *   src  [T * k] int32 out, may be NULL: the slot s of row r, ~s for a dropped slot's row

@@ -52,3 +52,28 @@ def test_training(bits):
     losses = example().train(steps=80, bits=bits)
     print(f"[loss] {bits}-bit states: {losses[0]:.4f} -> {losses[-1]:.4f}", flush=True)
     assert losses[-1] < 0.2 * losses[0]
+
+
+@pytest.mark.parametrize("T,G,K,N,k", [(200, 6, 256, 256, 3), (4, 3, 128, 128, 2)])
+def test_dropped_slots_through_the_products(T, G, K, N, k):
+    """Experts held elsewhere: the products take the kept rows, the sums leave the others out."""
+    gen = torch.Generator("cuda").manual_seed(T)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    idx = torch.randint(-2, G + 2, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+    idx[0, 0], idx[1, 0] = 0, G  # one slot of either kind at least
+    x, w, p = rand(T, K).to(torch.bfloat16), rand(G, N, K), rand(T, k)
+    ks = torch.empty(G, dtype=torch.int32, device="cuda")
+    pos, _ = kg.kg_route(idx, ks)
+    rows, sa = kg.kg_dispatch_fp8(x, pos)
+    n = int(ks.sum())
+    wq, sw = example().inputs.quantize_blocks_128x128(w)
+    y = torch.full((T * k, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    kg.kg_fprop(rows[:n], sa[:, :n].contiguous(), wq, sw, y[:n], ks, kg.KG_FLAG_FP8_MFMA)
+    assert kg.kg_status() == kg.KG_OK
+    assert y[n:].isnan().all()
+    out = kg.kg_combine(y, pos, p)
+    on = (idx >= 0) & (idx < G)
+    at = idx.clamp(0, G - 1).long().cpu()
+    one = torch.einsum("tk,tjnk->tjn", x.cpu().double(), w.cpu().double()[at])
+    want = (one * (p * on).cpu().double()[..., None]).sum(1)
+    assert float((out.cpu().double() - want).norm()) <= 2 * 2.0 ** -4 * float(want.norm())
