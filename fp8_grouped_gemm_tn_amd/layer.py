@@ -41,11 +41,18 @@ def _on(gpu, stream):
     return _current_stream(gpu) if stream is None else stream.cuda_stream
 
 
-def _made(shape, dtype, ref, stream):
-    """A new tensor on `ref`'s GPU for a call on `stream` (None: the current one)."""
-    t = torch.empty(shape, dtype=dtype, device=ref.device)
-    if stream is not None:
-        t.record_stream(stream)  # the memory is not handed on before the call is done with it
+def _made(shape, dtype, ref, stream, back=True):
+    """A new tensor on `ref`'s GPU for a call on `stream` (None: the current one). It is of that
+    stream's memory: memory that was freed on the current stream may still be in use by what is
+    queued there, which the call does not wait for. With `back` the caller is given the
+    tensor, for use on the current stream too; else it is the call's alone."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    here = torch.cuda.current_stream(ref.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=ref.device)
+    if back:
+        t.record_stream(here)  # not handed on before the current stream is done with it
     return t
 
 
@@ -132,7 +139,7 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
     if ws is None:
         n = L.kg_route_workspace_bytes(T, k, G)
         if n > 0:
-            ws = _made((n,), torch.uint8, idx, stream)
+            ws = _made((n,), torch.uint8, idx, stream, back=False)
     at, size = _workspace(ws)
     gpu = _gpu(idx, ks, pos, src, ws)
     rc = L.kg_route(idx.data_ptr(), T, k, G, ks.data_ptr(), pos.data_ptr(), src.data_ptr(), at,
@@ -194,7 +201,7 @@ def kg_dispatch_fp8(X, pos, Q=None, sa=None, ws=None, stream=None):
     if ws is None:
         n = L.kg_dispatch_fp8_workspace_bytes(T, k, H)
         if n > 0:
-            ws = _made((n,), torch.uint8, X, stream)
+            ws = _made((n,), torch.uint8, X, stream, back=False)
     at, size = _workspace(ws)
     gpu = _gpu(X, pos, Q, sa, ws)
     rc = L.kg_dispatch_fp8(X.data_ptr(), ldx, pos.data_ptr(), T, k, H, Q.data_ptr(),
