@@ -106,6 +106,21 @@ def _need(cond, msg):
         raise ValueError(msg)
 
 
+def made(torch, shape, dtype, device, stream, back=True):
+    """A new tensor for a call on `stream` (None: the current one). It is of that stream's
+    memory: memory that was freed on the current stream may still be in use by what is queued
+    there, which the call does not wait for. With `back` the caller is given the tensor, for
+    use on the current stream too; else it is the call's alone."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if back:
+        t.record_stream(here)  # not handed on before the current stream is done with it
+    return t
+
+
 def _tensors_on_gpu(ref, **named):
     """Every given tensor contiguous (or, for the names in `strided`, checked by the
     caller) and on `ref`'s GPU. Checked after the shapes, so that shape errors
@@ -350,9 +365,9 @@ def kg_requant(X, xs, ks, gran_k, scale_kind, nblk, Q=None, S=None, stream=None)
           "ks must be a contiguous int32 [G] tensor")
     sdt = torch.float32 if scale_kind == KG_E4M3_F32SCALE else torch.uint8
     if Q is None:
-        Q = torch.empty((K_total, H), dtype=torch.uint8, device=X.device)
+        Q = made(torch, (K_total, H), torch.uint8, X.device, stream)
     if S is None:
-        S = torch.empty((nblk, H), dtype=sdt, device=X.device)
+        S = made(torch, (nblk, H), sdt, X.device, stream)
     _need(tuple(Q.shape) == (K_total, H) and Q.element_size() == 1 and Q.is_contiguous(),
           "Q must be a contiguous 1-byte [K_total, H] tensor")
     _need(tuple(S.shape) == (nblk, H) and S.dtype == sdt and S.is_contiguous(),

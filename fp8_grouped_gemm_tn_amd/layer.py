@@ -11,7 +11,8 @@ import ctypes
 import numpy as np
 
 from ._binding import (KG_ADAMW_8BIT, KG_ADAMW_G_BF16, KG_ADAMW_P_BF16, KG_ERR_SHAPE,
-                       KG_FLAG_D_BF16, KG_OK, KG_ROWS_BF16, KG_ROWS_F32, KgError, _need, lib)
+                       KG_FLAG_D_BF16, KG_OK, KG_ROWS_BF16, KG_ROWS_F32, KgError, _need, lib,
+                       made)
 
 torch = None  # imported with the first call, as the library itself is loaded
 _lib = None
@@ -42,18 +43,7 @@ def _on(gpu, stream):
 
 
 def _made(shape, dtype, ref, stream, back=True):
-    """A new tensor on `ref`'s GPU for a call on `stream` (None: the current one). It is of that
-    stream's memory: memory that was freed on the current stream may still be in use by what is
-    queued there, which the call does not wait for. With `back` the caller is given the
-    tensor, for use on the current stream too; else it is the call's alone."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
-    here = torch.cuda.current_stream(ref.device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=ref.device)
-    if back:
-        t.record_stream(here)  # not handed on before the current stream is done with it
-    return t
+    return made(torch, shape, dtype, ref.device, stream, back)
 
 
 def _fail(rc, what):
