@@ -301,13 +301,16 @@ class AdamWTable:
     scale tensor float32 [ceil(n / 128)]); copies: bfloat16 tensors that receive the new
     parameters (None: none). All contiguous, on one GPU; all of a list have one dtype. The
     table keeps the tensors; it is made anew when one of them moves (a gradient that autograd
-    allocated anew)."""
+    allocated anew). It is made on the stream that its tensors' memory belongs to; a step may
+    run on any stream, and the table be dropped as soon as the call returns. A graph that
+    captured a step needs the table as long as it is replayed."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, m_scales=None, v_scales=None,
                  copies=None):
         L = _lib or _load()
         n = len(params)
         self.count, self.kinds, self.items, self.table = n, 0, 0, None
+        self.streams = set()  # those whose steps the allocator knows of
         none = [None] * n
         _need((m_scales is None) == (v_scales is None), "m_scales and v_scales go together")
         packed = m_scales is not None
@@ -354,6 +357,23 @@ class AdamWTable:
         if rc:
             _fail(rc, "kg_adamw_pack")
         self.table = image.to(device)
+        self.streams.add(_current_stream(device.index))
+
+    def used_on(self, handle, stream):
+        """A step goes to `stream` (None: the current one): from the first one on, the memory of
+        the table and of the tensors that it may be the last to keep is not handed on before
+        that stream is done with it."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.table.device)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return  # nothing runs now
+        for xs in self.tensors:
+            for x in xs:
+                if x is not None:
+                    x.record_stream(stream)
+        self.table.record_stream(stream)
+        self.streams.add(handle)
 
 
 def kg_adamw(table, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, gscale=None,
@@ -368,9 +388,10 @@ def kg_adamw(table, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step
         raise ValueError("dyn must be three contiguous float32")
     if table.table is None:  # no tensors
         return
-    gpu = _gpu(table.table, gscale, dyn)
+    on = _on(_gpu(table.table, gscale, dyn), stream)
     rc = L.kg_adamw(table.table.data_ptr(), table.count, table.items, table.kinds, lr, beta1,
-                    beta2, eps, weight_decay, step, _at(gscale), _at(dyn),
-                    _on(gpu, stream))
+                    beta2, eps, weight_decay, step, _at(gscale), _at(dyn), on)
+    if on not in table.streams:
+        table.used_on(on, stream)
     if rc:
         _fail(rc, "kg_adamw")

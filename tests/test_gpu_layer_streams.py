@@ -76,3 +76,35 @@ def test_what_is_handed_back_outlives_the_current_streams_use():
                 torch.zeros((T * k, H), dtype=BF16, device=DEV)
         torch.cuda.synchronize()
         assert torch.equal(kept, want)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_table_dropped_behind_a_step_on_another_stream(packed):
+    """The step waits behind other work when its table goes, with the gradients that only the
+    table kept; the current stream then fills the memory that is free."""
+    g = torch.Generator(DEV).manual_seed(7)
+    sizes = [5000, 130, 70000]
+    rnd = lambda n: torch.randn(n, generator=g, device=DEV)
+    x = torch.randn((4096, 4096), device=DEV)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        p, g0 = [rnd(n) for n in sizes], [rnd(n) * 1e-3 for n in sizes]
+        state = (lambda: [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in sizes]) if packed else \
+            (lambda: [torch.zeros(n, device=DEV) for n in sizes])
+        scales = lambda: [torch.zeros(-(-n // 128), device=DEV) for n in sizes]
+        more = lambda: [scales(), scales()] if packed else []
+        want = [t.clone() for t in p]
+        kg.kg_adamw(kg.AdamWTable(want, g0, state(), state(), *more()), 1e-3)
+        torch.cuda.synchronize()
+        table = kg.AdamWTable(p, [t.clone() for t in g0], state(), state(), *more())
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            busy(x)
+        kg.kg_adamw(table, 1e-3, stream=side)
+        del table
+        for n in [256, 1024, 2048] + [4 * n for n in sizes] + sizes:
+            for _ in range(8):  # (were it reused: pointers and lengths of zeros)
+                torch.zeros(n, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        for a, b in zip(p, want):
+            assert torch.equal(a, b)

@@ -116,3 +116,45 @@ def test_the_current_stream_needs_no_record(machine, name):
         fns[name](side)
     assert [s for _, s in machine.calls] == [side.cuda_stream] * 2
     assert all(b.owner is side and not b.recorded for b in machine.made)
+
+
+def adamw_table(m, packed):
+    n = 300
+    f32, u8, bf16 = torch.float32, torch.uint8, torch.bfloat16
+    lists = [[m.new(n), m.new(7)], [m.new(n, dtype=bf16), m.new(7, dtype=bf16)]]
+    lists += [[m.new(n, dtype=u8 if packed else f32), m.new(7, dtype=u8 if packed else f32)] for _ in "mv"]
+    scales = [[m.new(3), m.new(1)] for _ in "mv"] if packed else [None, None]
+    table = kg.AdamWTable(*lists, *scales, [m.new(n, dtype=bf16), m.new(7, dtype=bf16)])
+    m.calls.clear()
+    return table, [x for xs in table.tensors for x in xs if x is not None] + [table.table]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("given", [False, True])
+def test_a_table_is_kept_for_the_streams_that_step(machine, packed, given):
+    """The descriptors and what the table may be the last to keep are recorded on every stream
+    that a step goes to, once, whether it is given or the current one."""
+    table, kept = adamw_table(machine, packed)
+    kg.kg_adamw(table, 1e-3)
+    assert not any(x.recorded for x in kept)
+    sides = [Stream(22), Stream(33)]
+    for side in sides:
+        for _ in range(2):
+            if given:
+                kg.kg_adamw(table, 1e-3, stream=side)
+            else:
+                with machine.stream(side):
+                    kg.kg_adamw(table, 1e-3)
+    assert [s for _, s in machine.calls] == [11, 22, 22, 33, 33]
+    assert all(x.recorded == set(sides) for x in kept)
+
+
+def test_a_captured_step_records_nothing_and_a_later_one_does(machine):
+    table, kept = adamw_table(machine, True)
+    side = Stream(22)
+    machine.capturing.add(side)
+    kg.kg_adamw(table, 1e-3, stream=side)
+    assert not any(x.recorded for x in kept)
+    machine.capturing.clear()
+    kg.kg_adamw(table, 1e-3, stream=side)
+    assert all(x.recorded == {side} for x in kept)
