@@ -165,6 +165,9 @@ struct FCfg {
   static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = 8 / WT_, THREADS = 512, TK = 128;
   static constexpr int TT = BT / WT / 16;  // 16-token tiles of a wave
   static constexpr int NI = BN / WN / 16;  // 16-output tiles of a wave
+  // A block's partial sums of a wave, and how many MFMAs after its own each is scaled and added
+  // (a whole block's where it has fewer than three).
+  static constexpr int SUMS = NI * TT, LAG = SUMS < 3 ? SUMS : 3;
   static constexpr int NS = 2;
   static constexpr int OPW = BN * TK, OPT = BT * TK;
   static constexpr int SA_OFF = OPW + OPT;
@@ -357,7 +360,7 @@ __device__ __forceinline__ bool f_offsets(const int32_t* ms, int G, int bt, int6
 template <class C, bool FAST, bool OUTB>
 __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  constexpr int LAG = 3, S = C::NI * C::TT;
+  constexpr int LAG = C::LAG, S = C::SUMS;
   int* off = (int*)(smem + C::NS * C::STAGE);  // [G + 1]
   int* boff = off + p.G + 1;
   if (!f_offsets<C::THREADS>(p.ms, p.G, C::BT, p.M_total, off, boff)) {
