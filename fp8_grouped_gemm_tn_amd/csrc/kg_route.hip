@@ -308,22 +308,29 @@ __device__ __forceinline__ int64_t named_row(int at, int64_t rows) {
   return r < rows ? r : -1;
 }
 
-// This thread's token and unit of its row. A workgroup holds THREADS / lanes runs of `lanes` units,
-// a token `runs` of them; with 64 lanes or more the token is the same for a whole wave, and its k
-// positions come through scalar loads. Workgroups go to the 8 XCDs in turn; BY_XCD gives each
-// XCD a run of tokens instead.
+// Token and unit of a thread: `lane` of run `sub` in workgroup `id`, which holds `per` runs of
+// s.lanes units; a token has s.runs runs. False where there is none. Where runs > 1 row_shape
+// keeps T * runs below 2^32, so 32 bits hold the run's number q in every workgroup that has
+// work, but not in those that fill up the launch's last line.
+__host__ __device__ constexpr bool unit_of(const RowShape& s, int64_t id, int per, int sub,
+                                           int lane, int64_t* t, int* c) {
+  const int64_t q = id * per + sub;
+  const int64_t tok = s.runs == 1 ? q : (uint32_t)q / (uint32_t)s.runs;
+  *t = tok;
+  *c = (int)(q - tok * s.runs) * s.lanes + lane;
+  return id < s.groups && tok < s.T;
+}
+
+// This thread's token and unit of its row. With 64 lanes or more the token is the same for a
+// whole wave, and its k positions come through scalar loads. Workgroups go to the 8 XCDs in turn;
+// BY_XCD gives each XCD a run of tokens instead.
 template <bool BY_XCD = false, int THREADS = 256>
 __device__ __forceinline__ bool my_unit(const RowShape& s, int64_t* t, int* c) {
   const int64_t b = group_id(), per = s.groups / 8;
   const int64_t id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
   int sub = threadIdx.x / s.lanes;
   if (s.lanes >= 64) sub = uniform(sub);
-  const int64_t q = id * (THREADS / s.lanes) + sub;
-  // (T * runs stays below 2^32 where runs > 1: a run is 64 units or more)
-  const int64_t tok = s.runs == 1 ? q : (uint32_t)q / (uint32_t)s.runs;
-  *t = tok;
-  *c = (int)(q - tok * s.runs) * s.lanes + (threadIdx.x & (s.lanes - 1));
-  return tok < s.T;
+  return unit_of(s, id, THREADS / s.lanes, sub, threadIdx.x & (s.lanes - 1), t, c);
 }
 
 // Byte offset of 16-byte unit c of a row of `bytes` >= 16: the last unit ends with the row, so
