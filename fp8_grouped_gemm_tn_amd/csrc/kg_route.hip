@@ -321,16 +321,13 @@ __host__ __device__ constexpr bool unit_of(const RowShape& s, int64_t id, int pe
   return id < s.groups && tok < s.T;
 }
 
-// This thread's token and unit of its row. With 64 lanes or more the token is the same for a
-// whole wave, and its k positions come through scalar loads. Workgroups go to the 8 XCDs in turn;
-// BY_XCD gives each XCD a run of tokens instead.
+// This thread's token and unit of its row. Workgroups go to the 8 XCDs in turn; BY_XCD gives each
+// XCD a run of tokens instead.
 template <bool BY_XCD = false, int THREADS = 256>
 __device__ __forceinline__ bool my_unit(const RowShape& s, int64_t* t, int* c) {
   const int64_t b = group_id(), per = s.groups / 8;
   const int64_t id = BY_XCD && b < per * 8 ? (b & 7) * per + b / 8 : b;
-  int sub = threadIdx.x / s.lanes;
-  if (s.lanes >= 64) sub = uniform(sub);
-  return unit_of(s, id, THREADS / s.lanes, sub, threadIdx.x & (s.lanes - 1), t, c);
+  return unit_of(s, id, THREADS / s.lanes, threadIdx.x / s.lanes, threadIdx.x & (s.lanes - 1), t, c);
 }
 
 // Byte offset of 16-byte unit c of a row of `bytes` >= 16: the last unit ends with the row, so
