@@ -474,9 +474,12 @@ typedef struct {
  *   g' = g * gscale;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2;
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32, each operation rounded once. 8-bit states are rounded to nearest after the step
- * (the parameters see the unrounded ones), with scale amax / 448 per block of 128
- * elements; a nonzero sqrt(v) is never rounded to zero.
+ * in fp32, each operation rounded once. 8-bit states are rounded after the step (the parameters
+ * see the unrounded ones). Per block of 128 elements, with amax its largest magnitude and fl
+ * the rounding to fp32, the scale is fl(amax * fl(1 / 448)) and an element x has the e4m3 code
+ * nearest to fl(x * fl(448 * fl(1 / amax))), ties to even, but no sqrt(v) above zero the
+ * code of zero. A block with amax below 2^-118 is held as zeros; one with an element that is
+ * not finite has a scale that is not finite.
  *
  *   table  the image that kg_adamw_pack made on the host, copied to device memory by the
  *          caller (8-byte aligned); valid as long as the tensors stay where they are
