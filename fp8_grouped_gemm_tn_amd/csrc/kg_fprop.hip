@@ -728,11 +728,19 @@ struct FTile {
 //    else 32. TT token tiles hold the rows of a pass: the average, or twice it where several
 //    experts share M_total unevenly, up to 32, or 64 of one expert (N 4096, K 7168, 64 rows: 19.8
 //    us, in passes of 32 22.4), not in exact products, whose widened fragments spill (23.6).
-//  * Streaming as well for the fewest rows of long weight rows. 32 experts, N 4096, streaming /
-//    64 x 128 tiles, K 2048, 3584, 4096, 7168: fp8 MFMA, 1 row each 38 / 38, 52 / 55, 65 / 76,
-//    92 / 127 us, 2 rows 48 / 45, 73 / 74, 84 / 84, 136 / 146, 4 rows 55 / 47, 86 / 81, 93 / 90,
-//    146 / 152; exact, 1 row 48 / 45, 70 / 76, 76 / 76, 118 / 145, 2 rows 66 / 50, 89 / 80,
-//    98 / 89, 149 / 152. 256 experts of 1 row, N 2048, K 512: 102 / 37.
+//  * Streaming as well for the fewest rows of long weight rows with the fp8 MFMA. Measured where the
+//    rule above does not take it, with 32 to 128 experts, N 2048 to 8192: the time of the tile
+//    chosen else over streaming's, rows in different experts (from G on as many for each) /
+//    dealt out at random:
+//                         M < G          M = G          M = 2 G        M = 3 G
+//      fp8, K 2048                       0.86 / 0.91    0.86 / 0.92    0.84 / 0.86
+//      K 3584, 4096       0.99 / 1.02    1.01 / 1.11    0.99 / 1.04    0.97 / 0.98
+//      K 5120 to 7168     1.04 / 1.09    1.05 / 1.16    1.04 / 1.10    1.03 / 1.04
+//      K 8192                            1.00 / 1.05    0.97 / 1.00    0.97 / 0.99
+//      exact, K 3584, 4096  0.89 / 0.93  0.83 / 0.96    0.82 / 0.88
+//      K 5120 to 7168     0.95 / 1.02    0.91 / 1.04    0.90 / 0.96
+//    (32 experts, N 4096, K 7168, fp8, 1 row each / 32 dealt out: 156 and 164 us / 107 and 131;
+//    exact 180 and 161 / 128 and 149.)
 //  * Else the tile with the least estimated time, rounds over the compute units times a
 //    block's time. The number of 16-byte operand reads per MFMA falls with the tile's size,
 //    the latency of a block and the rows that an expert's last tile leaves empty rise.
@@ -748,7 +756,7 @@ static FLaunch f_choose(int64_t M, int G, int N, int K, int cus, bool fast, bool
   const int64_t avg = (M + G - 1) / G, live = G < M ? G : M;
   const int64_t groups = live * ((N + kStreamN - 1) / kStreamN), rows = G == 1 ? avg : 2 * avg;
   if ((avg <= 64 && groups * ((rows + 15) / 16) <= 3 * cus) ||
-      (groups < (1 << 23) && M <= (fast && K > 4096 ? 2 : 1) * (int64_t)G && K >= 3584)) {
+      (fast && groups < (1 << 23) && M <= (K > 4096 ? 2 : 1) * (int64_t)G && K >= 3584)) {
     if (fast && G == 1 && rows > 32) return f_stream<4, 1, true>(outb);
     if (groups <= cus / 2) {
       if (rows <= 16) return fast ? f_stream<1, 1, true>(outb) : f_stream<1, 1, false>(outb);
