@@ -201,8 +201,8 @@ __global__ __launch_bounds__(kAdamThreads) void kg_adamw_kernel(const AdamDesc* 
                                                                 const int32_t* owner, AdamArgs a) {
 #pragma clang fp contract(off)
   // fp32 states: the descriptor is read as a whole ahead of the stores, not again after them (160
-  // tensors of up to 40000 elements 6.5 -> 6.0 us; 1% slower on large ones). 8-bit states lose by
-  // it (eight tensors of 29.4 M elements 664 -> 699 us).
+  // tensors of up to 40000 elements 6.6 -> 6.1 us; eight of 29.4 M elements 1306 us, 5.4 TB/s,
+  // either way). 8-bit states lose by it (those eight 670 -> 701 us).
   typename DescFor<PACKED>::type d = table[owner[blockIdx.x]];
   const int64_t at =
       ((int64_t)blockIdx.x - d.first_item) * kItem + threadIdx.x * kAdamPer;

@@ -349,14 +349,11 @@ __device__ __forceinline__ bool f_offsets(const int32_t* ms, int G, int bt, int6
 // On 32768 tokens of 8 experts, K 7168, N 4096 (fp8 MFMA, bf16 out, 256 x 256): 1480 us with
 // a burst of loads, a vector load of the weight scale and no fragments ahead; 1110 with the
 // scale through a scalar load and four waves loading; 870 with fragments ahead and counted
-// waits, 847 without LDS conflicts and with spread loads (now 812 to 848 by card). 1.61 M cycles,
-// MFMA busy for 0.95 M of them, at 1.77 GHz, to which the clock falls under this load: without
-// the loads 1.50 M cycles at 1.92 GHz, without the meetings as well 1.32 M. (Operands of zeros:
-// 704 us, without loads 627, without meetings 649, without both 545, without W's LDS reads 614,
-// without the scaled sums 686.) Tried without gain: the
-// next tile's first loads before this one's stores (877), loads into the L2 two to four
-// blocks ahead (912), 32 x 32 MFMAs (924), raised wave priority (873), the last round's
-// tiles in quarters (840).
+// waits, 847 without LDS conflicts and with spread loads (812 to 856 by card; the first launches
+// behind an idle time take up to 1190, until the clock has settled). A counted launch takes 1.67 M
+// cycles at 2.05 GHz, MFMA busy for 0.94 M of them. Tried without gain: the next tile's first
+// loads before this one's stores (877), loads into the L2 two to four blocks ahead (912), 32 x 32
+// MFMAs (924), raised wave priority (873), the last round's tiles in quarters (840).
 template <class C, bool FAST, bool OUTB>
 __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -499,8 +496,9 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 // added in LDS in a fixed order. A lane reads 32 neighbouring channels of a row, so a
 // row's 128 bytes go to four lanes of one load.
 //
-// Bound by W's bytes: 64 rows through 32 experts of 4096 x 7168 take 124 to 140 us by card (up to
-// 7.4 TB/s; 138 where 127, with one block's loads at a time. 64 outputs per workgroup: 139 us.
+// Bound by W's bytes: 64 rows dealt out over 32 experts of 4096 x 7168, 28 of which get some (0.82
+// GB), take 124 to 136 us by card, 6.0 to 6.6 TB/s (with one block's loads at a time 138 us where
+// this takes 127; with 64 outputs per workgroup 139).
 constexpr int kStreamWaves = 8, kStreamN = 32;
 
 // The expert with rows that `nth` others with rows come before, its first row and their number, by
@@ -749,8 +747,8 @@ struct FTile {
 //    of 32 and 97 rows, K 7168 195 / 187 / 173 / 196 and 328 / 259 / 240 / 212.
 //    Exact products, 64 x 64 / 64 x 128 / 128 x 128 / 128 x 256: 256 rows 36 / 47 / 61 / 95 us;
 //    1024 rows, K 4096 59 / 45 / 41 / 57; 32 experts of 16 and 64 rows, K 7168 214 / 171 /
-//    247 / 207 and 312 / 246 / 268 / 226; 32768 rows of 8 experts, K 7168 1.69 ms with
-//    128 x 256 (256 x 256, whose widened fragments spill, 1.70). Two 128 x 128 workgroups
+//    247 / 207 and 312 / 246 / 268 / 226; 32768 rows of 8 experts, K 7168 1.61 to 1.71 ms by
+//    card with 128 x 256 (256 x 256, whose widened fragments spill: the same). Two 128 x 128 workgroups
 //    per compute unit spill too (61 -> 110 us on the 256 rows).
 static FLaunch f_choose(int64_t M, int G, int N, int K, int cus, bool fast, bool outb) {
   const int64_t avg = (M + G - 1) / G, live = G < M ? G : M;

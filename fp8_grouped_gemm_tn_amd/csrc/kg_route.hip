@@ -672,8 +672,9 @@ __global__ __launch_bounds__(THREADS) void kg_combine_bwd_kernel(
   }
 }
 
-// kg_combine_bwd takes slots one by one while the card holds all the workgroups at once.
-constexpr int64_t kSingleGroups = 512;
+// kg_combine_bwd takes slots one by one while the card holds all the workgroups at once: two of 1024
+// threads on each of 256 compute units (on fewer of them it would be slower, not wrong).
+constexpr int64_t kSingleGroups = 2 * 256;
 
 // Scales (rows times blocks) from which kg_dispatch_fp8 writes them in a second step.
 constexpr int64_t kTwoStepScales = 1 << 21;
