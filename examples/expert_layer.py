@@ -16,7 +16,8 @@ of the same shape with other weights. One step:
               kg_combine           ... summed per token (the layer's input gradient)
     update    kg_adamw             all tensors in one launch, states in 8 or 32 bits
 
-Nothing in a step waits for the GPU on the host.
+Nothing in a step waits for the GPU on the host. (Every slot here has an expert. Slots that are
+dropped leave the products fewer rows, and the host has to read how many.)
 """
 import argparse
 import os

@@ -3,7 +3,9 @@ include/kgwgrad.h): the sort of tokens by expert and the row copies (kg_route, k
 kg_dispatch_fp8, kg_combine, kg_combine_bwd), the forward product (kg_fprop) and the AdamW
 step (AdamWTable, kg_adamw).
 
-Argument marshalling only, as in _binding. A small call costs about as much here as on the
+Argument marshalling only, as in _binding. With `stream` given, what a call makes is of that
+stream's memory, and the current stream may use it once it waits for `stream`; the order of the
+given tensors' uses is the caller's. A small call costs about as much here as on the
 GPU, so the checks read each property of a tensor once.
 """
 import ctypes
