@@ -22,6 +22,7 @@ KG_ERR_SCALE_RANGE = -12
 KG_SRC_BF16, KG_SRC_E4M3_1X128 = 0, 1
 KG_ROWS_BF16, KG_ROWS_F32 = 0, 1
 KG_ADAMW_P_BF16, KG_ADAMW_G_BF16, KG_ADAMW_8BIT = 1, 2, 4
+KG_GATE_SIGMOID, KG_GATE_NORM = 1, 2
 ERROR_NAMES = {0: "KG_OK", -1: "KG_ERR_NULL", -2: "KG_ERR_SHAPE", -3: "KG_ERR_GRAN",
                -4: "KG_ERR_DTYPE", -5: "KG_ERR_ALIGN", -6: "KG_ERR_ALIAS",
                -7: "KG_ERR_UNSUPPORTED", -8: "KG_ERR_HIP", -9: "KG_ERR_KSUM",
@@ -63,6 +64,11 @@ SIGNATURES = {
     "kg_adamw_table_bytes": (_i64, [_vp, _i32]),
     "kg_adamw_pack": (_i32, [_vp, _i32, _i32, _vp, _i64]),
     "kg_adamw": (_i32, [_vp, _i32, _i64, _i32, _f64, _f64, _f64, _f64, _f64, _i64, _vp, _vp, _vp]),
+    "kg_gate": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _f64, _f64, _vp, _vp, _vp,
+                       _vp, _vp, _vp, _i64, _vp]),
+    "kg_gate_workspace_bytes": (_i64, [_i64, _i32]),
+    "kg_gate_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _f64, _f64,
+                           _vp, _i64, _vp]),
 }
 
 _lib = None

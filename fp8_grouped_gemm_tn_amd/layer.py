@@ -1,7 +1,7 @@
 """Bindings of the operators around an expert layer's products (the C ABI in
 include/kgwgrad.h): the sort of tokens by expert and the row copies (kg_route, kg_dispatch,
-kg_dispatch_fp8, kg_combine, kg_combine_bwd), the forward product (kg_fprop) and the AdamW
-step (AdamWTable, kg_adamw).
+kg_dispatch_fp8, kg_combine, kg_combine_bwd), the router's choice in front of it (kg_gate,
+kg_gate_bwd), the forward product (kg_fprop) and the AdamW step (AdamWTable, kg_adamw).
 
 Argument marshalling only, as in _binding. With `stream` given, what a call makes is of that
 stream's memory, and the current stream may use it once it waits for `stream`; the order of the
@@ -139,6 +139,88 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
     if rc:
         _fail(rc, "kg_route")
     return pos, src
+
+
+def new_gate_workspace(T, G, device):
+    """The workspace of kg_gate with statistics, for T tokens and G experts; keep it for later
+    calls of these sizes."""
+    n = _load().kg_gate_workspace_bytes(T, G)
+    if n < 0:
+        _fail(KG_ERR_SHAPE, "kg_gate_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _one(t, name):
+    if t is not None and (t.dtype is not _f32 or t.numel() != 1):
+        raise ValueError(f"{name} must be one float32")
+
+
+def kg_gate(X, k, bias=None, flags=0, scale=1.0, coef=0.0, idx=None, w=None, counts=None,
+            psum=None, loss=None, ws=None, stream=None):
+    """The router's choice: X [T, G] logits (bfloat16 or float32, rows contiguous), bias float32
+    [G] or None, flags KG_GATE_SIGMOID and KG_GATE_NORM. Writes idx int32 [T, k] and w float32
+    [T, k] (made if not given), and what is given of counts int32 [G], psum float32 [G] and loss,
+    one float32; ws: new_gate_workspace (made if not given and needed). Returns (idx, w)."""
+    L = _lib or _load()
+    ty, (T, G, ldx) = _row_type(X.dtype, "X"), _rows(X, "X")
+    if idx is None:
+        idx = _made((T, k), _int32, X, stream)
+    if w is None:
+        w = _made((T, k), _f32, X, stream)
+    _i32(idx, (T, k), "idx")
+    _expert_rows(w, (T, k), _f32, "w")
+    if bias is not None:
+        _expert_rows(bias, (G,), _f32, "bias")
+    at = size = None
+    if counts is not None or psum is not None or loss is not None:
+        if counts is not None:
+            _i32(counts, (G,), "counts")
+        if psum is not None:
+            _expert_rows(psum, (G,), _f32, "psum")
+        _one(loss, "loss")
+        if ws is None:
+            n = L.kg_gate_workspace_bytes(T, G)
+            if n > 0:
+                ws = _made((n,), torch.uint8, X, stream, back=False)
+        at, size = _workspace(ws)
+    gpu = _gpu(X, bias, idx, w, counts, psum, loss, ws)
+    rc = L.kg_gate(X.data_ptr(), ldx, _at(bias), T, G, k, ty, flags, scale, coef, idx.data_ptr(),
+                   w.data_ptr(), _at(counts), _at(psum), _at(loss), at, size or 0,
+                   _on(gpu, stream))
+    if rc:
+        _fail(rc, "kg_gate")
+    return idx, w
+
+
+def kg_gate_bwd(X, idx, dw=None, counts=None, dloss=None, flags=0, scale=1.0, coef=0.0, dX=None,
+                stream=None):
+    """The logits' gradient of kg_gate: X, idx, flags, scale and coef as given to and made by it,
+    dw float32 [T, k] (None: zeros), counts int32 [G] (None: no gradient of the loss), dloss one
+    float32 on the GPU (None: 1). Returns dX [T, G] of X's dtype (rows contiguous; made if not
+    given)."""
+    L = _lib or _load()
+    dtype = X.dtype
+    ty, (T, G, ldx) = _row_type(dtype, "X"), _rows(X, "X")
+    shape = idx.shape
+    if len(shape) != 2 or shape[0] != T:
+        raise ValueError(f"idx must be [{T}, k]")
+    _i32(idx, shape, "idx")
+    if dw is not None:
+        _expert_rows(dw, shape, _f32, "dw")
+    if counts is not None:
+        _i32(counts, (G,), "counts")
+    _one(dloss, "dloss")
+    if dX is None:
+        dX = _made((T, G), dtype, X, stream)
+    rows, cols, ldd = _rows(dX, "dX")
+    if dX.dtype is not dtype or rows != T or cols != G:
+        raise ValueError("dX must be [T, G] of X's dtype")
+    gpu = _gpu(X, idx, dw, counts, dloss, dX)
+    rc = L.kg_gate_bwd(X.data_ptr(), ldx, idx.data_ptr(), _at(dw), _at(counts), _at(dloss), T, G,
+                       shape[1], ty, flags, scale, coef, dX.data_ptr(), ldd, _on(gpu, stream))
+    if rc:
+        _fail(rc, "kg_gate_bwd")
+    return dX
 
 
 def _positions(pos, T):

@@ -505,6 +505,61 @@ int kg_adamw(const void* table, int count, int64_t items, int kinds, double lr, 
              double beta2, double eps, double weight_decay, int64_t step, const float* gscale,
              const float* dyn, void* stream);
 
+/* Flags of kg_gate and kg_gate_bwd (OR-ed). */
+#define KG_GATE_SIGMOID 1 /* scores are sigmoids of the logits, not their softmax            */
+#define KG_GATE_NORM 2    /* a token's weights are divided by their sum                      */
+
+/*
+ * kg_gate -- enqueue the router's choice: each token's k experts, their weights, and what the
+ * balance loss needs.
+ *
+ *   X      [T, G] logits (type: KG_ROWS_BF16 or KG_ROWS_F32), row t at element t * ldx
+ *   bias   [G] fp32, or NULL: added to the scores for the choice alone
+ *   idx    [T, k] int32 out: the k experts of the largest keys, largest first, of equal keys the
+ *          lower index first. The key is the logit, or with bias the score plus bias in 64 bits.
+ *          A logit of -inf or NaN (a key of -inf or NaN) is never chosen; a slot for which no
+ *          expert is left holds -1, which kg_route drops
+ *   w      [T, k] fp32 out: scale * s[idx], with KG_GATE_NORM divided by the token's sum of
+ *          chosen scores plus 1e-20; 0 for -1. Scores s are softmax(x), or sigmoid(x) with
+ *          KG_GATE_SIGMOID, in fp32
+ *   counts [G] int32 out, may be NULL: slots that hold g (kg_route's ks)
+ *   psum   [G] fp32 out, may be NULL: the sum over tokens of p[t][g] = softmax(x), or
+ *          s / (sum of the token's s); zeros for a token whose logits are all -inf
+ *   loss   one fp32 out, may be NULL: coef * sum_g counts[g] * psum[g]. With
+ *          coef = alpha G / (k T^2) it is alpha for an even load
+ *   workspace  device memory of kg_gate_workspace_bytes(T, G) bytes, 16-byte aligned, if counts,
+ *          psum or loss is given (else it is not used); needs no initialisation. Calls that share
+ *          one must not run concurrently
+ *
+ * All sums are taken in an order that does not depend on timing. A NaN logit makes the token's
+ * softmax (and its p) NaN. Errors before any launch: KG_ERR_DTYPE, KG_ERR_SHAPE (T < 0, G < 1,
+ * k < 1, k > G, ldx < G, a workspace that is too small), KG_ERR_NULL, KG_ERR_ALIGN (tensors by
+ * their elements), KG_ERR_ALIAS, KG_ERR_UNSUPPORTED (G > 1024, k > 16, T * k > 2^31 - 1,
+ * ldx > 2^30), KG_ERR_HIP.
+ */
+int kg_gate(const void* X, int64_t ldx, const float* bias, int64_t T, int G, int k, int type,
+            int flags, double scale, double coef, int32_t* idx, float* w, int32_t* counts,
+            float* psum, float* loss, void* workspace, int64_t workspace_bytes, void* stream);
+/* Workspace of kg_gate in bytes, or -1 for sizes it does not take. */
+int64_t kg_gate_workspace_bytes(int64_t T, int G);
+
+/*
+ * kg_gate_bwd -- enqueue the logits' gradient of kg_gate (the choice itself has none).
+ *
+ *   X, idx, flags, scale, coef  as given to and written by kg_gate; an idx outside [0, G) is an
+ *          empty slot, and an expert may be named twice
+ *   dw     [T, k] fp32: the gradient of w, or NULL for zeros (idx is then not read)
+ *   counts [G] int32: kg_gate's, or their sum over all ranks (with coef for all ranks' tokens);
+ *          NULL: no gradient of the loss
+ *   dloss  one fp32 on the device: the gradient of the loss, or NULL for 1
+ *   dX     [T, G] out, of X's type, row t at element t * ldd; 0 where the logit is -inf
+ *
+ * Errors as kg_gate.
+ */
+int kg_gate_bwd(const void* X, int64_t ldx, const int32_t* idx, const float* dw,
+                const int32_t* counts, const float* dloss, int64_t T, int G, int k, int type,
+                int flags, double scale, double coef, void* dX, int64_t ldd, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
