@@ -23,6 +23,7 @@ KG_SRC_BF16, KG_SRC_E4M3_1X128 = 0, 1
 KG_ROWS_BF16, KG_ROWS_F32 = 0, 1
 KG_ADAMW_P_BF16, KG_ADAMW_G_BF16, KG_ADAMW_8BIT = 1, 2, 4
 KG_GATE_SIGMOID, KG_GATE_NORM = 1, 2
+KG_W4_INT_BF16, KG_W4_INT_F32, KG_W4_E2M1 = 0, 1, 2
 ERROR_NAMES = {0: "KG_OK", -1: "KG_ERR_NULL", -2: "KG_ERR_SHAPE", -3: "KG_ERR_GRAN",
                -4: "KG_ERR_DTYPE", -5: "KG_ERR_ALIGN", -6: "KG_ERR_ALIAS",
                -7: "KG_ERR_UNSUPPORTED", -8: "KG_ERR_HIP", -9: "KG_ERR_KSUM",
@@ -53,6 +54,8 @@ SIGNATURES = {
     "kg_dgrad": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i32, _vp]),
     "kg_fprop": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i32, _i32, _i64, _i32,
                         _vp]),
+    "kg_fprop_w4": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i32, _i32, _i64, _i32,
+                           _i32, _i32, _vp]),
     "kg_route": (_i32, [_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp]),
     "kg_route_workspace_bytes": (_i64, [_i64, _i32, _i32]),
     "kg_dispatch": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),

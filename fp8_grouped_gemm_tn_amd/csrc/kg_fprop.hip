@@ -31,6 +31,7 @@
 
 #include "kg_device.h"
 #include "kg_host.h"
+#include "kg_rows.h"
 #include "kg_sched.h"
 #include "kgwgrad.h"
 
@@ -274,64 +275,6 @@ __device__ __forceinline__ void f_meet() {
 // compiler wait for them.
 typedef __attribute__((address_space(4))) const float ConstFloat;
 
-// Exclusive scans over the experts, in LDS: off[g] rows and boff[g] tiles of `bt` rows before
-// expert g, g = 0 .. G. Returns false if ms holds a negative count or does not add up to
-// M_total. (kg_sched.h's scan also orders the experts by length, G^2 LDS reads, which a walk in
-// expert order does not need.)
-template <int THREADS>
-__device__ __forceinline__ bool f_offsets(const int32_t* ms, int G, int bt, int64_t M_total,
-                                          int* off, int* boff) {
-  constexpr int E = kMaxGroups / THREADS, W = THREADS / 64;
-  __shared__ int64_t rows_of[W];
-  __shared__ int tiles_of[W];
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  int kv[E], bv[E], neg = 0, own_b = 0;
-  int64_t own = 0;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int g = E * t + e;
-    kv[e] = g < G ? ms[g] : 0;
-    neg |= kv[e] < 0;
-    bv[e] = kv[e] > 0 ? kv[e] / bt + (kv[e] % bt != 0) : 0;
-    own += kv[e];
-    own_b += bv[e];
-  }
-  const int64_t to = wave_incl_scan<int64_t>(own);
-  const int to_b = wave_incl_scan<int>(own_b);
-  if (lane == 63) {
-    rows_of[w] = to;
-    tiles_of[w] = to_b;
-  }
-  const int any_neg = __syncthreads_or(neg);
-  int64_t total = 0, run = to - own;
-  int run_b = to_b - own_b;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    total += rows_of[i];
-    if (i < w) {
-      run += rows_of[i];
-      run_b += tiles_of[i];
-    }
-  }
-  if (any_neg || total != M_total) return false;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int g = E * t + e;
-    if (g <= G) {  // (G < kMaxGroups: else the last entry is the next line's)
-      off[g] = (int)run;
-      boff[g] = run_b;
-    }
-    run += kv[e];
-    run_b += bv[e];
-  }
-  if (t == THREADS - 1 && G == kMaxGroups) {
-    off[G] = (int)run;
-    boff[G] = run_b;
-  }
-  __syncthreads();
-  return true;
-}
-
 // The loop over the blocks. The token fragments are read one block ahead, each right after its
 // last MFMA of the block before, so the buffer that block kb's tokens came from is free during
 // block kb and their block kb + 2 loads into it. W's block kb has been read before the
@@ -501,56 +444,6 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_kernel(FPa
 // this takes 127; with 64 outputs per workgroup 139).
 constexpr int kStreamWaves = 8, kStreamN = 32;
 
-// The expert with rows that `nth` others with rows come before, its first row and their number, by
-// a scan of ms in every wave (a lane holds consecutive experts). rows = 0: there is none.
-// Returns false if ms is inconsistent.
-__device__ __forceinline__ bool find_rows(const FParams& p, int nth, int* g, int64_t* row0,
-                                          int* rows) {
-  const int lane = threadIdx.x & 63, per = (p.G + 63) / 64;
-  const int e0 = lane * per, e1 = min(p.G, e0 + per);
-  int64_t sum = 0;
-  int live = 0, neg = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int v = p.ms[e];
-    neg |= v < 0;
-    sum += v;
-    live += v > 0;
-  }
-  int64_t to = sum;  // rows and experts up to this lane's last one
-  int live_to = live;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t u = __shfl_up(to, d, 64);
-    const int v = __shfl_up(live_to, d, 64);
-    if (lane >= d) {
-      to += u;
-      live_to += v;
-    }
-  }
-  const bool ok = __ballot(neg != 0) == 0 && __shfl(to, 63, 64) == p.M_total;
-  const uint64_t has = __ballot(live_to > nth);  // the first such lane has the expert
-  *rows = 0;
-  *g = 0;
-  *row0 = 0;
-  if (!ok || has == 0) return ok;
-  const int owner = __builtin_ctzll(has);
-  int64_t at = to - sum;
-  int mine = 0, mg = 0, left = nth - (live_to - live);
-  for (int e = e0; e < e1 && lane == owner; ++e) {
-    const int v = p.ms[e];
-    if (v > 0 && left-- == 0) {
-      mine = v;
-      mg = e;
-      break;
-    }
-    at += v;
-  }
-  *row0 = __shfl(at, owner, 64);
-  *rows = uniform(__shfl(mine, owner, 64));
-  *g = uniform(__shfl(mg, owner, 64));
-  return true;
-}
-
 template <int TT, int NJ, bool FAST, bool OUTB>
 __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FParams p) {
   constexpr int N0 = 16 * NJ;  // outputs of a workgroup
@@ -561,7 +454,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void kg_fprop_stream_kernel(FPar
   const int q = lane >> 4, j = lane & 15;
   int64_t row0;
   int rows, g;
-  if (!find_rows(p, nth, &g, &row0, &rows)) {
+  if (!find_rows(p.ms, p.G, p.M_total, nth, &g, &row0, &rows)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = KG_ERR_KSUM;
     return;
   }

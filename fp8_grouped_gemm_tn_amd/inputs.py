@@ -387,6 +387,36 @@ def quantize_blocks_128x128(w: torch.Tensor):
     return q, scale
 
 
+def _two_in_a_byte(c: torch.Tensor):
+    """4-bit codes [..., K] as bytes [..., K / 2], the even channel's in the low half."""
+    c = c.to(torch.uint8)
+    return c[..., 0::2] | (c[..., 1::2] << 4)
+
+
+def quantize_w4(w: torch.Tensor, group: int = 128, zero: bool = True, scale=torch.bfloat16):
+    """w [G, N, K] as whole-number 4-bit codes for kg_fprop_w4: bytes [G, N, K / 2], scales
+    [G, N, K / group] of dtype `scale`, and zero points (None with zero False: 8 everywhere)."""
+    x = w.float().unflatten(-1, (-1, group))
+    lo, hi = x.amin(-1).clamp(max=0), x.amax(-1).clamp(min=0)
+    s = ((hi - lo) / 15 if zero else torch.maximum(-lo / 8, hi / 7)).to(scale).float()
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    z = (-lo / s).round().clamp(0, 15) if zero else torch.full_like(s, 8)
+    c = ((x / s[..., None]).round() + z[..., None]).clamp(0, 15).flatten(-2)
+    return _two_in_a_byte(c), s.to(scale), z.to(torch.uint8) if zero else None
+
+
+def quantize_e2m1(w: torch.Tensor):
+    """w [G, N, K] as e2m1 codes for kg_fprop_w4 with an exponent byte per 32 channels (the largest
+    value falls into [4, 8), where 6 is the largest code): bytes [G, N, K / 2], [G, N, K / 32]."""
+    x = w.float().unflatten(-1, (-1, 32))
+    e = torch.frexp(x.abs().amax(-1))[1] - 3
+    e = (e + 127).clamp(0, 254)
+    y = torch.ldexp(x, (127 - e)[..., None])
+    edges = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device=w.device)
+    c = torch.bucketize(y.abs(), edges) + 8 * (y < 0)
+    return _two_in_a_byte(c.flatten(-2)), e.to(torch.uint8)
+
+
 def make_dgrad_case(name, ms, N, K, seed=0, device="cpu", a_std=1.0, w_std=1.0):
     """Seeded dgrad inputs. Draw order: A (dy), then W."""
     ms = np.asarray(ms, dtype=np.int32)

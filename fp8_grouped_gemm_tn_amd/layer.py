@@ -1,7 +1,7 @@
 """Bindings of the operators around an expert layer's products (the C ABI in
 include/kgwgrad.h): the sort of tokens by expert and the row copies (kg_route, kg_dispatch,
 kg_dispatch_fp8, kg_combine, kg_combine_bwd), the router's choice in front of it (kg_gate,
-kg_gate_bwd), the forward product (kg_fprop) and the AdamW step (AdamWTable, kg_adamw).
+kg_gate_bwd), the forward products (kg_fprop, kg_fprop_w4) and the AdamW step (AdamWTable, kg_adamw).
 
 Argument marshalling only, as in _binding. With `stream` given, what a call makes is of that
 stream's memory, and the current stream may use it once it waits for `stream`; the order of the
@@ -13,24 +13,25 @@ import ctypes
 import numpy as np
 
 from ._binding import (KG_ADAMW_8BIT, KG_ADAMW_G_BF16, KG_ADAMW_P_BF16, KG_ERR_SHAPE,
-                       KG_FLAG_D_BF16, KG_OK, KG_ROWS_BF16, KG_ROWS_F32, KgError, _need, lib,
-                       made)
+                       KG_FLAG_D_BF16, KG_OK, KG_ROWS_BF16, KG_ROWS_F32, KG_W4_E2M1,
+                       KG_W4_INT_BF16, KG_W4_INT_F32, KgError, _need, lib, made)
 
 torch = None  # imported with the first call, as the library itself is loaded
 _lib = None
 _f32 = _bf16 = _int32 = None
-_row_types = {}
+_row_types, _w4_kinds = {}, {}
 _current_gpu = _current_stream = None
 
 
 def _load():
     """The loaded library; sets what the calls read of torch."""
-    global torch, _lib, _f32, _bf16, _int32, _row_types, _current_gpu, _current_stream
+    global torch, _lib, _f32, _bf16, _int32, _row_types, _w4_kinds, _current_gpu, _current_stream
     if _lib is None:
         import torch as t
         L = lib()
         _f32, _bf16, _int32 = t.float32, t.bfloat16, t.int32
         _row_types = {t.bfloat16: KG_ROWS_BF16, t.float32: KG_ROWS_F32}
+        _w4_kinds = {t.bfloat16: KG_W4_INT_BF16, t.float32: KG_W4_INT_F32, t.uint8: KG_W4_E2M1}
         _current_gpu, _current_stream = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream
         torch, _lib = t, L
     return _lib
@@ -368,6 +369,45 @@ def kg_fprop(A, sa, W, sw, D, ms, flags=0, stream=None):
                     ldd, ms.data_ptr(), G, N, K, M, flags, _on(gpu, stream))
     if rc:
         _fail(rc, "kg_fprop")
+    return D
+
+
+def kg_fprop_w4(A, W, sw, D, ms, zp=None, stream=None):
+    """kg_fprop's product with 4-bit weights: A bfloat16 [M_total, K] (rows contiguous), W bytes
+    [G, N, K / 2] of two codes each (the even channel's in the low half), ms int32 [G], D
+    [M_total, N] (float32 or bfloat16, rows contiguous). sw [G, N, K / group] says what the codes
+    are: bfloat16 or float32, whole numbers w = (q - z) s with group 32, 64 or 128 and zp uint8 of
+    the same shape (None: 8); uint8, e2m1 codes times 2^(sw - 127) with group 32."""
+    L = _lib or _load()
+    if W.dim() != 3 or W.element_size() != 1 or not W.is_contiguous():
+        raise ValueError("W must be contiguous bytes [G, N, K / 2]")
+    G, N, K = W.shape
+    K *= 2
+    (M, cols, lda), (rows, outs, ldd) = _rows(A, "A"), _rows(D, "D")
+    if cols != K or A.dtype is not _bf16:
+        raise ValueError("A must be bfloat16 [M_total, K]")
+    shape, kind = sw.shape, _w4_kinds.get(sw.dtype)
+    if kind is None or len(shape) != 3 or shape[0] != G or shape[1] != N or not sw.is_contiguous():
+        raise ValueError("sw must be contiguous [G, N, K / group]: bfloat16, float32 or uint8")
+    group = K // shape[2] if shape[2] else 32
+    if group * shape[2] != K:
+        raise ValueError("sw must hold one scale per group of channels")
+    if zp is not None and (zp.dtype is not torch.uint8 or zp.shape != shape or
+                           not zp.is_contiguous()):
+        raise ValueError("zp must be contiguous uint8 of sw's shape")
+    _i32(ms, (G,), "ms")
+    flags = 0
+    if D.dtype is _bf16:
+        flags = KG_FLAG_D_BF16
+    elif D.dtype is not _f32:
+        raise ValueError("D must be float32 or bfloat16")
+    if rows != M or outs != N:
+        raise ValueError("D must be [M_total, N]")
+    gpu = _gpu(D, A, W, sw, ms, zp)
+    rc = L.kg_fprop_w4(A.data_ptr(), lda, W.data_ptr(), sw.data_ptr(), _at(zp), D.data_ptr(), ldd,
+                       ms.data_ptr(), G, N, K, M, group, kind, flags, _on(gpu, stream))
+    if rc:
+        _fail(rc, "kg_fprop_w4")
     return D
 
 

@@ -560,6 +560,43 @@ int kg_gate_bwd(const void* X, int64_t ldx, const int32_t* idx, const float* dw,
                 const int32_t* counts, const float* dloss, int64_t T, int G, int k, int type,
                 int flags, double scale, double coef, void* dX, int64_t ldd, void* stream);
 
+/* Kinds of 4-bit weights (argument `kind` of kg_fprop_w4). */
+#define KG_W4_INT_BF16 0 /* whole numbers, w = (q - z) s, scales bf16                        */
+#define KG_W4_INT_F32 1  /* ... scales fp32                                                  */
+#define KG_W4_E2M1 2     /* e2m1 codes (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5,
+                            2, 3, 4, 6), w = e2m1(q) 2^(e - 127), scales bytes e (E8M0)       */
+
+/*
+ * kg_fprop_w4 -- enqueue kg_fprop's product y = x . w^T of expert rows with 4-bit weights:
+ *
+ *   D[t][n] = sum_k A[t][k] * w[g][n][k],  t a row of expert g
+ *
+ *   A   [M_total, K] bf16, row t at element t * lda
+ *   W   [G, N, K/2] bytes of two codes each, channel 2 i in the low half of byte i
+ *   sw  [G, N, K/group]: the scale of each `group` consecutive channels, by kind
+ *   zp  [G, N, K/group] uint8: the zero points z (0 .. 255) of KG_W4_INT_*, or NULL for 8
+ *       everywhere; NULL for KG_W4_E2M1
+ *   D   [M_total, N] fp32 (bf16 with KG_FLAG_D_BF16), row t at element t * ldd
+ *   ms  [G] int32, device memory: rows per expert, in expert order (0 for any of them)
+ *   group  32, 64 or 128 (32 for KG_W4_E2M1); K is a multiple of it
+ *   flags  KG_FLAG_D_BF16 or 0
+ *
+ * Products are exact and summed in fp32; the result is rounded once. An infinity or NaN in a row
+ * of A makes its results NaN (or an infinity); so does a magnitude above 2^100 with KG_W4_INT_*,
+ * where a group's sums pass fp32's range. Exponent bytes 2 to 252 are exact, the outer ones give
+ * weights at the ends of fp32's range (0 and 1 may count as zero, 255 gives NaN).
+ * A and W are 16-byte aligned, lda is a multiple of 8, the others are aligned by their elements
+ * (rows of D that start at 16-byte boundaries are stored faster). Errors before any launch:
+ * KG_ERR_DTYPE, KG_ERR_SHAPE (negative sizes, lda < K, ldd < N), KG_ERR_GRAN, KG_ERR_NULL,
+ * KG_ERR_ALIGN, KG_ERR_ALIAS (D overlapping an input), KG_ERR_UNSUPPORTED (G > 1024, N > 2^24,
+ * lda > 2^22, ldd > 2^30, M_total > 2^31 - 1, or more tiles than a launch has), KG_ERR_HIP. An ms
+ * that holds a negative count or does not add up to M_total is reported by kg_status
+ * (KG_ERR_KSUM) and nothing is written. G, N or M_total == 0: KG_OK, no launch.
+ */
+int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void* sw, const void* zp, void* D,
+                int64_t ldd, const int32_t* ms, int G, int N, int K, int64_t M_total, int group,
+                int kind, int flags, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
