@@ -16,5 +16,6 @@ from ._binding import (KG_BF16, KG_E4M3_F32SCALE, KG_E4M3_UE8M0, KG_ERR_ALIAS,  
 from ._binding import (KG_ADAMW_8BIT, KG_ADAMW_G_BF16, KG_ADAMW_P_BF16, KG_GATE_NORM, KG_GATE_SIGMOID,  # noqa: F401
                        KG_ROWS_BF16, KG_ROWS_F32, KG_W4_E2M1, KG_W4_INT_BF16, KG_W4_INT_F32)
 from .layer import (AdamWTable, kg_adamw, kg_combine, kg_combine_bwd, kg_dispatch,  # noqa: F401
-                    kg_dispatch_fp8, kg_fprop, kg_fprop_w4, kg_gate, kg_gate_bwd, kg_route,
-                    new_gate_workspace, new_route_workspace)
+                    kg_dispatch_fp8, kg_fprop, kg_fprop_w4, kg_gate, kg_gate_bwd,
+                    kg_orthogonalize, kg_route, new_gate_workspace, new_orthogonalize_workspace,
+                    new_route_workspace)

@@ -67,6 +67,8 @@ SIGNATURES = {
     "kg_adamw_table_bytes": (_i64, [_vp, _i32]),
     "kg_adamw_pack": (_i32, [_vp, _i32, _i32, _vp, _i64]),
     "kg_adamw": (_i32, [_vp, _i32, _i64, _i32, _f64, _f64, _f64, _f64, _f64, _i64, _vp, _vp, _vp]),
+    "kg_orthogonalize": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp]),
+    "kg_orthogonalize_workspace_bytes": (_i64, [_i32, _i32, _i32]),
     "kg_gate": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _f64, _f64, _vp, _vp, _vp,
                        _vp, _vp, _vp, _i64, _vp]),
     "kg_gate_workspace_bytes": (_i64, [_i64, _i32]),

@@ -13,7 +13,8 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libkgwgrad.so")
 # kglib.hip includes kgwgrad.hip, and that kg_requant.h and kg_dgrad.h
 SOURCES = [os.path.join(PKG, "csrc", n) for n in ("kglib.hip", "kg_fprop.hip", "kg_route.hip",
-                                                  "kg_adamw.hip", "kg_gate.hip", "kg_fprop_w4.hip")]
+                                                  "kg_adamw.hip", "kg_gate.hip", "kg_fprop_w4.hip",
+                                                  "kg_ortho.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

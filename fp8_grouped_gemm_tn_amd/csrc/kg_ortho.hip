@@ -1,0 +1,581 @@
+// kg_ortho.hip -- weight updates made nearly orthogonal on gfx950, C ABI kg_orthogonalize.
+//
+// Newton-Schulz: X = U / |U|_F, and `steps` times, on the side of the shorter axis n of n x m,
+//   A = X X^T,  B = b A + c A A,  X = a X + B X,  (a, b, c) = (3.4445, -4.7750, 2.0315),
+// which takes every singular value of X towards 1 (into 0.68 .. 1.27, not onto it).
+//
+// The work is the three products, on the fp16 MFMA (bf16's rate; every matrix here has entries
+// bounded by its singular values, so fp16's range suffices, and its 11 bits are 8 times as exact).
+// A and A A are symmetric: only tiles on one side of the diagonal are computed, and stored
+// twice. All three products are of the form C[i][j] = sum_k P[i][k] Q[j][k] with contiguous k:
+// A of rows of X, A A of rows of A, B X of rows of B and of X^T, so X is kept in both orders, and the
+// kernel that makes X writes both.
+//
+// What fp16 costs, and what is done about it. Small singular values grow by a = 3.4445 a step and
+// carry the rounding of a X with them, so the X that is multiplied by a is kept as two halves
+// (22 bits) up to the last step but one. A and B are near multiples of the identity in the end, so
+// the rounding of their diagonals, which acts as a common factor, is kept beside them in fp32. With
+// both, results are 1e-3 of their norm off 64-bit ones (gaussian, channel-scaled, low-rank and
+// decaying spectra), against 1e-2 to 3e-1 with bf16 operands.
+//
+// Powers of two bring the entries into fp16's range: X by about sqrt(m) (entries of an orthonormal
+// row are 1 / sqrt(m)), A and B by 2^13 (|A| <= 1.7, |B| <= 2.9).
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "kg_device.h"
+#include "kg_host.h"
+#include "kgwgrad.h"
+
+namespace kg {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+constexpr float kScaleA = 0x1p13f, kScaleB = 0x1p13f, kLow = 0x1p11f;
+constexpr int kNormChunks = 64;  // partial sums of squares per matrix
+constexpr int kOrthoMax = 1 << 16;
+
+struct OParams {
+  const void* U;
+  unsigned short* O;
+  double* parts;  // [G][kNormChunks]
+  unsigned short *X, *XT, *XN, *LO, *A, *B;  // XN: the X^T that a step writes
+  float *dA, *dB;
+  int64_t sx, sxt, sa;  // elements of a matrix's X, XT and A
+  float cx;             // scale of X
+  int G, R, C, n, m, np, mp, ldn, ldm;
+  int b16, wide, tiles_i, tiles_j, per;  // per: tiles of a matrix
+  int low_in, low_out;
+};
+
+__device__ __forceinline__ float u_at(const OParams& p, int64_t i) {
+  return p.b16 ? __builtin_bit_cast(float, (uint32_t)((const unsigned short*)p.U)[i] << 16)
+               : ((const float*)p.U)[i];
+}
+
+// ---------------------------------------------------------------------------- norm, first X
+
+// Sums of squares in 64 bits (fp32 squares of gradients may leave its range), in a fixed order.
+__global__ __launch_bounds__(256) void kg_ortho_norm_kernel(OParams p) {
+  __shared__ double sums[4];
+  const int64_t size = (int64_t)p.R * p.C, base = (int64_t)blockIdx.y * size;
+  const int64_t per = (size + kNormChunks * 1024 - 1) / (kNormChunks * 1024) * 1024;
+  const int64_t from = blockIdx.x * per, to = from + per < size ? from + per : size;
+  double s = 0;
+  int64_t i = from + 4 * threadIdx.x;
+  for (; i + 4 <= to; i += 1024) {
+    float x[4];
+    if (p.b16) {
+      typedef unsigned short h4 __attribute__((ext_vector_type(4), aligned(2)));
+      const h4 h = *(const h4*)((const unsigned short*)p.U + base + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = __builtin_bit_cast(float, (uint32_t)h[e] << 16);
+    } else {
+      typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+      const f4 f = *(const f4*)((const float*)p.U + base + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = f[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s = fma((double)x[e], (double)x[e], s);
+  }
+  for (; i < to && i < from + per; ++i) {
+    const double x = u_at(p, base + i);
+    s = fma(x, x, s);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    p.parts[blockIdx.y * kNormChunks + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+
+// X and X^T of U / |U|, scaled, with their low halves; zeros in the padding. One 64 x 64 tile
+// per workgroup, turned in LDS.
+__global__ __launch_bounds__(256) void kg_ortho_init_kernel(OParams p) {
+  __shared__ unsigned short hi[64][72], lo[64][72];
+  __shared__ double inv_s;
+  const int g = blockIdx.y, t = threadIdx.x;
+  if (t < 64) {
+    double s = p.parts[g * kNormChunks + t];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+    if (t == 0) inv_s = s > 0 ? (double)p.cx / sqrt(s) : s == 0 ? 0.0 : s;  // NaN stays
+  }
+  __syncthreads();
+  const double inv = inv_s;
+  // rows and columns of U, and of the padded matrix
+  const int rp = p.wide ? p.np : p.mp, cp = p.wide ? p.mp : p.np;
+  const int across = cp / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
+  const int64_t base = (int64_t)g * p.R * p.C;
+  // direct: the order of U's rows; turned: the other one
+  unsigned short* direct = p.wide ? p.X + g * p.sx : p.XT + g * p.sxt;
+  unsigned short* turned = p.wide ? p.XT + g * p.sxt : p.X + g * p.sx;
+  unsigned short* low = p.LO + g * p.sxt;  // in the order of X^T
+  const int ldd = p.wide ? p.ldm : p.ldn, ldt = p.wide ? p.ldn : p.ldm;
+  const int r = t >> 2, c = (t & 3) * 16;
+  v8h h[2], l[2];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const bool in = r0 + r < p.R && c0 + c + e < p.C;
+    const float v =
+        in ? (float)((double)u_at(p, base + (int64_t)(r0 + r) * p.C + c0 + c + e) * inv) : 0.f;
+    const _Float16 top = (_Float16)v;
+    const _Float16 rest = (_Float16)((v - (float)top) * kLow);
+    h[e >> 3][e & 7] = top;
+    l[e >> 3][e & 7] = rest;
+    hi[c + e][r] = __builtin_bit_cast(unsigned short, top);
+    lo[c + e][r] = __builtin_bit_cast(unsigned short, rest);
+  }
+  const int64_t at = (int64_t)(r0 + r) * ldd + c0 + c;
+  *(v8h*)(direct + at) = h[0];
+  *(v8h*)(direct + at + 8) = h[1];
+  if (!p.wide) {
+    *(v8h*)(low + at) = l[0];
+    *(v8h*)(low + at + 8) = l[1];
+  }
+  __syncthreads();
+  const int64_t to = (int64_t)(c0 + r) * ldt + r0 + c;
+  *(v4i*)(turned + to) = *(const v4i*)&hi[r][c];
+  *(v4i*)(turned + to + 8) = *(const v4i*)&hi[r][c + 8];
+  if (p.wide) {
+    *(v4i*)(low + to) = *(const v4i*)&lo[r][c];
+    *(v4i*)(low + to + 8) = *(const v4i*)&lo[r][c + 8];
+  }
+}
+
+// ------------------------------------------------------------------------------- products
+
+// BS x BS results per workgroup of 8 waves (4 along j, 2 along i), two LDS stages of 64 k (128
+// bytes) of BS rows of P and of Q. The loop is kg_fprop's: Q's fragments are read a block ahead, loads go
+// straight to LDS and are spread over the MFMAs, waits count them.
+template <int BS_, int PER_CU_>
+struct OCfg {
+  static constexpr int BS = BS_, PER_CU = PER_CU_, THREADS = 512, WT = 4, WN = 2, TK = 64;
+  static constexpr int TT = BS / WT / 16, NI = BS / WN / 16;
+  static constexpr int OPW = BS * 128, STAGE = 2 * OPW;
+  static constexpr int LW = BS / 64, LOADS = 2 * LW;
+  static_assert(NI % 2 == 0 && TT * 16 * NI * 16 * 2 * 8 <= 2 * STAGE, "a wave's results fit in LDS");
+};
+
+// (as in kg_fprop: row m of MFMA row tile i holds result row orow(i, m) of the wave's, so a
+// lane's four results of two tiles are eight neighbours)
+__device__ __forceinline__ constexpr int orow(int i, int m) {
+  return 32 * (i >> 1) + 8 * (m >> 2) + 4 * (i & 1) + (m & 3);
+}
+// LDS slot of chunk c of a row is c ^ key, with the key m & 7 of the MFMA row (column) m.
+__device__ __forceinline__ constexpr int okey_q(int r) { return r & 7; }
+__device__ __forceinline__ constexpr int okey_p(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
+
+template <int N>
+__device__ __forceinline__ void o_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(N) & ~0xF00);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ v4f mfma_f16(const v8h& a, const v8h& b, const v4f& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+enum { kGram, kPoly, kStep, kLast };  // A; B; X; X as the result
+
+// Tile idx of the triangle of T x T tiles: panels of 4 rows I, in each J upwards.
+__device__ __forceinline__ void triangle(int idx, int T, int* I, int* J) {
+  for (int r = 0;; r += 4) {
+    const int rows = min(4, T - r), head = rows * (rows + 1) / 2;
+    const int n = head + rows * (T - r - rows);
+    if (idx < n) {
+      if (idx >= head) {
+        *J = r + rows + (idx - head) / rows;
+        *I = r + (idx - head) % rows;
+      } else {
+        int j = 0;
+        while (idx > j) idx -= ++j;
+        *J = r + j;
+        *I = r + idx;
+      }
+      return;
+    }
+    idx -= n;
+  }
+}
+
+template <class C, int MODE>
+__global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_ortho_kernel(OParams p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int TT = C::TT, NI = C::NI;
+  constexpr bool SYM = MODE == kGram || MODE == kPoly;
+  const int total = p.G * p.per, grid = gridDim.x, b = blockIdx.x;
+  const int slot = (grid % 8 == 0 && total > grid) ? (b % 8) * (grid / 8) + b / 8 : b;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int q = lane >> 4, jl = lane & 15;
+  const int wt = w % C::WT, wn = w / C::WT;
+  const int c0 = 16 * (q ^ (jl & 7)), c1 = 16 * ((q + 4) ^ (jl & 7));
+  const unsigned char* fragp = smem + (wn * NI * 16 + orow(0, jl)) * 128;
+  const unsigned char* fragq = smem + C::OPW + (wt * TT * 16 + jl) * 128;
+  const uint32_t lds = lds_addr(smem);
+  const int ld = MODE == kGram ? p.ldm : p.ldn, nk = (MODE == kGram ? p.mp : p.np) / C::TK;
+  const int rows_j = SYM ? p.np : p.mp;
+  // this lane's row and chunk of a load of 8 rows, for P and Q
+  const int lr = 8 * w + (lane >> 3);
+  const uint32_t offp = (uint32_t)(lr * ld * 2 + 16 * ((lane & 7) ^ okey_p(lr)));
+  const uint32_t offq = (uint32_t)(lr * ld * 2 + 16 * ((lane & 7) ^ okey_q(lr)));
+  for (int base = 0; base < total; base += grid) {
+    const int idx = base + slot;
+    if (idx >= total) break;
+    const int g = idx / p.per;
+    int I, J;
+    if constexpr (SYM) {
+      triangle(idx - g * p.per, p.tiles_i, &I, &J);
+    } else {
+      const int r = idx - g * p.per, per_panel = 4 * p.tiles_j, panel = r / per_panel;
+      const int wi = r - panel * per_panel, pm = min(4, p.tiles_i - 4 * panel);
+      I = 4 * panel + wi % pm, J = wi / pm;
+    }
+    const int i0 = uniform(I) * C::BS, j0 = uniform(J) * C::BS;
+    const unsigned short* P = MODE == kGram   ? p.X + g * p.sx
+                              : MODE == kPoly ? p.A + g * p.sa
+                                              : p.B + g * p.sa;
+    const unsigned short* Q = SYM ? P : p.XT + g * p.sxt;
+    const unsigned char* Pb = (const unsigned char*)(P + (int64_t)i0 * ld);
+    const unsigned char* Qb = (const unsigned char*)(Q + (int64_t)j0 * ld);
+    const uint32_t pbytes = (uint32_t)((min(C::BS, p.np - i0) - 1) * ld * 2 + 128);
+    const uint32_t qbytes = (uint32_t)((min(C::BS, rows_j - j0) - 1) * ld * 2 + 128);
+    // rows that the matrix lacks and blocks past the last one read as zeros
+    auto load_p = [&](int kb, int x) {
+      load16_lds(make_rsrc(Pb + (int64_t)kb * 128, kb < nk ? pbytes : 0u),
+                 lds + (kb & 1) * C::STAGE + 1024 * (w + 8 * x), offp + (uint32_t)(64 * x * ld * 2));
+    };
+    auto load_q = [&](int kb, int x) {
+      load16_lds(make_rsrc(Qb + (int64_t)kb * 128, kb < nk ? qbytes : 0u),
+                 lds + (kb & 1) * C::STAGE + C::OPW + 1024 * (w + 8 * x),
+                 offq + (uint32_t)(64 * x * ld * 2));
+    };
+    v4f acc[NI][TT];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
+    v8h qf[TT][2], pf[2][2];
+    auto read_q = [&](int kb, int tt) {
+      const unsigned char* r = fragq + (kb & 1) * C::STAGE + 16 * tt * 128;
+      qf[tt][0] = *(const v8h*)(r + c0);
+      qf[tt][1] = *(const v8h*)(r + c1);
+    };
+    auto read_p = [&](int kb, int i) {
+      const unsigned char* r = fragp + (kb & 1) * C::STAGE + orow(i, 0) * 128;
+      pf[i & 1][0] = *(const v8h*)(r + c0);
+      pf[i & 1][1] = *(const v8h*)(r + c1);
+    };
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int x = 0; x < C::LW; ++x) load_q(kb, x);
+#pragma unroll
+      for (int x = 0; x < C::LW; ++x) load_p(kb, x);
+    }
+    o_meet<C::LOADS>();
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) read_q(0, tt);
+    o_meet<C::LOADS>();
+    for (int kb = 0; kb < nk; ++kb) {
+      constexpr int S = NI * 2 * TT, LASTI = S - 2 * TT;  // MFMAs of a block, and before the last i
+      read_p(kb, 0);
+#pragma unroll
+      for (int u = 0; u < S; ++u) {
+        const int i = u / (2 * TT), h = u / TT % 2, tt = u % TT;
+        // Q's next block is there, P's block has been read by every wave
+        if (u == LASTI) o_meet<C::LOADS>();
+        if (h == 0 && tt == 0 && i + 1 < NI) read_p(kb, i + 1);
+        acc[i][tt] = mfma_f16(pf[i & 1][h], qf[tt][h], acc[i][tt]);
+        if (i == NI - 1 && h == 1) read_q(kb + 1, tt);  // (past the last block: not used)
+#pragma unroll
+        for (int x = 0; x < C::LW; ++x) {
+          if (x * LASTI / C::LW == u) load_q(kb + 2, x);
+          if (LASTI + x * 2 * TT / C::LW == u) load_p(kb + 2, x);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // P's next block is there, Q's has been read by every wave
+      o_meet<C::LOADS>();
+    }
+    // No load is under way into the LDS that turns the results.
+    o_meet<0>();
+    unsigned char* turn = smem + w * (TT * 16 * NI * 16 * 2);  // [j][i] of this wave
+    const int iw = i0 + wn * NI * 16, jw = j0 + wt * TT * 16;
+    const bool mirror = !SYM || I != J;
+    unsigned short* out = MODE == kGram   ? p.A + g * p.sa
+                          : MODE == kPoly ? p.B + g * p.sa
+                                          : p.XN + g * p.sxt;
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      const int j = jw + 16 * tt + jl;
+#pragma unroll
+      for (int i2 = 0; i2 < NI / 2; ++i2) {
+        const int i = iw + 32 * i2 + 8 * q;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[2 * i2 + (e >> 2)][tt][e & 3];
+        const bool in = j < rows_j && i < p.np;
+        const int64_t at = (int64_t)j * p.ldn + i;
+        v8h o;
+        if constexpr (MODE == kGram) {
+          const float s = kScaleA / (p.cx * p.cx);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] *= s;
+            o[e] = (_Float16)v[e];
+          }
+        } else if constexpr (MODE == kPoly) {
+          v8h a = {};
+          float di[8], dj = 0.f;
+          if (in) {
+            a = *(const v8h*)(p.A + g * p.sa + at);
+            dj = p.dA[g * p.np + j];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) di[e] = in ? p.dA[g * p.np + i + e] : 0.f;
+          constexpr float fb = kScaleB / kScaleA * kNsB, fc = kScaleB / (kScaleA * kScaleA) * kNsC;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = (float)a[e];
+            v[e] = fmaf(fc, fmaf(di[e] + dj, x, v[e]), fb * (i + e == j ? x + dj : x));
+            o[e] = (_Float16)v[e];
+          }
+        } else {
+          v8h x = {}, l = {};
+          float di[8];
+          if (in) {
+            x = *(const v8h*)(p.XT + g * p.sxt + at);
+            if (p.low_in) l = *(const v8h*)(p.LO + g * p.sxt + at);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) di[e] = in ? p.dB[g * p.np + i + e] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float st = fmaf((float)l[e], 1 / kLow, (float)x[e]);
+            v[e] = fmaf(kNsA + di[e] / kScaleB, st, v[e] / kScaleB);
+            if constexpr (MODE == kStep) o[e] = (_Float16)v[e];
+            else o[e] = __builtin_bit_cast(_Float16, (__bf16)(v[e] / p.cx));
+          }
+        }
+        if constexpr (SYM) {
+          float* d = MODE == kGram ? p.dA : p.dB;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (i + e == j && in) d[g * p.np + j] = v[e] - (float)o[e];
+        }
+        if constexpr (MODE == kLast) {
+          if (!p.wide && j < p.m && i < p.n) {  // O [m, n]
+            unsigned short* d = p.O + ((int64_t)g * p.m + j) * p.n + i;
+            if (i + 8 <= p.n) {
+              typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+              *(v4i_any*)d = __builtin_bit_cast(v4i, o);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const _Float16 one = o[e];  // (a bit cast of the element itself reads the first one)
+                if (i + e < p.n) d[e] = __builtin_bit_cast(unsigned short, one);
+              }
+            }
+          }
+        } else if (in) {
+          *(v8h*)(out + at) = o;
+        }
+        if constexpr (MODE == kStep) {
+          if (p.low_out && in) {
+            v8h l;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) l[e] = (_Float16)((v[e] - (float)o[e]) * kLow);
+            *(v8h*)(p.LO + g * p.sxt + at) = l;
+          }
+        }
+        if (mirror && (MODE != kLast || p.wide)) {
+          const int jr = 16 * tt + jl, c = 4 * i2 + q;
+          *(v8h*)(turn + jr * (NI * 32) + 16 * (c ^ (jr & (2 * NI - 1)))) = o;
+        }
+      }
+    }
+    if (mirror && (MODE != kLast || p.wide)) {
+      // the other order: lane c of 16 gets column i = c of 4 rows j per read
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int r4 = (lane & 15) >> 2, c4 = lane & 3;
+      unsigned short* mir = MODE == kGram   ? p.A + g * p.sa
+                            : MODE == kPoly ? p.B + g * p.sa
+                                            : p.X + g * p.sx;
+      const int ldo = SYM ? p.ldn : p.ldm;
+#pragma unroll
+      for (int ib = 0; ib < NI; ++ib)
+#pragma unroll
+        for (int jb = 0; jb < (TT + 1) / 2; ++jb) {
+          const int jr = 32 * jb + 8 * q;
+          const int c = 2 * ib + (c4 >> 1);
+          v4bf half[2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int row = jr + 4 * s + r4;
+            half[s] = tr16(turn + row * (NI * 32) + 16 * (c ^ (row & (2 * NI - 1))) + 8 * (c4 & 1));
+          }
+          const v2i x = __builtin_bit_cast(v2i, half[0]), y = __builtin_bit_cast(v2i, half[1]);
+          const v4i o = {x.x, x.y, y.x, y.y};
+          const int i = iw + 16 * ib + jl, j = jw + jr;
+          if constexpr (MODE == kLast) {
+            if (i < p.n && j < p.m) {  // O [n, m]
+              unsigned short* d = p.O + ((int64_t)g * p.n + i) * p.m + j;
+              if (j + 8 <= p.m) {
+                typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+                *(v4i_any*)d = o;
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (j + e < p.m) d[e] = (unsigned short)((uint32_t)o[e >> 1] >> (16 * (e & 1)));
+              }
+            }
+          } else if (i < p.np && j < rows_j) {
+            *(v4i*)(mir + (int64_t)i * ldo + j) = o;
+          }
+        }
+    }
+    __syncthreads();  // the results have left the LDS that the next tile loads into
+  }
+}
+
+struct OSizes {
+  int n, m, np, mp, ldn, ldm;
+  int64_t sx, sxt, sa;
+  // byte offsets in the workspace
+  int64_t x, xt[2], lo, a, b, da, db, total;
+};
+
+// Rows that lie a multiple of 4096 bytes apart would use few of the memory's channels.
+static int o_ld(int x) { return x % 2048 == 0 ? x + 64 : x; }
+
+static OSizes o_sizes(int G, int R, int C) {
+  OSizes s;
+  s.n = R < C ? R : C, s.m = R < C ? C : R;
+  s.np = (s.n + 63) / 64 * 64, s.mp = (s.m + 63) / 64 * 64;
+  s.ldn = o_ld(s.np), s.ldm = o_ld(s.mp);
+  s.sx = (int64_t)s.np * s.ldm, s.sxt = (int64_t)s.mp * s.ldn, s.sa = (int64_t)s.np * s.ldn;
+  int64_t at = (int64_t)G * kNormChunks * 8;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  s.x = take(2 * s.sx * G);
+  s.xt[0] = take(2 * s.sxt * G);
+  s.xt[1] = take(2 * s.sxt * G);
+  s.lo = take(2 * s.sxt * G);
+  s.a = take(2 * s.sa * G);
+  s.b = take(2 * s.sa * G);
+  s.da = take(4ll * s.np * G);
+  s.db = take(4ll * s.np * G);
+  s.total = at;
+  return s;
+}
+
+static bool o_taken(int G, int R, int C) {
+  return G <= kOrthoMax - 1 && R <= kOrthoMax && C <= kOrthoMax;
+}
+
+template <class C, int MODE>
+static int o_launch(OParams& p, int cus, int dev, void* stream) {
+  constexpr int LDS = 2 * C::STAGE;
+  static std::mutex mu;
+  static bool set[64];
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!set[dev] &&
+        hipFuncSetAttribute((const void*)kg_ortho_kernel<C, MODE>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, LDS) != hipSuccess)
+      return KG_ERR_HIP;
+    set[dev] = true;
+  }
+  constexpr bool SYM = MODE == kGram || MODE == kPoly;
+  p.tiles_i = (p.np + C::BS - 1) / C::BS;
+  p.tiles_j = SYM ? p.tiles_i : (p.mp + C::BS - 1) / C::BS;
+  const int64_t per = SYM ? (int64_t)p.tiles_i * (p.tiles_i + 1) / 2 : (int64_t)p.tiles_i * p.tiles_j;
+  if (per * p.G > INT32_MAX - 4096) return KG_ERR_UNSUPPORTED;
+  p.per = (int)per;
+  const int64_t most = (int64_t)cus * C::PER_CU;
+  return launch(kg_ortho_kernel<C, MODE>, per * p.G < most ? per * p.G : most, C::THREADS, LDS,
+                stream, p);
+}
+
+// Tiles of 256 where they give every compute unit one, else of 128.
+template <int MODE>
+static int o_product(OParams& p, int cus, int dev, void* stream) {
+  constexpr bool SYM = MODE == kGram || MODE == kPoly;
+  const int64_t ti = (p.np + 255) / 256, tj = (p.mp + 255) / 256;
+  if (p.G * (SYM ? ti * (ti + 1) / 2 : ti * tj) >= cus / 2)
+    return o_launch<OCfg<256, 1>, MODE>(p, cus, dev, stream);
+  return o_launch<OCfg<128, 2>, MODE>(p, cus, dev, stream);
+}
+
+}  // namespace kg
+
+extern "C" int64_t kg_orthogonalize_workspace_bytes(int G, int R, int C) {
+  using namespace kg;
+  if (G < 0 || R < 0 || C < 0 || !o_taken(G, R, C)) return -1;
+  return G == 0 || R == 0 || C == 0 ? 0 : o_sizes(G, R, C).total;
+}
+
+extern "C" int kg_orthogonalize(const void* U, void* O, int G, int R, int C, int type, int steps,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+  using namespace kg;
+  if (type != KG_ROWS_BF16 && type != KG_ROWS_F32) return KG_ERR_DTYPE;
+  if (G < 0 || R < 0 || C < 0 || steps < 1 || workspace_bytes < 0) return KG_ERR_SHAPE;
+  if (!o_taken(G, R, C) || steps > 64) return KG_ERR_UNSUPPORTED;
+  if (G == 0 || R == 0 || C == 0) return KG_OK;
+  if (!U || !O || !workspace) return KG_ERR_NULL;
+  const size_t e = type == KG_ROWS_BF16 ? 2 : 4;
+  if (((uintptr_t)U & (e - 1)) || ((uintptr_t)O & 1) || ((uintptr_t)workspace & 255))
+    return KG_ERR_ALIGN;
+  const OSizes s = o_sizes(G, R, C);
+  if (workspace_bytes < s.total) return KG_ERR_SHAPE;
+  const size_t count = (size_t)G * R * C;
+  if (ranges_overlap(workspace, s.total, U, count * e) ||
+      ranges_overlap(workspace, s.total, O, count * 2))
+    return KG_ERR_ALIAS;
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return KG_ERR_HIP;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+    return KG_ERR_HIP;
+  char* ws = (char*)workspace;
+  OParams p;
+  p.U = U, p.O = (unsigned short*)O, p.parts = (double*)ws;
+  p.X = (unsigned short*)(ws + s.x);
+  p.LO = (unsigned short*)(ws + s.lo);
+  p.A = (unsigned short*)(ws + s.a);
+  p.B = (unsigned short*)(ws + s.b);
+  p.dA = (float*)(ws + s.da), p.dB = (float*)(ws + s.db);
+  p.sx = s.sx, p.sxt = s.sxt, p.sa = s.sa;
+  p.cx = (float)ldexp(1.0, (int)lrint(log2((double)s.m) / 2));
+  p.G = G, p.R = R, p.C = C, p.n = s.n, p.m = s.m, p.np = s.np, p.mp = s.mp;
+  p.ldn = s.ldn, p.ldm = s.ldm;
+  p.b16 = type == KG_ROWS_BF16, p.wide = R <= C;
+  p.XT = (unsigned short*)(ws + s.xt[0]), p.XN = (unsigned short*)(ws + s.xt[1]);
+  int rc = launch2(kg_ortho_norm_kernel, kNormChunks, G, 256, 0, stream, p);
+  if (rc == KG_OK)
+    rc = launch2(kg_ortho_init_kernel, (int64_t)(s.np / 64) * (s.mp / 64), G, 256, 0, stream, p);
+  for (int t = 0; t < steps && rc == KG_OK; ++t) {
+    p.low_in = t < steps - 1, p.low_out = t + 1 < steps - 1;
+    rc = o_product<kGram>(p, cus, dev, stream);
+    if (rc == KG_OK) rc = o_product<kPoly>(p, cus, dev, stream);
+    if (rc == KG_OK)
+      rc = t < steps - 1 ? o_product<kStep>(p, cus, dev, stream)
+                         : o_product<kLast>(p, cus, dev, stream);
+    unsigned short* x = p.XT;
+    p.XT = p.XN, p.XN = x;
+  }
+  return rc;
+}

@@ -1,7 +1,8 @@
 """Bindings of the operators around an expert layer's products (the C ABI in
 include/kgwgrad.h): the sort of tokens by expert and the row copies (kg_route, kg_dispatch,
 kg_dispatch_fp8, kg_combine, kg_combine_bwd), the router's choice in front of it (kg_gate,
-kg_gate_bwd), the forward products (kg_fprop, kg_fprop_w4) and the AdamW step (AdamWTable, kg_adamw).
+kg_gate_bwd), the forward products (kg_fprop, kg_fprop_w4) and the steps
+of the optimizers (AdamWTable, kg_adamw; kg_orthogonalize).
 
 Argument marshalling only, as in _binding. With `stream` given, what a call makes is of that
 stream's memory, and the current stream may use it once it waits for `stream`; the order of the
@@ -519,3 +520,37 @@ def kg_adamw(table, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step
         table.used_on(on, stream)
     if rc:
         _fail(rc, "kg_adamw")
+
+
+def new_orthogonalize_workspace(G, R, C, device):
+    """The workspace of kg_orthogonalize for G matrices [R, C]; keep it for later calls of these
+    sizes."""
+    n = _load().kg_orthogonalize_workspace_bytes(G, R, C)
+    if n < 0:
+        _fail(KG_ERR_SHAPE, "kg_orthogonalize_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kg_orthogonalize(U, O=None, steps=5, ws=None, stream=None):
+    """The nearly orthogonal form of weight updates by Newton-Schulz steps: U [R, C] or [G, R, C]
+    (bfloat16 or float32, contiguous), O bfloat16 of U's shape (made if not given; may be U); ws:
+    new_orthogonalize_workspace (made if not given). Returns O."""
+    L = _lib or _load()
+    ty, shape = _row_type(U.dtype, "U"), U.shape
+    if len(shape) not in (2, 3) or not U.is_contiguous():
+        raise ValueError("U must be contiguous [R, C] or [G, R, C]")
+    G, R, C = shape if len(shape) == 3 else (1, *shape)
+    if O is None:
+        O = _made(shape, _bf16, U, stream)
+    _expert_rows(O, shape, _bf16, "O")
+    if ws is None:
+        n = L.kg_orthogonalize_workspace_bytes(G, R, C)
+        if n > 0:
+            ws = _made((n,), torch.uint8, U, stream, back=False)
+    at, size = _workspace(ws)
+    gpu = _gpu(U, O, ws)
+    rc = L.kg_orthogonalize(U.data_ptr(), O.data_ptr(), G, R, C, ty, steps, at, size,
+                            _on(gpu, stream))
+    if rc:
+        _fail(rc, "kg_orthogonalize")
+    return O

@@ -597,6 +597,35 @@ int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void* sw, const
                 int64_t ldd, const int32_t* ms, int G, int N, int K, int64_t M_total, int group,
                 int kind, int flags, void* stream);
 
+/*
+ * kg_orthogonalize -- enqueue the nearly orthogonal form of weight updates by Newton-Schulz steps
+ * (the Muon optimiser's step): for each of G matrices U [R, C], X = U / |U|_F (0 for zeros) and
+ * `steps` times, on the side of the shorter axis,
+ *
+ *   A = X X^T,  X = 3.4445 X + (-4.7750 A + 2.0315 A A) X      (X^T X and from the right, if R > C)
+ *
+ * which leaves U's singular vectors and takes its singular values into 0.68 .. 1.27 (those above
+ * about 1/300 of the norm in 5 steps; each step multiplies smaller ones by 3.4).
+ *
+ *   U  [G, R, C] contiguous (type: KG_ROWS_BF16 or KG_ROWS_F32)
+ *   O  [G, R, C] bf16 out, contiguous; may overlap U
+ *   workspace  device memory of kg_orthogonalize_workspace_bytes(G, R, C) bytes, 256-byte aligned;
+ *        needs no initialisation. Calls that share one must not run concurrently
+ *
+ * The products take fp16 operands with fp32 sums; what their rounding would add to small singular
+ * values and to the diagonals is carried beside them. Results are within 2e-3 of their norm, before
+ * their rounding to bf16, of the same steps in 64 bits. A NaN or an infinity in a matrix makes NaNs
+ * of that matrix's result alone. Nothing depends on timing. Errors before any launch: KG_ERR_DTYPE,
+ * KG_ERR_SHAPE (negative sizes, steps < 1, a workspace that is too small), KG_ERR_NULL,
+ * KG_ERR_ALIGN (U and O by their elements), KG_ERR_ALIAS (the workspace overlapping U or O),
+ * KG_ERR_UNSUPPORTED (G > 65535, R or C > 65536, steps > 64, more tiles than a launch has),
+ * KG_ERR_HIP. G, R or C == 0: KG_OK, no launch.
+ */
+int kg_orthogonalize(const void* U, void* O, int G, int R, int C, int type, int steps,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+/* Workspace of kg_orthogonalize in bytes, or -1 for sizes it does not take. */
+int64_t kg_orthogonalize_workspace_bytes(int G, int R, int C);
+
 #ifdef __cplusplus
 }
 #endif
