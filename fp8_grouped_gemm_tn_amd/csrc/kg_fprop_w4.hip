@@ -6,19 +6,13 @@
 //   whole numbers  w = (q - z) s, q 0 .. 15, one scale s (and zero point z, or 8) per `group` channels
 //   e2m1           w = e2m1(q) 2^(e - 127), one exponent byte e per 32 channels
 //
-// Products are exact on the bf16 MFMA: e2m1 values times a power of two are bf16 numbers, made by
-// the conversion instruction that takes the scale along; whole-number codes become 16 + q by
-// putting q into the mantissa bits of the bf16 number 16. A group's sum of x (16 + q) then loses
-// (16 + z) times the group's sum of x, which an MFMA with ones gives in the lanes that need it, and
-// is scaled and added in fp32. The result is rounded once.
-//
-// Tokens are the MFMA's rows, outputs its columns: a lane holds one output (of each tile), whose
-// codes and scales it reads itself, so scales need no exchange between lanes. A wave's outputs are
-// dealt to its tiles in turn, so a lane has neighbouring ones and stores them together.
+// Products are exact on the bf16 MFMA and summed in fp32: e2m1 values times a power of two are bf16
+// numbers, made by the conversion instruction that takes the scale along; whole numbers are bf16
+// numbers before their scale, which multiplies the group's sum. The result is rounded once.
 //
 // Two kernels, as in kg_fprop. Streaming (few rows): W goes from memory into registers, the
-// contraction axis is split over a workgroup's waves; W's bytes bound it. Tiled: tokens go through
-// LDS, each wave reads and widens its own outputs' codes.
+// contraction axis is split over a workgroup's waves; W's bytes bound it. Tiled: a workgroup widens
+// its outputs' codes once into LDS, beside its tokens.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -35,7 +29,7 @@ namespace kg {
 struct WParams {
   const unsigned char* A;   // [M_total, K] bf16, row stride lda elements
   const unsigned char* W;   // [G, N, K / 2]
-  const void* sw;           // [G, N, K / group]
+  const unsigned char* sw;  // [G, N, K / group] bf16, fp32 or bytes
   const unsigned char* zp;  // the same shape, or null
   void* D;                  // [M_total, N] fp32 or bf16, row stride ldd
   const int32_t* ms;        // [G]
@@ -43,161 +37,59 @@ struct WParams {
   int64_t M_total, lda, ldd;
   int G, N, K;
   int tiles_n;
+  int lds_rows;  // token rows that the streaming kernel's LDS holds
 };
 
 // Formats: whole numbers by channels per scale, and e2m1.
 constexpr int kE2M1 = 0;
-// Scales that a lane holds per block of 128 channels (e2m1: of its own 32 channels).
 template <int GRP>
-constexpr int kScales = GRP == kE2M1 || GRP == 128 ? 1 : 128 / GRP;
+constexpr int kPerScale = GRP == kE2M1 ? 32 : GRP;  // channels
+template <int GRP, bool SB>
+constexpr int kScaleBytes = GRP == kE2M1 ? 1 : SB ? 2 : 4;
 
-// Two codes (a byte) become 16 + q: the byte goes into the upper half of both 16-bit lanes, from
-// where the shifts bring either nibble to bits 3 .. 6.
-typedef unsigned short v2us __attribute__((ext_vector_type(2)));
-template <int B>
-__device__ __forceinline__ int two_codes(uint32_t x) {
-  v2us h = __builtin_bit_cast(v2us, __builtin_amdgcn_perm(x, x, 0x000C000Cu | B << 24 | B << 8));
-  h = h >> v2us{5, 9};
-  return (int)((__builtin_bit_cast(uint32_t, h) & 0x00780078u) | 0x41804180u);
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)bytes, kRsrcWord3);
+}
+__device__ __forceinline__ v4i load16(Rsrc r, uint32_t off) {
+  typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(v4i, (v4u)__builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+__device__ __forceinline__ v2i load8(Rsrc r, uint32_t off) {
+  typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(v2i, (v2u)__builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
+}
+__device__ __forceinline__ uint32_t load4(Rsrc r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
+}
+__device__ __forceinline__ uint32_t load2(Rsrc r, uint32_t off) {
+  return (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+}
+__device__ __forceinline__ uint32_t load1(Rsrc r, uint32_t off) {
+  return (unsigned char)__builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, 0);
+}
+__device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
+
+// Eight e2m1 codes times 2^(e - 127), of which `scale` has the exponent bits.
+__device__ __forceinline__ v8bf eight_e2m1(uint32_t x, float scale) {
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 0);
+  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 1);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 2);
+  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 3);
+  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Eight codes as the MFMA reads them.
-template <int GRP>
-__device__ __forceinline__ v8bf eight_codes(uint32_t x, float scale) {
-  if constexpr (GRP == kE2M1) {
-    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 0);
-    const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 1);
-    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 2);
-    const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 3);
-    return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-  } else {
-    return __builtin_bit_cast(
-        v8bf, v4i{two_codes<0>(x), two_codes<1>(x), two_codes<2>(x), two_codes<3>(x)});
+// Eight whole numbers minus z, as bf16 (exact: at most 8 bits).
+__device__ __forceinline__ v8bf eight_less(uint32_t x, float z) {
+  const uint32_t even = x & 0x0F0F0F0Fu, odd = (x >> 4) & 0x0F0F0F0Fu;
+  v4i r;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float lo = (float)((even >> (8 * b)) & 0xFF) - z, hi = (float)((odd >> (8 * b)) & 0xFF) - z;
+    r[b] = (int)__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi),
+                                      __builtin_bit_cast(uint32_t, lo), 0x07060302);
   }
-}
-
-// A lane's 32 channels of one block: lane quad q reads the bytes of channels 32 q .. 32 q + 31 of
-// its output, and word j of them meets the tokens' channels chunk<GRP>(q, j) .. + 7. With scales
-// per 32 or 64 channels the quads exchange words (a 4 x 4 transposition), so that MFMA j covers
-// channels 32 j .. 32 j + 31 alone.
-template <int GRP>
-__device__ __forceinline__ constexpr int chunk(int q, int j) {  // of 8 channels
-  return GRP == kE2M1 || GRP == 128 ? 4 * q + j : 4 * j + q;
-}
-template <int GRP>
-__device__ __forceinline__ void deal(v4i& x) {
-  if constexpr (GRP == 32 || GRP == 64) {
-    auto a = __builtin_amdgcn_permlane32_swap((unsigned)x.x, (unsigned)x.z, false, false);
-    auto b = __builtin_amdgcn_permlane32_swap((unsigned)x.y, (unsigned)x.w, false, false);
-    auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    x = v4i{(int)c[0], (int)c[1], (int)d[0], (int)d[1]};
-  }
-}
-
-// A lane's scales of one block (and what is subtracted per unit of x: 16 + z).
-template <int GRP>
-struct Scales {
-  float s[kScales<GRP>], z[kScales<GRP>];
-};
-typedef unsigned short us2_any __attribute__((ext_vector_type(2), aligned(2)));
-typedef unsigned short us4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f2_any __attribute__((ext_vector_type(2), aligned(4)));
-typedef float f4_any __attribute__((ext_vector_type(4), aligned(4)));
-typedef unsigned char uc2_any __attribute__((ext_vector_type(2), aligned(1)));
-typedef unsigned char uc4_any __attribute__((ext_vector_type(4), aligned(1)));
-__device__ __forceinline__ float bf(unsigned short h) {
-  return __builtin_bit_cast(float, (uint32_t)h << 16);
-}
-
-// Scales of block kb of the output whose scales begin at element `at`; `left` groups of this
-// block exist (kScales unless TAIL).
-template <int GRP, bool SB, bool TAIL>
-__device__ __forceinline__ Scales<GRP> load_scales(const WParams& p, int64_t at, int kb, int q,
-                                                   int left) {
-  constexpr int NG = kScales<GRP>;
-  Scales<GRP> r;
-  if constexpr (GRP == kE2M1) {
-    const unsigned char* e = (const unsigned char*)p.sw + at + 4 * kb;
-    const int byte = !TAIL || q < left ? e[q] : 127;
-    r.s[0] = __builtin_bit_cast(float, (uint32_t)byte << 23);
-    r.z[0] = 0.f;
-  } else {
-    const int64_t o = at + (int64_t)NG * kb;
-    // without zero points the bytes of the scales are read in their place, and not used
-    const unsigned char* z = (p.zp ? p.zp : (const unsigned char*)p.sw) + o;
-    int zi[NG];
-    if constexpr (TAIL || NG == 1) {
-#pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const bool in = !TAIL || i < left;
-        if constexpr (SB) r.s[i] = in ? bf(((const unsigned short*)p.sw)[o + i]) : 0.f;
-        else r.s[i] = in ? ((const float*)p.sw)[o + i] : 0.f;
-        zi[i] = in ? z[i] : 0;
-      }
-    } else if constexpr (NG == 2) {
-      if constexpr (SB) {
-        const us2_any h = *(const us2_any*)((const unsigned short*)p.sw + o);
-        r.s[0] = bf(h[0]), r.s[1] = bf(h[1]);
-      } else {
-        const f2_any f = *(const f2_any*)((const float*)p.sw + o);
-        r.s[0] = f[0], r.s[1] = f[1];
-      }
-      const uc2_any b = *(const uc2_any*)z;
-      zi[0] = b[0], zi[1] = b[1];
-    } else {
-      if constexpr (SB) {
-        const us4_any h = *(const us4_any*)((const unsigned short*)p.sw + o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.s[i] = bf(h[i]);
-      } else {
-        const f4_any f = *(const f4_any*)((const float*)p.sw + o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.s[i] = f[i];
-      }
-      const uc4_any b = *(const uc4_any*)z;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) zi[i] = b[i];
-    }
-#pragma unroll
-    for (int i = 0; i < NG; ++i) r.z[i] = 16.f + (p.zp ? (float)zi[i] : 8.f);
-  }
-  return r;
-}
-
-__device__ __forceinline__ v8bf ones() {
-  constexpr int one = 0x3F803F80;
-  return __builtin_bit_cast(v8bf, v4i{one, one, one, one});
-}
-
-// Adds one block: the widened codes w[i][j] (word j of output tile i) and a token tile's words t[j].
-template <int GRP, int NI>
-__device__ __forceinline__ void add_block(const v8bf (&w)[NI][4], const Scales<GRP> (&sc)[NI],
-                                          const v8bf (&t)[4], v4f (&acc)[NI]) {
-  if constexpr (GRP == kE2M1) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) acc[i] = mfma_bf16(t[j], w[i][j], acc[i]);
-  } else {
-    constexpr int NG = kScales<GRP>, PER = 4 / NG;  // MFMAs per group
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      v4f sum = {0.f, 0.f, 0.f, 0.f}, part[NI];
-#pragma unroll
-      for (int j = g * PER; j < (g + 1) * PER; ++j) {
-        sum = mfma_bf16(t[j], ones(), sum);
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-          part[i] = mfma_bf16(t[j], w[i][j], j == g * PER ? v4f{0.f, 0.f, 0.f, 0.f} : part[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][r] = fmaf(sc[i].s[g], fmaf(-sc[i].z[g], sum[r], part[i][r]), acc[i][r]);
-    }
-  }
+  return __builtin_bit_cast(v8bf, r);
 }
 
 // Stores N neighbouring outputs of one row, of which `left` exist, at element `at`.
@@ -220,40 +112,168 @@ __device__ __forceinline__ void store_outputs(void* D, int64_t at, int left, con
         if (i < left) d[i] = h[i];
     }
   } else {
-    typedef float vec __attribute__((ext_vector_type(N), aligned(4)));
+    typedef float vec __attribute__((ext_vector_type(N < 4 ? N : 4), aligned(4)));
+    constexpr int P = N < 4 ? N : 4;
     float* d = (float*)D + at;
-    if (left >= N) {
-      vec v;
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = x[i];
-      *(vec*)d = v;
-    } else {
+    for (int o = 0; o < N; o += P) {
+      if (left >= o + P) {
+        vec v;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < left) d[i] = x[i];
+        for (int i = 0; i < P; ++i) v[i] = x[o + i];
+        *(vec*)(d + o) = v;
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (o + i < left) d[o + i] = x[o + i];
+      }
     }
   }
 }
 
-__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  typedef unsigned int v4u __attribute__((ext_vector_type(4)));
-  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
-}
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)bytes, kRsrcWord3);
+// Waits for this wave's LDS operations, then for the workgroup's other waves; loads into
+// registers stay under way.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(63) & ~0xF00);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // ------------------------------------------------------------------------ streaming kernel
 
-// A workgroup computes 16 NJ outputs of one expert for all its rows, 16 TT at a time; its 8 waves
-// take the blocks of 128 channels in turn, with the next block's operands on their way, and add
-// up in LDS in a fixed order. Rows, outputs and channels that do not exist read as zeros.
+// A workgroup computes 16 NJ outputs of one expert for all its rows, as many rows at a time as its
+// LDS holds (16 at most), which come first. Its 8 waves take the blocks of 128 channels in turn,
+// each with D blocks of W under way, and add up in LDS in a fixed order.
+//
+// Tokens are the MFMA's rows, outputs its columns: a lane holds one output (of each tile), whose
+// codes and scales it reads itself, so scales need no exchange between lanes. A workgroup's
+// outputs are dealt to its tiles in turn, so a lane has neighbouring ones and stores them together.
+//
+// A whole-number code is put into the mantissa bits of the bf16 number 16 (two instructions for
+// two codes, four channels apart; the tokens' channels are put into the same order). A group's sum of
+// x (16 + q) then loses (16 + z) times the group's sum of x, which an MFMA with ones gives in the
+// lanes that need it, before it is scaled.
 constexpr int kW4Waves = 8;
 
-template <int GRP, bool SB, int TT, int NJ, bool OUTB>
-__global__ __launch_bounds__(64 * kW4Waves) void kg_fprop_w4_stream_kernel(WParams p) {
-  constexpr int N0 = 16 * NJ;
-  __shared__ v4f sums[kW4Waves][TT * NJ][64];
+// Scales that a lane holds per block of 128 channels (e2m1: of its own 32 channels).
+template <int GRP>
+constexpr int kScales = GRP == kE2M1 || GRP == 128 ? 1 : 128 / GRP;
+
+// Codes c and c + 4 of eight, c = 0 .. 3, as the bf16 numbers 16 + q.
+__device__ __forceinline__ v8bf eight_plus(uint32_t x) {
+  constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
+  return __builtin_bit_cast(v8bf, v4i{(int)(((x << 3) & mask) | base), (int)(((x >> 1) & mask) | base),
+                                      (int)(((x >> 5) & mask) | base), (int)(((x >> 9) & mask) | base)});
+}
+// Eight tokens' channels in that order.
+__device__ __forceinline__ v8bf by_fours(const v4i& x) {
+  const uint32_t a = x.x, b = x.y, c = x.z, d = x.w;
+  return __builtin_bit_cast(v8bf, v4i{(int)__builtin_amdgcn_perm(c, a, 0x05040100),
+                                      (int)__builtin_amdgcn_perm(c, a, 0x07060302),
+                                      (int)__builtin_amdgcn_perm(d, b, 0x05040100),
+                                      (int)__builtin_amdgcn_perm(d, b, 0x07060302)});
+}
+
+// A lane's 32 channels of one block: lane quad q reads the bytes of channels 32 q .. 32 q + 31 of
+// its output, and word j of them meets the tokens' channels 8 chunk<GRP>(q, j) .. + 7. With scales
+// per 32 or 64 channels the quads exchange words (a 4 x 4 transposition), so that MFMA j covers
+// channels 32 j .. 32 j + 31 alone.
+template <int GRP>
+__device__ __forceinline__ constexpr int chunk(int q, int j) {
+  return GRP == kE2M1 || GRP == 128 ? 4 * q + j : 4 * j + q;
+}
+template <int GRP>
+__device__ __forceinline__ void deal(v4i& x) {
+  if constexpr (GRP == 32 || GRP == 64) {
+    auto a = __builtin_amdgcn_permlane32_swap((unsigned)x.x, (unsigned)x.z, false, false);
+    auto b = __builtin_amdgcn_permlane32_swap((unsigned)x.y, (unsigned)x.w, false, false);
+    auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    x = v4i{(int)c[0], (int)c[1], (int)d[0], (int)d[1]};
+  }
+}
+
+// LDS layout of the tokens: 256-byte blocks of 128 channels, row by row, with 16-byte chunk c of a
+// block in slot c ^ key. A 16-byte read serves lanes 0-3, 12-15, 20-27 at a time, then the other 16
+// of the lower half (the upper half alike): the 16 tokens once each, some with quad q's chunk and the
+// rest with quad q + 1's. The slots are distinct if no two of those tokens' keys differ by the
+// two chunks' difference: 1 where quads hold neighbouring chunks, 4 where they hold four each.
+template <int GRP>
+__device__ __forceinline__ constexpr int key_of(int r) {
+  return chunk<GRP>(1, 0) == 1 ? r & 15 : (r & 10) | ((r & 1) << 2) | ((r >> 2) & 1);
+}
+
+// A lane's scales of one block as they were loaded, and as numbers (z: what is subtracted per
+// unit of x, 16 + the zero point).
+template <int GRP, bool SB>
+struct Raw {
+  uint32_t s[SB ? (kScales<GRP> + 1) / 2 : kScales<GRP>], z;
+};
+template <int GRP, bool SB>
+__device__ __forceinline__ Raw<GRP, SB> load_scales(Rsrc sr, Rsrc zr, uint32_t o) {
+  constexpr int NG = kScales<GRP>;
+  Raw<GRP, SB> r;
+  if constexpr (GRP == kE2M1) {
+    r.s[0] = load1(sr, o);
+    r.z = 0;
+  } else {
+    const uint32_t b = o * kScaleBytes<GRP, SB>;
+    if constexpr (NG == 1) {
+      r.s[0] = SB ? load2(sr, b) : load4(sr, b);
+      r.z = load1(zr, o);
+    } else if constexpr (NG == 2) {
+      if constexpr (SB) {
+        r.s[0] = load4(sr, b);
+      } else {
+        const v2i x = load8(sr, b);
+        r.s[0] = x.x, r.s[1] = x.y;
+      }
+      r.z = load2(zr, o);
+    } else {
+      if constexpr (SB) {
+        const v2i x = load8(sr, b);
+        r.s[0] = x.x, r.s[1] = x.y;
+      } else {
+        const v4i x = load16(sr, b);
+        r.s[0] = x.x, r.s[1] = x.y, r.s[2] = x.z, r.s[3] = x.w;
+      }
+      r.z = load4(zr, o);
+    }
+  }
+  return r;
+}
+// ... of the last block, of which `left` scales exist, one by one (a load across the end of a buffer
+// reads nothing).
+template <int GRP, bool SB>
+__device__ __forceinline__ Raw<GRP, SB> load_last_scales(Rsrc sr, Rsrc zr, uint32_t o, int q,
+                                                         int left) {
+  Raw<GRP, SB> r = {};
+  if constexpr (GRP == kE2M1) {
+    r.s[0] = q < left ? load1(sr, o) : 127u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScales<GRP>; ++i) {
+      if (i >= left) continue;
+      const uint32_t x = SB ? load2(sr, (o + i) * 2) : load4(sr, (o + i) * 4);
+      r.s[SB ? i / 2 : i] |= SB ? x << (16 * (i & 1)) : x;
+      r.z |= load1(zr, o + i) << (8 * i);
+    }
+  }
+  return r;
+}
+template <int GRP, bool SB>
+__device__ __forceinline__ float scale_of(const Raw<GRP, SB>& r, int i) {
+  if constexpr (SB) return as_float(i & 1 ? r.s[i / 2] & 0xFFFF0000u : r.s[i / 2] << 16);
+  else return as_float(r.s[i]);
+}
+
+template <int GRP, bool SB, int NJ, bool OUTB>
+__global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WParams p) {
+  constexpr int N0 = 16 * NJ, NG = kScales<GRP>;
+  constexpr int D = NJ == 2 && NG > 1 ? 3 : 4;  // (what the registers hold)
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int per = p.tiles_n;  // workgroups per expert
   const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * N0;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
@@ -264,120 +284,154 @@ __global__ __launch_bounds__(64 * kW4Waves) void kg_fprop_w4_stream_kernel(WPara
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = KG_ERR_KSUM;
     return;
   }
-  if (rows == 0) return;
-  const int nk = (p.K + 127) / 128, nfull = p.K / 128, kbytes = p.K / 2;
+  // (known to be one value per wave: buffers are described by scalars)
+  g = uniform(g), rows = uniform(rows);
+  row0 = uniform((int)row0);  // below 2^31
+  const int nk = (p.K + 127) / 128, nfull = p.K / 128;
+  const int kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
   const int outs = min(N0, p.N - n0);
   const int64_t out0 = (int64_t)g * p.N + n0;
-  const __amdgpu_buffer_rsrc_t wr = rsrc_of(p.W + out0 * kbytes, (uint32_t)(outs * kbytes));
-  uint32_t woff[NJ];
-  int64_t sat[NJ];
+  const unsigned char* wbase = p.W + out0 * kbytes;
+  const unsigned char* sbase = p.sw + out0 * groups * kScaleBytes<GRP, SB>;
+  // (without zero points the scales' bytes are read in their place, and not used)
+  const unsigned char* zbase = p.zp ? p.zp + out0 * groups : sbase;
+  const bool zeros = p.zp != nullptr;
+  uint32_t woff[NJ], soff[NJ];
 #pragma unroll
-  for (int i = 0; i < NJ; ++i) {
+  for (int i = 0; i < NJ; ++i) {  // outputs past the last one read as zeros
     woff[i] = (uint32_t)((NJ * j + i) * kbytes + 16 * q);
-    sat[i] = (out0 + min(NJ * j + i, outs - 1)) * (p.K / (GRP == kE2M1 ? 32 : GRP));
+    soff[i] = (uint32_t)((NJ * j + i) * groups + (GRP == kE2M1 ? q : 0));
   }
-  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
-    const int here = min(16 * TT, rows - r0);
-    const int64_t lda2 = 2 * p.lda;
-    const __amdgpu_buffer_rsrc_t ar =
-        rsrc_of(p.A + (row0 + r0) * lda2, (uint32_t)((here - 1) * lda2 + 2 * p.K));
-    uint32_t aoff[TT];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) aoff[tt] = (uint32_t)((16 * tt + j) * lda2);
-    v4f acc[TT][NJ];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-      for (int i = 0; i < NJ; ++i) acc[tt][i] = v4f{0.f, 0.f, 0.f, 0.f};
-    v4i wx[2][NJ], tx[2][TT][4];
-    Scales<GRP> sc[2][NJ];
-    auto load = [&](int kb, int h) {
-#pragma unroll
-      for (int i = 0; i < NJ; ++i) {
-        wx[h][i] = load16(wr, woff[i] + (uint32_t)kb * 64);
-        sc[h][i] = load_scales<GRP, SB, false>(p, sat[i], kb, q, 4);
+  for (int r0 = 0; r0 < rows; r0 += p.lds_rows) {
+    const int here = min(p.lds_rows, rows - r0);
+    // the tokens, 4 blocks of 256 bytes per load of a wave; channels past K are zeros
+    {
+      const int64_t lda2 = 2 * p.lda;
+      const v4i ar = make_rsrc(p.A + (row0 + r0) * lda2, (uint32_t)((here - 1) * lda2 + 2 * p.K));
+      const uint32_t lds = lds_addr(smem);
+      for (int x = w; x < (here * nk + 3) / 4; x += kW4Waves) {
+        const int u = 4 * x + q, row = u / nk, kb = u - row * nk;
+        const int ch = 8 * (j ^ key_of<GRP>(row & 15)) + 128 * kb;
+        load16_lds(ar, lds + 1024 * x,
+                   row < here && ch < p.K ? (uint32_t)(row * lda2 + 2 * ch) : kOobOffset);
       }
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tx[h][tt][c] = load16(ar, aoff[tt] + (uint32_t)kb * 256 + 16 * chunk<GRP>(q, c));
-    };
-    auto block = [&](int h) {
-      v8bf wf[NJ][4];
-#pragma unroll
-      for (int i = 0; i < NJ; ++i) {
-        deal<GRP>(wx[h][i]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          wf[i][c] = eight_codes<GRP>((uint32_t)wx[h][i][c], sc[h][i].s[0]);
-      }
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        v8bf t[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) t[c] = __builtin_bit_cast(v8bf, tx[h][tt][c]);
-        add_block<GRP, NJ>(wf, sc[h], t, acc[tt]);
-      }
-    };
-    // This wave's blocks w, w + 8, ...; every load in the loop is unconditional, so the compiler
-    // counts how many are under way.
-    const int nb = nfull > w ? (nfull - w + kW4Waves - 1) / kW4Waves : 0;
-    int n = 0, kb = w;
-    if (nb > 0) load(kb, 0);
-    for (; n + 2 < nb; n += 2, kb += 2 * kW4Waves) {
-      load(kb + kW4Waves, 1);
-      block(0);
-      __builtin_amdgcn_sched_barrier(0);
-      load(kb + 2 * kW4Waves, 0);
-      block(1);
-      __builtin_amdgcn_sched_barrier(0);
     }
-    if (n + 1 < nb) {
-      load(kb + kW4Waves, 1);
-      block(0);
-      block(1);
-    } else if (n < nb) {
-      block(0);
+    v4i wx[D][NJ];
+    Raw<GRP, SB> sx[D][NJ];
+    // blocks past the last whole one read as zeros
+    auto load = [&](int kb, int d) {
+      const bool in = kb < nfull;
+      const int first = kb * (GRP == kE2M1 ? 4 : NG);  // scale of an output
+      const Rsrc wr = rsrc_of(wbase + kb * 64, in ? (uint32_t)(outs * kbytes - kb * 64) : 0u);
+      const Rsrc sr = rsrc_of(sbase + first * kScaleBytes<GRP, SB>,
+                              in ? (uint32_t)((outs * groups - first) * kScaleBytes<GRP, SB>) : 0u);
+      const Rsrc zr = rsrc_of(zbase + first, in ? (uint32_t)(outs * groups - first) : 0u);
+#pragma unroll
+      for (int i = 0; i < NJ; ++i) {
+        wx[d][i] = load16(wr, woff[i]);
+        sx[d][i] = load_scales<GRP, SB>(sr, zr, soff[i]);
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(w + kW4Waves * d, d);
+    wait_all_and_barrier();
+    v4f acc[NJ];
+#pragma unroll
+    for (int i = 0; i < NJ; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    // (lanes of rows that do not exist compute row 0 once more)
+    const int jr = j < here ? j : 0, key = key_of<GRP>(jr);
+    const unsigned char* tok = smem + jr * nk * 256;
+    auto block = [&](int kb, int d) {
+      const unsigned char* t = tok + kb * 256;
+      v4i tx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tx[c] = *(const v4i*)(t + 16 * (chunk<GRP>(q, c) ^ key));
+      // (one word of each tile at a time: widened words of a whole block would not fit the registers)
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (GRP == kE2M1) {
+        float s[NJ];
+#pragma unroll
+        for (int i = 0; i < NJ; ++i)
+          s[i] = as_float(sx[d][i].s[0] << 23);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const v8bf x = __builtin_bit_cast(v8bf, tx[c]);
+#pragma unroll
+          for (int i = 0; i < NJ; ++i)
+            acc[i] = mfma_bf16(x, eight_e2m1((uint32_t)wx[d][i][c], s[i]), acc[i]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        constexpr int one = 0x3F803F80;
+        const v8bf ones = __builtin_bit_cast(v8bf, v4i{one, one, one, one});
+#pragma unroll
+        for (int i = 0; i < NJ; ++i) deal<GRP>(wx[d][i]);
+        v4f sum, part[NJ];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const v8bf x = by_fours(tx[c]);
+          const bool first = c % (4 / NG) == 0, last = (c + 1) % (4 / NG) == 0;
+          sum = mfma_bf16(x, ones, first ? v4f{0.f, 0.f, 0.f, 0.f} : sum);
+#pragma unroll
+          for (int i = 0; i < NJ; ++i)
+            part[i] = mfma_bf16(x, eight_plus((uint32_t)wx[d][i][c]),
+                                first ? v4f{0.f, 0.f, 0.f, 0.f} : part[i]);
+          if (last) {
+            const int n = c / (4 / NG);
+#pragma unroll
+            for (int i = 0; i < NJ; ++i) {
+              const float s = scale_of<GRP, SB>(sx[d][i], n);
+              const float z = 16.f + (zeros ? (float)((sx[d][i].z >> (8 * n)) & 0xFF) : 8.f);
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[i][r] = fmaf(s, fmaf(-z, sum[r], part[i][r]), acc[i][r]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    };
+    for (int b = w; b < nfull; b += D * kW4Waves) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int kb = b + kW4Waves * d;
+        if (kb < nfull) block(kb, d);
+        load(kb + D * kW4Waves, d);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     if constexpr (GRP != 128) {
       if (nfull < nk && w == nfull % kW4Waves) {  // the last block's K % 128 channels
-        const int left = p.K - nfull * 128;
+        const int first = nfull * (GRP == kE2M1 ? 4 : NG);
+        const Rsrc wr = rsrc_of(wbase + nfull * 64, (uint32_t)(outs * kbytes - nfull * 64));
+        const Rsrc sr = rsrc_of(sbase + first * kScaleBytes<GRP, SB>,
+                                (uint32_t)((outs * groups - first) * kScaleBytes<GRP, SB>));
+        const Rsrc zr = rsrc_of(zbase + first, (uint32_t)(outs * groups - first));
 #pragma unroll
         for (int i = 0; i < NJ; ++i) {
-          wx[0][i] = load16(wr, woff[i] + (uint32_t)nfull * 64);
-          sc[0][i] =
-              load_scales<GRP, SB, true>(p, sat[i], nfull, q, left / (GRP == kE2M1 ? 32 : GRP));
+          wx[0][i] = load16(wr, woff[i]);
+          sx[0][i] = load_last_scales<GRP, SB>(sr, zr, soff[i], q, groups - first);
         }
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int ch = 8 * chunk<GRP>(q, c);
-            tx[0][tt][c] = load16(
-                ar, ch < left ? aoff[tt] + (uint32_t)nfull * 256 + 2 * ch : kOobOffset);
-          }
-        block(0);
+        block(nfull, 0);
       }
     }
+    __syncthreads();  // every wave has read the tokens
+    v4f* sums = (v4f*)smem;
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-      for (int i = 0; i < NJ; ++i) sums[w][tt * NJ + i][lane] = acc[tt][i];
+    for (int i = 0; i < NJ; ++i) sums[(w * NJ + i) * 64 + lane] = acc[i];
     __syncthreads();
-    // wave w joins and stores row r = w % 4 of each lane's four of token tile w / 4
-    for (int u = w; u < 4 * TT; u += kW4Waves) {
-      const int tt = u >> 2, r = u & 3;
+    if (w < 4) {  // wave r joins and stores row r of each lane's four
       float x[NJ];
 #pragma unroll
       for (int i = 0; i < NJ; ++i) {
-        x[i] = sums[0][tt * NJ + i][lane][r];
+        const float* f = (const float*)(sums + i * 64 + lane) + w;
+        x[i] = f[0];
 #pragma unroll
-        for (int v = 1; v < kW4Waves; ++v) x[i] += sums[v][tt * NJ + i][lane][r];
+        for (int v = 1; v < kW4Waves; ++v) x[i] += f[v * NJ * 64 * 4];
       }
-      const int row = r0 + 16 * tt + 4 * q + r;
-      if (row < rows)
-        store_outputs<OUTB, NJ>(p.D, (row0 + row) * p.ldd + n0 + NJ * j, outs - NJ * j, x);
+      const int row = 4 * q + w;
+      if (row < here)
+        store_outputs<OUTB, NJ>(p.D, (row0 + r0 + row) * p.ldd + n0 + NJ * j, outs - NJ * j, x);
     }
     __syncthreads();
   }
@@ -385,35 +439,41 @@ __global__ __launch_bounds__(64 * kW4Waves) void kg_fprop_w4_stream_kernel(WPara
 
 // ---------------------------------------------------------------------------- tiled kernel
 
-// BT tokens x BN outputs per workgroup of 8 waves (WT along the tokens), two stages of one block of
-// 128 channels of the tokens in LDS; codes and scales go into registers one block ahead.
-template <int BT_, int BN_, int WT_>
+// BT tokens x BN outputs per workgroup of 8 waves (WT along the tokens), two LDS stages of 64
+// channels: widened weights, tokens, and whole-number codes' scales. Codes, scales and tokens come
+// into registers D blocks ahead (the compiler counts those loads); during block kb the threads
+// widen block kb + 1 into the other stage, a word between MFMAs.
+//
+// Outputs are the MFMA's rows, tokens its columns, as in kg_fprop: by the order in which
+// the outputs are dealt to its rows a lane holds eight neighbouring outputs of one token.
+template <int BT_, int BN_, int WT_, int PER_CU_, int D_>
 struct WCfg {
-  static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = 8 / WT_, THREADS = 512;
+  static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = 8 / WT_, PER_CU = PER_CU_, D = D_;
+  static constexpr int THREADS = 512, TK = 64;
   static constexpr int TT = BT / WT / 16;  // 16-token tiles of a wave
   static constexpr int NI = BN / WN / 16;  // 16-output tiles of a wave
-  static constexpr int STAGE = BT * 256;
-  static constexpr int LOADS = (BT + 31) / 32;  // a wave's 1 KB loads of a stage
-  static_assert(BT % 16 == 0 && BT * 256 % 1024 == 0, "whole wave loads");
+  static constexpr int OPW = BN * 128, OPT = BT * 128, STAGE = OPW + OPT + 2 * BN * 4;
+  static constexpr int WORDS = BN / 64;              // of eight codes, of a thread and block
+  static constexpr int UNITS = (BT * 8 + 511) / 512; // of 16 bytes of tokens
+  static_assert(NI % 2 == 0 && (BN == 128 || BN == 256), "whole runs of outputs, whole words");
 };
-
-// LDS layout: a token's 256 bytes in order, but its 16-byte chunk c in slot c ^ key. A 16-byte read
-// serves lanes 0-3, 12-15, 20-27 at a time, then the other 16 of the lower half (the upper half
-// alike): the tokens of a tile once each, some with quad q's chunk and the rest with quad
-// q + 1's. The slots are distinct if no two of those tokens' keys differ by the two chunks'
-// difference: 1 where quads hold neighbouring chunks, 4 where they hold four each.
-template <int GRP>
-__device__ __forceinline__ constexpr int key_of(int r) {
-  return chunk<GRP>(1, 0) == 1 ? r & 15 : (r & 10) | ((r & 1) << 2) | ((r >> 2) & 1);
+// Row m of MFMA row tile i holds output wrow(i, m) of the wave's.
+__device__ __forceinline__ constexpr int wrow(int i, int m) {
+  return 32 * (i >> 1) + 8 * (m >> 2) + 4 * (i & 1) + (m & 3);
 }
+// LDS slot of 16-byte chunk c of a row is c ^ key, the key m & 7 of the MFMA row (column) m.
+__device__ __forceinline__ constexpr int key_t(int r) { return r & 7; }
+__device__ __forceinline__ constexpr int key_w(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
 
 template <class C, int GRP, bool SB, bool OUTB>
-__global__ __launch_bounds__(C::THREADS, 2) void kg_fprop_w4_kernel(WParams p) {
+__global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(WParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  constexpr int TT = C::TT, NI = C::NI;
+  constexpr int TT = C::TT, NI = C::NI, D = C::D, BN = C::BN, BT = C::BT;
+  constexpr bool INT = GRP != kE2M1;
+  constexpr int NG = GRP == 32 ? 2 : 1;  // scales of an output and block (whole numbers)
   int* off = (int*)(smem + 2 * C::STAGE);  // [G + 1]
   int* boff = off + p.G + 1;
-  if (!f_offsets<C::THREADS>(p.ms, p.G, C::BT, p.M_total, off, boff)) {
+  if (!f_offsets<C::THREADS>(p.ms, p.G, BT, p.M_total, off, boff)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = KG_ERR_KSUM;
     return;
   }
@@ -421,117 +481,205 @@ __global__ __launch_bounds__(C::THREADS, 2) void kg_fprop_w4_kernel(WParams p) {
   const int grid = gridDim.x, b = blockIdx.x;
   // XCD-contiguous runs when the items take several rounds, as in kg_fprop
   const int slot = (grid % 8 == 0 && total > grid) ? (b % 8) * (grid / 8) + b / 8 : b;
-  const int nk = (p.K + 127) / 128, kbytes = p.K / 2;
-  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int nk = (p.K + C::TK - 1) / C::TK, kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
+  const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6);
   const int q = lane >> 4, j = lane & 15;
   const int wt = w % C::WT, wn = w / C::WT;
-  const uint32_t lds = lds_addr(smem);
+  const int c0 = 16 * (q ^ (j & 7)), c1 = 16 * ((q + 4) ^ (j & 7));
+  const unsigned char* fragw = smem + (wn * NI * 16 + wrow(0, j)) * 128;
+  const unsigned char* fragt = smem + C::OPW + (wt * TT * 16 + j) * 128;
+  const unsigned char* scales = smem + C::OPW + C::OPT + (wn * NI * 16 + 8 * q) * 4;
+  // this thread's codes: words [first, first + WORDS) of eight codes of output `out`
+  constexpr int PER_ROW = 512 / BN;
+  const int out = t / PER_ROW, first = t % PER_ROW * C::WORDS;
+  const int half = first / 4;  // of the block's channels
   for (int base = 0; base < total; base += grid) {
     const int idx = base + slot;
     if (idx >= total) break;
     const int per_panel = kPanelM * p.tiles_n;
     const int panel = idx / per_panel, wi = idx - panel * per_panel;
     const int pm = min(kPanelM, mt_total - panel * kPanelM);
-    const int mtg = panel * kPanelM + wi % pm, nt = wi / pm;
+    const int mtg = panel * kPanelM + wi % pm, nt = uniform(wi / pm);
     int lo_g = 0, hi_g = p.G;  // expert of m-tile mtg: the last g with boff[g] <= mtg
     while (hi_g - lo_g > 1) {
       const int mid = (lo_g + hi_g) >> 1;
       if (boff[mid] <= mtg) lo_g = mid; else hi_g = mid;
     }
     const int g = uniform(lo_g);
-    const int row0 = uniform(off[g] + (mtg - boff[g]) * C::BT);
-    const int rows = uniform(min(C::BT, off[g + 1] - row0));
-    const int n0 = nt * C::BN + wn * NI * 16;  // this wave's outputs
-    const int outs = uniform(max(0, min(NI * 16, p.N - n0)));
-    const int64_t out0 = (int64_t)g * p.N + (outs ? n0 : 0);
-    const __amdgpu_buffer_rsrc_t wr = rsrc_of(p.W + out0 * kbytes, (uint32_t)(outs * kbytes));
-    uint32_t woff[NI];
-    int64_t sat[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      woff[i] = (uint32_t)((NI * j + i) * kbytes + 16 * q);
-      sat[i] = (out0 + min(NI * j + i, max(outs, 1) - 1)) * (p.K / (GRP == kE2M1 ? 32 : GRP));
-    }
-    // tokens: wave w's load x takes rows 4 (w + 8 x) .. + 3
-    const unsigned char* A = p.A + (int64_t)row0 * p.lda * 2;
+    const int row0 = uniform(off[g] + (mtg - boff[g]) * BT);
+    const int rows = uniform(min(BT, off[g + 1] - row0));
+    const int n0 = nt * BN, outs = min(BN, p.N - n0);
+    const int64_t out0 = (int64_t)g * p.N + n0;
+    const unsigned char* wbase = p.W + out0 * kbytes;
+    const unsigned char* sbase = p.sw + out0 * groups * kScaleBytes<GRP, SB>;
+    const unsigned char* zbase = p.zp ? p.zp + out0 * groups : sbase;
+    const unsigned char* abase = p.A + (int64_t)row0 * p.lda * 2;
     const int lda2 = (int)(2 * p.lda);
-    auto load_tokens = [&](int kb) {
-      const int left = min(256, 2 * p.K - kb * 256);
-      const v4i r = make_rsrc(A + (int64_t)kb * 256, (uint32_t)((rows - 1) * lda2 + left));
-#pragma unroll
-      for (int x = 0; x < C::LOADS; ++x) {
-        if (C::BT % 32 != 0 && w + 8 * x >= C::BT / 4) continue;
-        const int row = 4 * (w + 8 * x) + q, c = 16 * ((lane & 15) ^ key_of<GRP>(row & 15));
-        load16_lds(r, lds + (kb & 1) * C::STAGE + 1024 * (w + 8 * x),
-                   c < left ? (uint32_t)(row * lda2 + c) : kOobOffset);
+    const uint32_t woff = (uint32_t)(out * kbytes + 4 * first), soff = (uint32_t)(out * groups + (kPerScale<GRP> == 32 ? half : 0));
+    // Ring of the loads. Rows and outputs that do not exist and blocks past the last one read as
+    // zeros; so do the tokens' channels past K.
+    v4i ax[D][C::UNITS], wx[D];
+    uint32_t sx[D], zx[D];
+    auto load_tokens = [&](int kb, int d, int x) {
+      const Rsrc ar = rsrc_of(abase + (int64_t)kb * 128,
+                              kb < nk ? (uint32_t)((rows - 1) * lda2 + min(128, 2 * p.K - 128 * kb)) : 0u);
+      const int u = 512 * x + t, c = u & 7;
+      const bool ok = (BT * 8 % 512 == 0 || u < BT * 8) && 64 * kb + 8 * c < p.K;
+      ax[d][x] = load16(ar, ok ? (uint32_t)((u >> 3) * lda2 + 16 * c) : kOobOffset);
+    };
+    auto load_codes = [&](int kb, int d) {
+      const bool in = kb < nk;
+      const int n = GRP == 128 ? kb >> 1 : GRP == 64 ? kb : 2 * kb;  // first scale of an output
+      const Rsrc wr = rsrc_of(wbase + kb * 32, in ? (uint32_t)(outs * kbytes - kb * 32) : 0u);
+      const Rsrc sr = rsrc_of(sbase + n * kScaleBytes<GRP, SB>,
+                              in ? (uint32_t)((outs * groups - n) * kScaleBytes<GRP, SB>) : 0u);
+      if constexpr (C::WORDS == 4) {
+        wx[d] = load16(wr, woff);
+      } else {
+        const v2i x = load8(wr, woff);
+        wx[d] = v4i{x.x, x.y, 0, 0};
+      }
+      // (the second half of K's last block may not exist)
+      const uint32_t at = kPerScale<GRP> > 32 || n + half < groups ? soff : kOobOffset / 4;
+      if constexpr (!INT) {
+        sx[d] = load1(sr, at);
+      } else {
+        sx[d] = SB ? load2(sr, 2 * at) : load4(sr, 4 * at);
+        zx[d] = load1(rsrc_of(zbase + n, in ? (uint32_t)(outs * groups - n) : 0u), at);
       }
     };
-    v4i wx[NI];
-    Scales<GRP> sn[NI];
-    auto load_codes = [&](int kb) {
-      const int left = (p.K - kb * 128) / (GRP == kE2M1 ? 32 : GRP);
+    v4f acc[NI][TT];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        wx[i] = load16(wr, woff[i] + (uint32_t)kb * 64);
-        if (GRP == 128 || kb * 128 + 128 <= p.K) sn[i] = load_scales<GRP, SB, false>(p, sat[i], kb, q, 4);
-        else sn[i] = load_scales<GRP, SB, true>(p, sat[i], kb, q, left);
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
+    // What this thread writes of block kb, held in slot d, into its stage
+    auto put_tokens = [&](int kb, int d, int x) {
+      const int u = 512 * x + t, r = u >> 3;
+      if (BT * 8 % 512 == 0 || u < BT * 8)
+        *(v4i*)(smem + (kb & 1) * C::STAGE + C::OPW + r * 128 + 16 * ((u & 7) ^ key_t(r))) = ax[d][x];
+    };
+    auto put_word = [&](int kb, int d, int n) {
+      v8bf v;
+      if constexpr (INT) v = eight_less((uint32_t)wx[d][n], p.zp ? (float)zx[d] : 8.f);
+      else v = eight_e2m1((uint32_t)wx[d][n], as_float(sx[d] << 23));
+      *(v8bf*)(smem + (kb & 1) * C::STAGE + out * 128 + 16 * ((first + n) ^ key_w(out))) = v;
+    };
+    auto put_scale = [&](int kb, int d) {
+      if constexpr (INT)
+        if (first % (GRP == 32 ? 4 : 8) == 0)
+          *(float*)(smem + (kb & 1) * C::STAGE + C::OPW + C::OPT + ((GRP == 32 ? half : 0) * BN + out) * 4) =
+              as_float(SB ? sx[d] << 16 : sx[d]);
+    };
+    v8bf tf[TT][2], wf[2][2];
+    v4f sc[3][NG];
+    auto read_t = [&](int kb, int tt) {
+      const unsigned char* r = fragt + (kb & 1) * C::STAGE + 16 * tt * 128;
+      tf[tt][0] = *(const v8bf*)(r + c0);
+      tf[tt][1] = *(const v8bf*)(r + c1);
+    };
+    auto read_w = [&](int kb, int i) {
+      const unsigned char* r = fragw + (kb & 1) * C::STAGE + wrow(i, 0) * 128;
+      wf[i & 1][0] = *(const v8bf*)(r + c0);
+      wf[i & 1][1] = *(const v8bf*)(r + c1);
+      if constexpr (INT) {
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+          sc[i % 3][n] = *(const v4f*)(scales + (kb & 1) * C::STAGE + (n * BN + wrow(i, 0)) * 4);
       }
     };
-    v4f acc[TT][NI];
+    auto load = [&](int kb, int d) {
+      load_codes(kb, d);
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) acc[tt][i] = v4f{0.f, 0.f, 0.f, 0.f};
-    const int key = key_of<GRP>(j);
-    const unsigned char* frag = smem + (wt * TT * 16 + j) * 256;
+      for (int x = 0; x < C::UNITS; ++x) load_tokens(kb, d, x);
+    };
     if (nk > 0) {
-      load_tokens(0);
-      load_codes(0);
+#pragma unroll
+      for (int d = 0; d < D; ++d) load(d, d);
+#pragma unroll
+      for (int n = 0; n < C::WORDS; ++n) put_word(0, 0, n);
+      put_scale(0, 0);
+#pragma unroll
+      for (int x = 0; x < C::UNITS; ++x) put_tokens(0, 0, x);
+      load(D, 0);
+      meet();
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) read_t(0, tt);
     }
-    for (int kb = 0; kb < nk; ++kb) {
-      v8bf wf[NI][4];
-      Scales<GRP> sc[NI];
-      // this block's tokens are there, the last block's have been read by every wave
-      wait_all_and_barrier();
+    // Block kb; block kb + 1 is in slot d, and written to its stage in turn with the MFMAs before the
+    // last tile of outputs. One meeting per block, there: behind it the next block's tokens are read,
+    // and every wave has read this block's weights, whose stage the next block writes to.
+    auto block = [&](int kb, int d) {
+      constexpr int S = NI * 2 * TT, LAST = S - 2 * TT, WORK = C::WORDS + C::UNITS;
+      v4f part[2][TT];
+      auto add = [&](int i, int tt, int n) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        sc[i] = sn[i];
-        deal<GRP>(wx[i]);
+        for (int r = 0; r < 4; ++r)
+          acc[i][tt][r] = fmaf(sc[i % 3][n][r], part[i & 1][tt][r], acc[i][tt][r]);
+        asm volatile("" : "+v"(acc[i][tt]));
+      };
+      read_w(kb, 0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) wf[i][c] = eight_codes<GRP>((uint32_t)wx[i][c], sc[i].s[0]);
+      for (int u = 0; u < S; ++u) {
+        const int i = u / (2 * TT), h = u / TT % 2, tt = u % TT;
+        if (u == LAST) meet();
+        if (h == 0 && tt == 0 && i + 1 < NI) read_w(kb, i + 1);
+        if constexpr (INT) {
+          const bool fresh = h == 0 || NG == 2;
+          // sums are scaled and added half a tile after their last MFMA was issued
+          if (h == 0 && i > 0) add(i - 1, tt, NG - 1);
+          if (h == 1 && NG == 2) add(i, tt, 0);
+          part[i & 1][tt] = mfma_bf16(wf[i & 1][h], tf[tt][h],
+                                      fresh ? v4f{0.f, 0.f, 0.f, 0.f} : part[i & 1][tt]);
+        } else {
+          acc[i][tt] = mfma_bf16(wf[i & 1][h], tf[tt][h], acc[i][tt]);
+        }
+        if (i == NI - 1 && h == 1) read_t(kb + 1, tt);  // (past the last block: not used)
+#pragma unroll
+        for (int x = 0; x < WORK; ++x) {
+          if (x * LAST / WORK != u) continue;
+          if (x < C::WORDS) {
+            put_word(kb + 1, d, x);
+            if (x == C::WORDS - 1) {
+              put_scale(kb + 1, d);
+              load_codes(kb + 1 + D, d);
+            }
+          } else {
+            put_tokens(kb + 1, d, x - C::WORDS);
+            load_tokens(kb + 1 + D, d, x - C::WORDS);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (kb + 1 < nk) {
-        load_tokens(kb + 1);
-        load_codes(kb + 1);
-      }
-      const unsigned char* st = frag + (kb & 1) * C::STAGE;
+      if constexpr (INT) {
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        v8bf t[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          t[c] = *(const v8bf*)(st + tt * 16 * 256 + 16 * (chunk<GRP>(q, c) ^ key));
-        add_block<GRP, NI>(wf, sc, t, acc[tt]);
+        for (int tt = 0; tt < TT; ++tt) add(NI - 1, tt, NG - 1);
       }
+    };
+    for (int k0 = 0; k0 < nk; k0 += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (k0 + d < nk) block(k0 + d, (d + 1) % D);
     }
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
+    for (int tt = 0; tt < TT; ++tt) {
+      const int r = (wt * TT + tt) * 16 + j;
+      if (r >= rows) continue;
+      const int64_t at = (int64_t)(row0 + r) * p.ldd + n0;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = (wt * TT + tt) * 16 + 4 * q + r;
-        if (row >= rows) continue;
-        float x[NI];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) x[i] = acc[tt][i][r];
-        store_outputs<OUTB, NI>(p.D, (int64_t)(row0 + row) * p.ldd + n0 + NI * j, outs - NI * j, x);
+      for (int i = 0; i < NI; i += 2) {
+        const int n = wn * NI * 16 + 16 * i + 8 * q;
+        const float x[8] = {acc[i][tt][0],     acc[i][tt][1],     acc[i][tt][2],     acc[i][tt][3],
+                            acc[i + 1][tt][0], acc[i + 1][tt][1], acc[i + 1][tt][2], acc[i + 1][tt][3]};
+        store_outputs<OUTB, 8>(p.D, at + n, outs - n, x);
       }
-    __syncthreads();  // every wave has read the last stage
+    }
   }
 }
 
 struct WLaunch {
   const void* fn;
-  int bt, bn, lds, id;  // id < 0: streaming
+  int bt, bn, lds, per_cu;
 };
 
 // The kernel by type: format, scale type, result type.
@@ -545,11 +693,11 @@ static const void* w_pick(int kind, int group, bool outb) {
   return group == 32 ? KG_W4_GROUP(32) : group == 64 ? KG_W4_GROUP(64) : KG_W4_GROUP(128);
 #undef KG_W4_GROUP
 }
-template <int TT, int NJ>
+template <int NJ>
 struct StreamOf {
   template <int GRP, bool SB, bool OUTB>
   struct F {
-    static const void* fn() { return (const void*)kg_fprop_w4_stream_kernel<GRP, SB, TT, NJ, OUTB>; }
+    static const void* fn() { return (const void*)kg_fprop_w4_stream_kernel<GRP, SB, NJ, OUTB>; }
   };
 };
 template <class C>
@@ -559,25 +707,24 @@ struct TiledOf {
     static const void* fn() { return (const void*)kg_fprop_w4_kernel<C, GRP, SB, OUTB>; }
   };
 };
-template <int TT, int NJ>
-static WLaunch w_stream(int kind, int group, bool outb) {
-  return WLaunch{w_pick<StreamOf<TT, NJ>::template F>(kind, group, outb), 16 * TT, 16 * NJ, 0, -1};
-}
 template <class C>
-static WLaunch w_tiled(int kind, int group, bool outb, int id) {
-  return WLaunch{w_pick<TiledOf<C>::template F>(kind, group, outb), C::BT, C::BN, 2 * C::STAGE, id};
+static WLaunch w_tiled(int kind, int group, bool outb) {
+  return WLaunch{w_pick<TiledOf<C>::template F>(kind, group, outb), C::BT, C::BN, 2 * C::STAGE,
+                 C::PER_CU};
 }
 
-// Which kernel and tile, by M_total and G (the experts' sizes are known on the device only); every
-// choice is right for every distribution of the rows.
-static WLaunch w_choose(int64_t M, int G, int N, int cus, int kind, int group, bool outb) {
-  const int64_t avg = (M + G - 1) / G, live = G < M ? G : M;
-  if (avg <= 16) {
-    if (live * ((N + 31) / 32) <= cus / 2) return w_stream<1, 1>(kind, group, outb);
-    return w_stream<1, 2>(kind, group, outb);
-  }
-  if (avg <= 64) return w_tiled<WCfg<64, 256, 1>>(kind, group, outb, 0);
-  return w_tiled<WCfg<128, 256, 2>>(kind, group, outb, 1);
+// Lets a kernel have all of a compute unit's LDS, once per kernel and device.
+static bool w_lds_allowed(const void* fn, int dev) {
+  static std::mutex mu;
+  static const void* set[64][128];
+  static int count[64];
+  std::lock_guard<std::mutex> lk(mu);
+  for (int i = 0; i < count[dev]; ++i)
+    if (set[dev][i] == fn) return true;
+  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - 512) != hipSuccess)
+    return false;
+  if (count[dev] < 128) set[dev][count[dev]++] = fn;
+  return true;
 }
 
 }  // namespace kg
@@ -614,7 +761,7 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
   WParams p;
   p.A = (const unsigned char*)A;
   p.W = (const unsigned char*)W;
-  p.sw = sw;
+  p.sw = (const unsigned char*)sw;
   p.zp = (const unsigned char*)zp;
   p.D = D;
   p.ms = ms;
@@ -626,32 +773,43 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
   p.G = G;
   p.N = N;
   p.K = K;
-  WLaunch l = w_choose(M_total, G, N, cus, kind, group, outb);
-  p.tiles_n = (N + l.bn - 1) / l.bn;
+  p.lds_rows = 0;
+  // Which kernel and tile, by M_total and G (the experts' sizes are known on the device only); every
+  // choice is right for every distribution of the rows.
+  const int64_t avg = (M_total + G - 1) / G, live = G < M_total ? G : M_total;
+  // Streaming: the rows that a workgroup's LDS holds, and what they take
+  const int64_t row_bytes = (K + 127) / 128 * 256;
+  int64_t hold = row_bytes ? 64 * 1024 / row_bytes : 16;
+  if (hold < 2 * avg && row_bytes) hold = 150 * 1024 / row_bytes;
+  if (hold > 16) hold = 16;
+  if (hold > M_total) hold = M_total;
+  WLaunch l;
   int64_t grid;
-  if (l.id < 0) {
-    grid = (int64_t)(G < M_total ? G : M_total) * p.tiles_n;
+  if (hold > 0 && (2 * avg <= hold || M_total <= hold)) {
+    const bool narrow = live * ((N + 31) / 32) <= cus / 2;
+    l.fn = narrow ? w_pick<StreamOf<1>::F>(kind, group, outb) : w_pick<StreamOf<2>::F>(kind, group, outb);
+    l.bn = narrow ? 16 : 32;
+    p.lds_rows = (int)hold;
+    const int64_t tokens = (hold * row_bytes + 1023) / 1024 * 1024, sums = kW4Waves * (l.bn / 16) * 1024;
+    l.lds = (int)(tokens > sums ? tokens : sums);
+    p.tiles_n = (N + l.bn - 1) / l.bn;
+    grid = live * p.tiles_n;
     if (grid > INT32_MAX / 512) return KG_ERR_UNSUPPORTED;
   } else {
+    using Large = WCfg<256, 256, 4, 1, 1>;
+    l = avg <= 32    ? w_tiled<WCfg<32, 256, 1, 2, 2>>(kind, group, outb)
+        : avg <= 64  ? w_tiled<WCfg<64, 128, 2, 2, 2>>(kind, group, outb)
+        : avg <= 128 ? w_tiled<WCfg<128, 128, 2, 1, 2>>(kind, group, outb)
+        : mx && avg > 256 ? WLaunch{outb ? (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, true> : (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, false>, Large::BT, Large::BN, 2 * Large::STAGE, 1}
+                     : w_tiled<WCfg<128, 256, 2, 1, 2>>(kind, group, outb);
     l.lds += 2 * (G + 1) * 4;
-    static std::mutex mu;
-    static const void* set[64][64];  // kernels that may have the largest LDS size
-    static int count[64];
-    {
-      std::lock_guard<std::mutex> lk(mu);
-      bool found = false;
-      for (int i = 0; i < count[dev]; ++i) found |= set[dev][i] == l.fn;
-      if (!found) {
-        if (hipFuncSetAttribute(l.fn, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                l.lds - 2 * (G + 1) * 4 + 2 * (kMaxGroups + 1) * 4) != hipSuccess)
-          return KG_ERR_HIP;
-        if (count[dev] < 64) set[dev][count[dev]++] = l.fn;
-      }
-    }
+    p.tiles_n = (N + l.bn - 1) / l.bn;
     const int64_t max_items = (M_total / l.bt + G) * (int64_t)p.tiles_n;
     if (max_items > INT32_MAX - 4096) return KG_ERR_UNSUPPORTED;  // (indexes pass it by a grid)
-    grid = max_items < cus ? max_items : cus;
+    const int64_t at_once = (int64_t)cus * l.per_cu;
+    grid = max_items < at_once ? max_items : at_once;
   }
+  if (!w_lds_allowed(l.fn, dev)) return KG_ERR_HIP;
   void* args[] = {&p};
   return hipLaunchKernel(l.fn, dim3((unsigned)grid), dim3(512), args, (size_t)l.lds,
                          (hipStream_t)stream) == hipSuccess
