@@ -37,7 +37,8 @@ struct WParams {
   int64_t M_total, lda, ldd;
   int G, N, K;
   int tiles_n;
-  int lds_rows;  // token rows that the streaming kernel's LDS holds
+  int lds_rows;      // token rows that the streaming kernel's LDS holds
+  int lds_s, lds_z;  // where scales and zero points begin there
 };
 
 // Formats: whole numbers by channels per scale, and e2m1.
@@ -205,74 +206,27 @@ __device__ __forceinline__ constexpr int key_of(int r) {
   return chunk<GRP>(1, 0) == 1 ? r & 15 : (r & 10) | ((r & 1) << 2) | ((r >> 2) & 1);
 }
 
-// A lane's scales of one block as they were loaded, and as numbers (z: what is subtracted per
-// unit of x, 16 + the zero point).
-template <int GRP, bool SB>
-struct Raw {
-  uint32_t s[SB ? (kScales<GRP> + 1) / 2 : kScales<GRP>], z;
-};
-template <int GRP, bool SB>
-__device__ __forceinline__ Raw<GRP, SB> load_scales(Rsrc sr, Rsrc zr, uint32_t o) {
-  constexpr int NG = kScales<GRP>;
-  Raw<GRP, SB> r;
-  if constexpr (GRP == kE2M1) {
-    r.s[0] = load1(sr, o);
-    r.z = 0;
-  } else {
-    const uint32_t b = o * kScaleBytes<GRP, SB>;
-    if constexpr (NG == 1) {
-      r.s[0] = SB ? load2(sr, b) : load4(sr, b);
-      r.z = load1(zr, o);
-    } else if constexpr (NG == 2) {
-      if constexpr (SB) {
-        r.s[0] = load4(sr, b);
-      } else {
-        const v2i x = load8(sr, b);
-        r.s[0] = x.x, r.s[1] = x.y;
-      }
-      r.z = load2(zr, o);
-    } else {
-      if constexpr (SB) {
-        const v2i x = load8(sr, b);
-        r.s[0] = x.x, r.s[1] = x.y;
-      } else {
-        const v4i x = load16(sr, b);
-        r.s[0] = x.x, r.s[1] = x.y, r.s[2] = x.z, r.s[3] = x.w;
-      }
-      r.z = load4(zr, o);
-    }
+// `bytes` bytes from memory (at any address) to LDS at smem + at, by all waves of the workgroup: whole
+// 16-byte units straight there, the last few bytes through registers once those have landed
+// (they would else be zeroed behind them). Up to the next KB is overwritten.
+__device__ __forceinline__ void copy_units(unsigned char* smem, int at, const unsigned char* from,
+                                           int bytes, int w, int lane) {
+  const v4i r = make_rsrc(from, (uint32_t)bytes);
+  for (int x = w; 1024 * x < bytes; x += kW4Waves) {
+    const int o = 1024 * x + 16 * lane;
+    load16_lds(r, lds_addr(smem) + at + 1024 * x, o + 16 <= bytes ? (uint32_t)o : kOobOffset);
   }
-  return r;
 }
-// ... of the last block, of which `left` scales exist, one by one (a load across the end of a buffer
-// reads nothing).
-template <int GRP, bool SB>
-__device__ __forceinline__ Raw<GRP, SB> load_last_scales(Rsrc sr, Rsrc zr, uint32_t o, int q,
-                                                         int left) {
-  Raw<GRP, SB> r = {};
-  if constexpr (GRP == kE2M1) {
-    r.s[0] = q < left ? load1(sr, o) : 127u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kScales<GRP>; ++i) {
-      if (i >= left) continue;
-      const uint32_t x = SB ? load2(sr, (o + i) * 2) : load4(sr, (o + i) * 4);
-      r.s[SB ? i / 2 : i] |= SB ? x << (16 * (i & 1)) : x;
-      r.z |= load1(zr, o + i) << (8 * i);
-    }
-  }
-  return r;
-}
-template <int GRP, bool SB>
-__device__ __forceinline__ float scale_of(const Raw<GRP, SB>& r, int i) {
-  if constexpr (SB) return as_float(i & 1 ? r.s[i / 2] & 0xFFFF0000u : r.s[i / 2] << 16);
-  else return as_float(r.s[i]);
+__device__ __forceinline__ void copy_rest(unsigned char* smem, int at, const unsigned char* from,
+                                          int bytes, int t) {
+  const int o = (bytes & ~15) + t;
+  if (t < (bytes & 15)) smem[at + o] = from[o];
 }
 
 template <int GRP, bool SB, int NJ, bool OUTB>
 __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WParams p) {
   constexpr int N0 = 16 * NJ, NG = kScales<GRP>;
-  constexpr int D = NJ == 2 && NG > 1 ? 3 : 4;  // (what the registers hold)
+  constexpr int D = NJ == 2 ? 4 : 6, SBYTES = kScaleBytes<GRP, SB>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int per = p.tiles_n;  // workgroups per expert
   const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * N0;
@@ -287,21 +241,25 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
   // (known to be one value per wave: buffers are described by scalars)
   g = uniform(g), rows = uniform(rows);
   row0 = uniform((int)row0);  // below 2^31
-  const int nk = (p.K + 127) / 128, nfull = p.K / 128;
+  const int nk = (p.K + 127) / 128;
   const int kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
   const int outs = min(N0, p.N - n0);
   const int64_t out0 = (int64_t)g * p.N + n0;
   const unsigned char* wbase = p.W + out0 * kbytes;
-  const unsigned char* sbase = p.sw + out0 * groups * kScaleBytes<GRP, SB>;
-  // (without zero points the scales' bytes are read in their place, and not used)
-  const unsigned char* zbase = p.zp ? p.zp + out0 * groups : sbase;
+  const unsigned char* sbase = p.sw + out0 * groups * SBYTES;
+  const unsigned char* zbase = p.zp + out0 * groups;
   const bool zeros = p.zp != nullptr;
-  uint32_t woff[NJ], soff[NJ];
+  uint32_t woff[NJ];
+  int soff[NJ];
 #pragma unroll
-  for (int i = 0; i < NJ; ++i) {  // outputs past the last one read as zeros
-    woff[i] = (uint32_t)((NJ * j + i) * kbytes + 16 * q);
-    soff[i] = (uint32_t)((NJ * j + i) * groups + (GRP == kE2M1 ? q : 0));
+  for (int i = 0; i < NJ; ++i) {
+    woff[i] = (uint32_t)((NJ * j + i) * kbytes + 16 * q);  // past the last output: zeros
+    soff[i] = min(NJ * j + i, outs - 1) * groups;
   }
+  // the outputs' scales and zero points, which lie side by side
+  const int sbytes = outs * groups * SBYTES, zbytes = zeros ? outs * groups : 0;
+  copy_units(smem, p.lds_s, sbase, sbytes, w, lane);
+  if (zeros) copy_units(smem, p.lds_z, zbase, zbytes, w, lane);
   for (int r0 = 0; r0 < rows; r0 += p.lds_rows) {
     const int here = min(p.lds_rows, rows - r0);
     // the tokens, 4 blocks of 256 bytes per load of a wave; channels past K are zeros
@@ -317,24 +275,23 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
       }
     }
     v4i wx[D][NJ];
-    Raw<GRP, SB> sx[D][NJ];
-    // blocks past the last whole one read as zeros
+    // The wave's blocks come in pairs: a row's 64 bytes of one block are half of a line.
+    auto block_of = [&](int n) { return 2 * kW4Waves * (n >> 1) + 2 * w + (n & 1); };
+    // blocks past the last one read as zeros
     auto load = [&](int kb, int d) {
-      const bool in = kb < nfull;
-      const int first = kb * (GRP == kE2M1 ? 4 : NG);  // scale of an output
+      const bool in = kb < nk;
       const Rsrc wr = rsrc_of(wbase + kb * 64, in ? (uint32_t)(outs * kbytes - kb * 64) : 0u);
-      const Rsrc sr = rsrc_of(sbase + first * kScaleBytes<GRP, SB>,
-                              in ? (uint32_t)((outs * groups - first) * kScaleBytes<GRP, SB>) : 0u);
-      const Rsrc zr = rsrc_of(zbase + first, in ? (uint32_t)(outs * groups - first) : 0u);
 #pragma unroll
-      for (int i = 0; i < NJ; ++i) {
-        wx[d][i] = load16(wr, woff[i]);
-        sx[d][i] = load_scales<GRP, SB>(sr, zr, soff[i]);
-      }
+      for (int i = 0; i < NJ; ++i) wx[d][i] = load16(wr, woff[i]);
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(w + kW4Waves * d, d);
+    for (int d = 0; d < D; ++d) load(block_of(d), d);
     wait_all_and_barrier();
+    if (r0 == 0 && ((sbytes | zbytes) & 15)) {
+      copy_rest(smem, p.lds_s, sbase, sbytes, threadIdx.x);
+      copy_rest(smem, p.lds_z, zbase, zbytes, threadIdx.x);
+      __syncthreads();
+    }
     v4f acc[NJ];
 #pragma unroll
     for (int i = 0; i < NJ; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -351,8 +308,10 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
       if constexpr (GRP == kE2M1) {
         float s[NJ];
 #pragma unroll
-        for (int i = 0; i < NJ; ++i)
-          s[i] = as_float(sx[d][i].s[0] << 23);
+        for (int i = 0; i < NJ; ++i) {  // (past K: any scale that is a number)
+          const int n = 4 * kb + q;
+          s[i] = as_float((n < groups ? (uint32_t)smem[p.lds_s + soff[i] + n] : 127u) << 23);
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const v8bf x = __builtin_bit_cast(v8bf, tx[c]);
@@ -366,6 +325,17 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
         const v8bf ones = __builtin_bit_cast(v8bf, v4i{one, one, one, one});
 #pragma unroll
         for (int i = 0; i < NJ; ++i) deal<GRP>(wx[d][i]);
+        float sc[NJ][NG], sz[NJ][NG];
+#pragma unroll
+        for (int i = 0; i < NJ; ++i)
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {  // (past K: 0)
+            const int g = NG * kb + n, at = soff[i] + g;
+            const bool in = GRP == 128 || g < groups;
+            const unsigned char* f = smem + p.lds_s + at * SBYTES;
+            sc[i][n] = !in ? 0.f : SB ? as_float((uint32_t) * (const unsigned short*)f << 16) : *(const float*)f;
+            sz[i][n] = 16.f + (zeros ? in ? (float)smem[p.lds_z + at] : 0.f : 8.f);
+          }
         v4f sum, part[NJ];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -380,8 +350,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
             const int n = c / (4 / NG);
 #pragma unroll
             for (int i = 0; i < NJ; ++i) {
-              const float s = scale_of<GRP, SB>(sx[d][i], n);
-              const float z = 16.f + (zeros ? (float)((sx[d][i].z >> (8 * n)) & 0xFF) : 8.f);
+              const float s = sc[i][n], z = sz[i][n];
 #pragma unroll
               for (int r = 0; r < 4; ++r)
                 acc[i][r] = fmaf(s, fmaf(-z, sum[r], part[i][r]), acc[i][r]);
@@ -391,28 +360,13 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
         }
       }
     };
-    for (int b = w; b < nfull; b += D * kW4Waves) {
+    for (int n = 0; block_of(n) < nk; n += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        const int kb = b + kW4Waves * d;
-        if (kb < nfull) block(kb, d);
-        load(kb + D * kW4Waves, d);
+        const int kb = block_of(n + d);
+        if (kb < nk) block(kb, d);
+        load(block_of(n + d + D), d);
         __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    if constexpr (GRP != 128) {
-      if (nfull < nk && w == nfull % kW4Waves) {  // the last block's K % 128 channels
-        const int first = nfull * (GRP == kE2M1 ? 4 : NG);
-        const Rsrc wr = rsrc_of(wbase + nfull * 64, (uint32_t)(outs * kbytes - nfull * 64));
-        const Rsrc sr = rsrc_of(sbase + first * kScaleBytes<GRP, SB>,
-                                (uint32_t)((outs * groups - first) * kScaleBytes<GRP, SB>));
-        const Rsrc zr = rsrc_of(zbase + first, (uint32_t)(outs * groups - first));
-#pragma unroll
-        for (int i = 0; i < NJ; ++i) {
-          wx[0][i] = load16(wr, woff[i]);
-          sx[0][i] = load_last_scales<GRP, SB>(sr, zr, soff[i], q, groups - first);
-        }
-        block(nfull, 0);
       }
     }
     __syncthreads();  // every wave has read the tokens
@@ -773,25 +727,33 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
   p.G = G;
   p.N = N;
   p.K = K;
-  p.lds_rows = 0;
+  p.lds_rows = p.lds_s = p.lds_z = 0;
   // Which kernel and tile, by M_total and G (the experts' sizes are known on the device only); every
   // choice is right for every distribution of the rows.
   const int64_t avg = (M_total + G - 1) / G, live = G < M_total ? G : M_total;
-  // Streaming: the rows that a workgroup's LDS holds, and what they take
-  const int64_t row_bytes = (K + 127) / 128 * 256;
-  int64_t hold = row_bytes ? 64 * 1024 / row_bytes : 16;
-  if (hold < 2 * avg && row_bytes) hold = 150 * 1024 / row_bytes;
+  // Streaming: a workgroup's LDS holds scales, zero points and as many rows as fit
+  const bool narrow = live * ((N + 31) / 32) <= cus / 2;
+  const int bn = narrow ? 16 : 32;
+  auto kbytes = [](int64_t n) { return (n + 1023) / 1024 * 1024; };
+  const int64_t row_bytes = (K + 127) / 128 * 256, per_out = K / group;
+  const int64_t scales_at = kbytes(bn * per_out * sb), zeros_at = zp ? kbytes(bn * per_out) : 0;
+  const int64_t rest = scales_at + zeros_at + 1024;
+  int64_t hold = row_bytes ? (76 * 1024 - rest) / row_bytes : 16;
+  if (hold < 2 * avg && row_bytes) hold = (156 * 1024 - rest) / row_bytes;
   if (hold > 16) hold = 16;
   if (hold > M_total) hold = M_total;
   WLaunch l;
   int64_t grid;
   if (hold > 0 && (2 * avg <= hold || M_total <= hold)) {
-    const bool narrow = live * ((N + 31) / 32) <= cus / 2;
     l.fn = narrow ? w_pick<StreamOf<1>::F>(kind, group, outb) : w_pick<StreamOf<2>::F>(kind, group, outb);
-    l.bn = narrow ? 16 : 32;
+    l.bn = bn;
     p.lds_rows = (int)hold;
-    const int64_t tokens = (hold * row_bytes + 1023) / 1024 * 1024, sums = kW4Waves * (l.bn / 16) * 1024;
-    l.lds = (int)(tokens > sums ? tokens : sums);
+    int64_t tokens = kbytes(hold * row_bytes);
+    const int64_t sums = kW4Waves * (bn / 16) * 1024;
+    if (tokens < sums) tokens = sums;
+    p.lds_s = (int)tokens;
+    p.lds_z = (int)(tokens + scales_at);
+    l.lds = (int)(tokens + scales_at + zeros_at);
     p.tiles_n = (N + l.bn - 1) / l.bn;
     grid = live * p.tiles_n;
     if (grid > INT32_MAX / 512) return KG_ERR_UNSUPPORTED;
