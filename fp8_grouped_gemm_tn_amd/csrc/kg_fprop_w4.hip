@@ -162,9 +162,17 @@ constexpr int kW4Waves = 8;
 template <int GRP>
 constexpr int kScales = GRP == kE2M1 || GRP == 128 ? 1 : 128 / GRP;
 
-// Codes c and c + 4 of eight, c = 0 .. 3, as the bf16 numbers 16 + q.
-__device__ __forceinline__ v8bf eight_plus(uint32_t x) {
-  constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
+// Codes c and c + 4 of eight, c = 0 .. 3, as the bf16 numbers 16 + q. The constants come in a scalar
+// and a vector register: written as numbers they cost two instructions where v_and_or_b32 is one.
+struct Plus {
+  uint32_t mask, base;
+  __device__ __forceinline__ Plus() {
+    asm("s_mov_b32 %0, 0x00780078" : "=s"(mask));
+    asm("v_mov_b32 %0, 0x41804180" : "=v"(base));
+  }
+};
+__device__ __forceinline__ v8bf eight_plus(uint32_t x, const Plus& c) {
+  const uint32_t mask = c.mask, base = c.base;
   return __builtin_bit_cast(v8bf, v4i{(int)(((x << 3) & mask) | base), (int)(((x >> 1) & mask) | base),
                                       (int)(((x >> 5) & mask) | base), (int)(((x >> 9) & mask) | base)});
 }
@@ -241,7 +249,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
   // (known to be one value per wave: buffers are described by scalars)
   g = uniform(g), rows = uniform(rows);
   row0 = uniform((int)row0);  // below 2^31
-  const int nk = (p.K + 127) / 128;
+  const int nk = (p.K + 127) / 128, pieces = max(1, (nk + 3) / 4);
   const int kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
   const int outs = min(N0, p.N - n0);
   const int64_t out0 = (int64_t)g * p.N + n0;
@@ -262,47 +270,57 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
   if (zeros) copy_units(smem, p.lds_z, zbase, zbytes, w, lane);
   for (int r0 = 0; r0 < rows; r0 += p.lds_rows) {
     const int here = min(p.lds_rows, rows - r0);
-    // the tokens, 4 blocks of 256 bytes per load of a wave; channels past K are zeros
+    // the tokens, a row's 4 blocks of 256 bytes per load of a wave; channels past K are zeros
     {
       const int64_t lda2 = 2 * p.lda;
       const v4i ar = make_rsrc(p.A + (row0 + r0) * lda2, (uint32_t)((here - 1) * lda2 + 2 * p.K));
       const uint32_t lds = lds_addr(smem);
-      for (int x = w; x < (here * nk + 3) / 4; x += kW4Waves) {
-        const int u = 4 * x + q, row = u / nk, kb = u - row * nk;
-        const int ch = 8 * (j ^ key_of<GRP>(row & 15)) + 128 * kb;
-        load16_lds(ar, lds + 1024 * x,
-                   row < here && ch < p.K ? (uint32_t)(row * lda2 + 2 * ch) : kOobOffset);
+      int row = 0, piece = w;
+      while (piece >= pieces) piece -= pieces, ++row;
+      while (row < here) {
+        const int ch = 8 * (j ^ key_of<GRP>(row & 15)) + 128 * (4 * piece + q);
+        load16_lds(ar, lds + 1024 * (row * pieces + piece),
+                   ch < p.K ? (uint32_t)(row * (int)lda2 + 2 * ch) : kOobOffset);
+        piece += kW4Waves;
+        while (piece >= pieces) piece -= pieces, ++row;
       }
     }
     v4i wx[D][NJ];
-    // The wave's blocks come in pairs: a row's 64 bytes of one block are half of a line.
-    auto block_of = [&](int n) { return 2 * kW4Waves * (n >> 1) + 2 * w + (n & 1); };
-    // blocks past the last one read as zeros
+    // This wave's blocks, [from, to); what lies past them reads as zeros.
+    const int from = w * nk / kW4Waves, to = (w + 1) * nk / kW4Waves;
     auto load = [&](int kb, int d) {
-      const bool in = kb < nk;
+      const bool in = kb < to;
       const Rsrc wr = rsrc_of(wbase + kb * 64, in ? (uint32_t)(outs * kbytes - kb * 64) : 0u);
 #pragma unroll
       for (int i = 0; i < NJ; ++i) wx[d][i] = load16(wr, woff[i]);
     };
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(block_of(d), d);
+    for (int d = 0; d < D; ++d) load(from + d, d);
     wait_all_and_barrier();
-    if (r0 == 0 && ((sbytes | zbytes) & 15)) {
+    if (r0 == 0) {
       copy_rest(smem, p.lds_s, sbase, sbytes, threadIdx.x);
       copy_rest(smem, p.lds_z, zbase, zbytes, threadIdx.x);
-      __syncthreads();
     }
+    if constexpr (GRP != kE2M1) {
+      for (int c = threadIdx.x; c < here * pieces * 64; c += 64 * kW4Waves) {
+        v4i* x = (v4i*)smem + c;
+        *x = __builtin_bit_cast(v4i, by_fours(*x));
+      }
+    }
+    __syncthreads();
     v4f acc[NJ];
 #pragma unroll
     for (int i = 0; i < NJ; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
     // (lanes of rows that do not exist compute row 0 once more)
     const int jr = j < here ? j : 0, key = key_of<GRP>(jr);
-    const unsigned char* tok = smem + jr * nk * 256;
+    const unsigned char* tok[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      tok[c] = smem + jr * pieces * 1024 + from * 256 + 16 * (chunk<GRP>(q, c) ^ key);
     auto block = [&](int kb, int d) {
-      const unsigned char* t = tok + kb * 256;
       v4i tx[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tx[c] = *(const v4i*)(t + 16 * (chunk<GRP>(q, c) ^ key));
+      for (int c = 0; c < 4; ++c) tx[c] = *(const v4i*)(tok[c] + 256 * d);
       // (one word of each tile at a time: widened words of a whole block would not fit the registers)
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (GRP == kE2M1) {
@@ -323,6 +341,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
       } else {
         constexpr int one = 0x3F803F80;
         const v8bf ones = __builtin_bit_cast(v8bf, v4i{one, one, one, one});
+        const Plus plus;
 #pragma unroll
         for (int i = 0; i < NJ; ++i) deal<GRP>(wx[d][i]);
         float sc[NJ][NG], sz[NJ][NG];
@@ -339,12 +358,12 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
         v4f sum, part[NJ];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const v8bf x = by_fours(tx[c]);
+          const v8bf x = __builtin_bit_cast(v8bf, tx[c]);
           const bool first = c % (4 / NG) == 0, last = (c + 1) % (4 / NG) == 0;
           sum = mfma_bf16(x, ones, first ? v4f{0.f, 0.f, 0.f, 0.f} : sum);
 #pragma unroll
           for (int i = 0; i < NJ; ++i)
-            part[i] = mfma_bf16(x, eight_plus((uint32_t)wx[d][i][c]),
+            part[i] = mfma_bf16(x, eight_plus((uint32_t)wx[d][i][c], plus),
                                 first ? v4f{0.f, 0.f, 0.f, 0.f} : part[i]);
           if (last) {
             const int n = c / (4 / NG);
@@ -360,14 +379,15 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
         }
       }
     };
-    for (int n = 0; block_of(n) < nk; n += D) {
+    for (int k0 = from; k0 < to; k0 += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        const int kb = block_of(n + d);
-        if (kb < nk) block(kb, d);
-        load(block_of(n + d + D), d);
+        if (k0 + d < to) block(k0 + d, d);
+        load(k0 + d + D, d);
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tok[c] += 256 * D;
     }
     __syncthreads();  // every wave has read the tokens
     v4f* sums = (v4f*)smem;
@@ -735,7 +755,7 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
   const bool narrow = live * ((N + 31) / 32) <= cus / 2;
   const int bn = narrow ? 16 : 32;
   auto kbytes = [](int64_t n) { return (n + 1023) / 1024 * 1024; };
-  const int64_t row_bytes = (K + 127) / 128 * 256, per_out = K / group;
+  const int64_t row_bytes = kbytes((K + 127) / 128 * 256), per_out = K / group;
   const int64_t scales_at = kbytes(bn * per_out * sb), zeros_at = zp ? kbytes(bn * per_out) : 0;
   const int64_t rest = scales_at + zeros_at + 1024;
   int64_t hold = row_bytes ? (76 * 1024 - rest) / row_bytes : 16;

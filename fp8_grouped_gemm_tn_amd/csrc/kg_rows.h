@@ -65,6 +65,25 @@ __device__ __forceinline__ bool f_offsets(const int32_t* ms, int G, int bt, int6
   return true;
 }
 
+// Inclusive scans over a wave by DPP: within rows of 16 lanes, then from row to row. (Shuffles through
+// LDS take 1 us of a short kernel's time.)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_0(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void scan_step(int64_t* sum, int* count) {
+  const uint32_t lo = (uint32_t)dpp_or_0<CTRL, ROWS>((int)(uint32_t)*sum);
+  const int hi = dpp_or_0<CTRL, ROWS>((int)(*sum >> 32));
+  *sum += (int64_t)(((uint64_t)(uint32_t)hi << 32) | lo);
+  *count += dpp_or_0<CTRL, ROWS>(*count);
+}
+__device__ __forceinline__ int64_t read_lane(int64_t x, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // The expert with rows that `nth` others with rows come before, its first row and their number, by
 // a scan of ms in every wave (a lane holds consecutive experts). rows = 0: there is none.
 // Returns false if ms is inconsistent.
@@ -82,16 +101,13 @@ __device__ __forceinline__ bool find_rows(const int32_t* ms, int G, int64_t M_to
   }
   int64_t to = sum;  // rows and experts up to this lane's last one
   int live_to = live;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t u = __shfl_up(to, d, 64);
-    const int v = __shfl_up(live_to, d, 64);
-    if (lane >= d) {
-      to += u;
-      live_to += v;
-    }
-  }
-  const bool ok = __ballot(neg != 0) == 0 && __shfl(to, 63, 64) == M_total;
+  scan_step<0x111, 0xF>(&to, &live_to);  // row_shr: 1, 2, 4, 8
+  scan_step<0x112, 0xF>(&to, &live_to);
+  scan_step<0x114, 0xF>(&to, &live_to);
+  scan_step<0x118, 0xF>(&to, &live_to);
+  scan_step<0x142, 0xA>(&to, &live_to);  // row_bcast: 15, 31
+  scan_step<0x143, 0xC>(&to, &live_to);
+  const bool ok = __ballot(neg != 0) == 0 && read_lane(to, 63) == M_total;
   const uint64_t has = __ballot(live_to > nth);  // the first such lane has the expert
   *rows = 0;
   *g = 0;
@@ -99,19 +115,23 @@ __device__ __forceinline__ bool find_rows(const int32_t* ms, int G, int64_t M_to
   if (!ok || has == 0) return ok;
   const int owner = __builtin_ctzll(has);
   int64_t at = to - sum;
-  int mine = 0, mg = 0, left = nth - (live_to - live);
-  for (int e = e0; e < e1 && lane == owner; ++e) {
-    const int v = ms[e];
-    if (v > 0 && left-- == 0) {
-      mine = v;
-      mg = e;
-      break;
+  int mine = (int)sum, mg = e0;
+  if (per > 1) {
+    int left = nth - (live_to - live);
+    mine = 0;
+    for (int e = e0; e < e1 && lane == owner; ++e) {
+      const int v = ms[e];
+      if (v > 0 && left-- == 0) {
+        mine = v;
+        mg = e;
+        break;
+      }
+      at += v;
     }
-    at += v;
   }
-  *row0 = __shfl(at, owner, 64);
-  *rows = uniform(__shfl(mine, owner, 64));
-  *g = uniform(__shfl(mg, owner, 64));
+  *row0 = read_lane(at, owner);
+  *rows = __builtin_amdgcn_readlane(mine, owner);
+  *g = __builtin_amdgcn_readlane(mg, owner);
   return true;
 }
 
