@@ -39,6 +39,7 @@ struct WParams {
   int tiles_n;
   int lds_rows;      // token rows that the streaming kernel's LDS holds
   int lds_s, lds_z;  // where scales and zero points begin there
+  int split;         // its waves that share the contraction axis of an output: 8 or 4
 };
 
 // Formats: whole numbers by channels per scale, and e2m1.
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
   constexpr int D = NJ == 2 ? 4 : 6, SBYTES = kScaleBytes<GRP, SB>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int per = p.tiles_n;  // workgroups per expert
-  const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * N0;
+  const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * N0 * (kW4Waves / p.split);
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, j = lane & 15;
   int64_t row0;
@@ -251,21 +252,24 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
   row0 = uniform((int)row0);  // below 2^31
   const int nk = (p.K + 127) / 128, pieces = max(1, (nk + 3) / 4);
   const int kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
-  const int outs = min(N0, p.N - n0);
+  const int all = min(N0 * (kW4Waves / p.split), p.N - n0);  // outputs of the workgroup
   const int64_t out0 = (int64_t)g * p.N + n0;
-  const unsigned char* wbase = p.W + out0 * kbytes;
   const unsigned char* sbase = p.sw + out0 * groups * SBYTES;
   const unsigned char* zbase = p.zp + out0 * groups;
+  // ... and of this wave, the part-th of those that share them
+  const int side = w / p.split, part = w - side * p.split, m0 = side * N0;
+  const int outs = max(0, min(N0, all - m0));
+  const unsigned char* wbase = p.W + (out0 + (outs ? m0 : 0)) * kbytes;
   const bool zeros = p.zp != nullptr;
   uint32_t woff[NJ];
   int soff[NJ];
 #pragma unroll
   for (int i = 0; i < NJ; ++i) {
     woff[i] = (uint32_t)((NJ * j + i) * kbytes + 16 * q);  // past the last output: zeros
-    soff[i] = min(NJ * j + i, outs - 1) * groups;
+    soff[i] = min(m0 + NJ * j + i, all - 1) * groups;
   }
   // the outputs' scales and zero points, which lie side by side
-  const int sbytes = outs * groups * SBYTES, zbytes = zeros ? outs * groups : 0;
+  const int sbytes = all * groups * SBYTES, zbytes = zeros ? all * groups : 0;
   copy_units(smem, p.lds_s, sbase, sbytes, w, lane);
   if (zeros) copy_units(smem, p.lds_z, zbase, zbytes, w, lane);
   for (int r0 = 0; r0 < rows; r0 += p.lds_rows) {
@@ -287,7 +291,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
     }
     v4i wx[D][NJ];
     // This wave's blocks, [from, to); what lies past them reads as zeros.
-    const int from = w * nk / kW4Waves, to = (w + 1) * nk / kW4Waves;
+    const int from = part * nk / p.split, to = (part + 1) * nk / p.split;
     auto load = [&](int kb, int d) {
       const bool in = kb < to;
       const Rsrc wr = rsrc_of(wbase + kb * 64, in ? (uint32_t)(outs * kbytes - kb * 64) : 0u);
@@ -394,18 +398,19 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
 #pragma unroll
     for (int i = 0; i < NJ; ++i) sums[(w * NJ + i) * 64 + lane] = acc[i];
     __syncthreads();
-    if (w < 4) {  // wave r joins and stores row r of each lane's four
+    if (part < 4) {  // wave r of those that share outputs joins and stores row r of each lane's four
       float x[NJ];
 #pragma unroll
       for (int i = 0; i < NJ; ++i) {
-        const float* f = (const float*)(sums + i * 64 + lane) + w;
+        const float* f = (const float*)(sums + (side * p.split * NJ + i) * 64 + lane) + part;
         x[i] = f[0];
 #pragma unroll
-        for (int v = 1; v < kW4Waves; ++v) x[i] += f[v * NJ * 64 * 4];
+        for (int v = 1; v < kW4Waves; ++v)
+          if (v < p.split) x[i] += f[v * NJ * 64 * 4];
       }
-      const int row = 4 * q + w;
+      const int row = 4 * q + part;
       if (row < here)
-        store_outputs<OUTB, NJ>(p.D, (row0 + r0 + row) * p.ldd + n0 + NJ * j, outs - NJ * j, x);
+        store_outputs<OUTB, NJ>(p.D, (row0 + r0 + row) * p.ldd + n0 + m0 + NJ * j, outs - NJ * j, x);
     }
     __syncthreads();
   }
@@ -748,12 +753,15 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
   p.N = N;
   p.K = K;
   p.lds_rows = p.lds_s = p.lds_z = 0;
+  p.split = kW4Waves;
   // Which kernel and tile, by M_total and G (the experts' sizes are known on the device only); every
   // choice is right for every distribution of the rows.
   const int64_t avg = (M_total + G - 1) / G, live = G < M_total ? G : M_total;
   // Streaming: a workgroup's LDS holds scales, zero points and as many rows as fit
-  const bool narrow = live * ((N + 31) / 32) <= cus / 2;
-  const int bn = narrow ? 16 : 32;
+  // A workgroup has 16 outputs where 32 would leave half of the compute units idle, 64 (two sets of
+  // 32, four waves each) where those make four workgroups or more for each compute unit.
+  const bool narrow = live * ((N + 31) / 32) <= cus / 2, wide = live * ((N + 63) / 64) >= 4 * cus;
+  const int bn = narrow ? 16 : wide ? 64 : 32;
   auto kbytes = [](int64_t n) { return (n + 1023) / 1024 * 1024; };
   const int64_t row_bytes = kbytes((K + 127) / 128 * 256), per_out = K / group;
   const int64_t scales_at = kbytes(bn * per_out * sb), zeros_at = zp ? kbytes(bn * per_out) : 0;
@@ -769,7 +777,7 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
     l.bn = bn;
     p.lds_rows = (int)hold;
     int64_t tokens = kbytes(hold * row_bytes);
-    const int64_t sums = kW4Waves * (bn / 16) * 1024;
+    const int64_t sums = kW4Waves * (narrow ? 1 : 2) * 1024;
     if (tokens < sums) tokens = sums;
     p.lds_s = (int)tokens;
     p.lds_z = (int)(tokens + scales_at);
