@@ -18,8 +18,8 @@
 namespace kg {
 
 constexpr int kGateMaxK = 16;       // lane j of a token's lanes holds its j-th choice
-constexpr int kGateThreads = 256;   // per workgroup
-constexpr int kGateBlocks = 1024;   // most workgroups of a launch, each with a line of sums
+constexpr int kGateThreads = 512;   // per workgroup
+constexpr int kGateBlocks = 512;    // most workgroups of a launch, each with a line of sums
 constexpr float kGateTiny = 1e-20f; // beside the sum of a token's chosen scores
 
 struct GateParams {
@@ -92,11 +92,12 @@ __device__ __forceinline__ float sum_of(float x) {
   return as_f(reduce<LPR>(as_u(x), [](uint32_t a, uint32_t b) { return as_u(as_f(a) + as_f(b)); }));
 }
 
-// A float's place in the order of all floats, as an unsigned number (both zeros the same); 0 for
-// what is never chosen. Every other value gives more than 0x007fffff.
+// A float's place in the order of all floats, as an unsigned number (both zeros the same). What is
+// never chosen, -inf and NaN, has the lowest place of all.
+constexpr uint32_t kNever = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t place(float x) {
-  const uint32_t u = as_u(x + 0.0f);
-  return x > -INFINITY ? u ^ ((uint32_t)((int)u >> 31) | 0x80000000u) : 0u;
+  const uint32_t u = as_u(fmaxf(x + 0.0f, -INFINITY));  // (the maximum passes over NaN)
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value(uint32_t p) {
   return as_f(p & 0x80000000u ? p ^ 0x80000000u : ~p);
@@ -114,7 +115,7 @@ __device__ __forceinline__ void gate_load(const void* row, int G, int l, float (
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = (c * LPR + l) * 4;
-    if (i + 4 <= G) {
+    if ((c + 1) * LPR * 4 <= G || i + 4 <= G) {
       if constexpr (B16) {
         const h4_any h = *(const h4_any*)((const unsigned short*)row + i);
 #pragma unroll
@@ -131,7 +132,17 @@ __device__ __forceinline__ void gate_load(const void* row, int G, int l, float (
   }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// exp(x - m) by the exponential unit: two roundings of the exponent, 2^-24 of its size each, and one of
+// the result. (As 2^(x log2(e) - m log2(e)), one instruction less, it would overflow for masks of the
+// type's lowest value.)
+constexpr float kLog2E = 1.44269504f;
+__device__ __forceinline__ float exp_less(float x, float m) {
+  return __builtin_amdgcn_exp2f((x - m) * kLog2E);
+}
+// (a sum from 1 to infinity: v_rcp_f32 is within 2^-23 there)
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * x));
+}
 
 // Scores of a token in place of its logits. *top: the largest logit (softmax; 0 where there is
 // none), *inv: one over the sum (0 for a token without experts; finite for any sum).
@@ -146,7 +157,7 @@ __device__ __forceinline__ void gate_scores(float (&x)[V], bool sig, float* top,
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    x[v] = sig ? sigmoid(x[v]) : expf(x[v] - m);
+    x[v] = sig ? sigmoid(x[v]) : exp_less(x[v], m);
     sum += x[v];
   }
   sum = sum_of<LPR>(sum);
@@ -154,11 +165,11 @@ __device__ __forceinline__ void gate_scores(float (&x)[V], bool sig, float* top,
   *inv = sum == 0.0f ? 0.0f : sum < 0x1p-126f ? 0x1p126f : 1.0f / sum;
 }
 
-// The first `n` in order of (place descending, index ascending): lane j is given the j-th one's
-// index and place (-1 and 0 where there is none).
+// The first `n` in order of (place descending, index ascending): the j-th one's index to lane j (-1
+// where there is none).
 template <int LPR, int V>
-__device__ __forceinline__ void choose_exact(uint32_t (&p)[V], int l, int n, int* index,
-                                             uint32_t* its) {
+__device__ __forceinline__ int choose_exact(uint32_t (&p)[V], int l, int n) {
+  int index = -1;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     uint32_t m = 0;
@@ -170,35 +181,27 @@ __device__ __forceinline__ void choose_exact(uint32_t (&p)[V], int l, int n, int
     for (int v = V - 1; v >= 0; --v)
       if (p[v] == m) at = (uint32_t)Lanes<LPR, V / 4>::at(l, v);
     at = min_of<LPR>(at);
-    if (l == j) {
-      *index = m ? (int)at : -1;
-      *its = m;
-    }
+    if (l == j) index = m > kNever ? (int)at : -1;
     const uint32_t rel = at - 4 * l;
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (rel == (uint32_t)((v >> 2) * LPR * 4 + (v & 3))) p[v] = 0;
   }
+  return index;
 }
 
-// The k largest logits. Keys that hold the place's upper bits and, reversed, the index are
-// distinct, so the next one is the largest below the last, found without taking any out:
-// of key - last, unsigned, the keys below have the largest. bf16's 16 bits are a whole place;
-// fp32 choices that differ in the cut bits alone are ambiguous, and a wave with one of those (or
-// with equal logits) chooses by whole places, at three times the cost.
+// Keys that hold a place's upper bits and, reversed, the index are distinct, so the next one is the
+// largest below the last, found without taking any out: of key - last, unsigned, the keys below
+// have the largest. The j-th largest of the tokens' keys to lane j, j < n (0 where there is none).
+template <bool B16, int LPR>
+constexpr uint32_t kIndexBits = B16 ? 0xFFFFu : LPR == 16 ? 0xFFu : 0x3FFu;
 template <bool B16, int LPR, int V>
-__device__ __forceinline__ int choose_logits(const float (&x)[V], int l, int k) {
-  constexpr uint32_t MASK = B16 ? 0xFFFFu : LPR == 16 ? 0xFFu : 0x3FFu;
-  uint32_t key[V], last = 0;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const uint32_t p = place(x[v]);
-    key[v] = p ? (p & ~MASK) | (MASK - (uint32_t)Lanes<LPR, V / 4>::at(l, v)) : 0u;
-  }
-  int index = -1;
-  bool unsure = false;
+__device__ __forceinline__ uint32_t largest_keys(const uint32_t (&key)[V], int l, int n) {
+  constexpr uint32_t MASK = kIndexBits<B16, LPR>;
+  uint32_t last = 0, mine = 0;
+  bool more = true;
 #pragma unroll 1
-  for (int j = 0; j < k + (B16 ? 0 : 1); ++j) {
+  for (int j = 0; j < n; ++j) {
     uint32_t m = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -206,16 +209,32 @@ __device__ __forceinline__ int choose_logits(const float (&x)[V], int l, int k) 
       m = m > t ? m : t;
     }
     m = max_of<LPR>(m) + last;
-    if (j > 0 && last == 0) m = 0;  // nothing was left before
-    if (!B16 && j > 0 && m != 0) unsure |= ((m ^ last) & ~MASK) == 0;
-    if (l == j) index = m ? (int)(MASK - (m & MASK)) : -1;
+    more = more && (m | MASK) > (kNever | MASK);  // (places and masks end in ones)
+    if (l == j) mine = more ? m : 0u;
     last = m;
   }
-  if (!B16 && __any(unsure)) {
-    uint32_t its;
+  return mine;
+}
+
+// The k largest logits. bf16's 16 bits are a whole place; fp32 choices whose places differ in the
+// cut bits alone are ambiguous, and a wave with one of those (or with equal logits) chooses by whole
+// places, at three times the cost.
+template <bool B16, int LPR, int V>
+__device__ __forceinline__ int choose_logits(const float (&x)[V], const uint32_t (&id)[V], int l,
+                                             int k) {
+  constexpr uint32_t MASK = kIndexBits<B16, LPR>;
+  uint32_t key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = place(x[v]);
-    choose_exact<LPR, V>(key, l, k, &index, &its);
+  for (int v = 0; v < V; ++v) key[v] = (place(x[v]) & ~MASK) | id[v];
+  const uint32_t mine = largest_keys<B16, LPR, V>(key, l, k + (B16 ? 0 : 1));
+  int index = mine ? (int)(MASK - (mine & MASK)) : -1;
+  if constexpr (!B16) {
+    const uint32_t next = (uint32_t)__shfl_down((int)mine, 1, LPR);
+    if (__any(l < k && next != 0 && ((mine ^ next) & ~MASK) == 0)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = place(x[v]);
+      index = choose_exact<LPR, V>(key, l, k);
+    }
   }
   return index;
 }
@@ -273,63 +292,70 @@ __device__ __attribute__((noinline)) int choose64(const void* row, const float* 
   return index;
 }
 
-// The k largest of score + bias: by 32-bit keys where those tell the keys apart, else in 64 bits.
-// A 32-bit key is off by less than 2^-19 (a score is at most 1; its sum has at most 22 roundings in
-// a row, the exponential and the quotient one or two each) and 2^-23 of the key itself. Where only
-// choices known to be among the first k + 1 are that close, those alone are compared in 64 bits.
+// The k largest of score + bias. Cut 32-bit keys give k + 1 candidates and a bound for all others;
+// the candidates are put in order by their whole 32-bit keys where those tell them apart, else by
+// 64-bit ones; and where the k-th is not above the bound, everything is chosen in 64 bits. A 32-bit
+// key is off by less than 2^-19 (a score is at most 1; its sum has at most 22 roundings in a row,
+// the exponential and the quotient a few) and 2^-23 of the key itself.
 template <bool B16, int LPR, int V>
-__device__ __forceinline__ int choose_biased(const float (&x)[V], const float (&s)[V], float inv,
-                                             float top, const void* row, const float* bias, int G,
-                                             int l, int k, bool sig) {
-  uint32_t p[V];
+__device__ __forceinline__ int choose_biased(const float (&x)[V], const float (&s)[V],
+                                             const uint32_t (&id)[V], float inv, float top,
+                                             const void* row, const float* bias, int G, int l, int k,
+                                             bool sig) {
+  constexpr uint32_t MASK = kIndexBits<false, LPR>;
+  uint32_t key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = Lanes<LPR, V / 4>::at(l, v);
-    const float key = i < G ? (sig ? s[v] : s[v] * inv) + bias[i] : 0.0f;
-    p[v] = i < G && x[v] > -INFINITY ? place(key) : 0u;
+    const float f = i < G ? (sig ? s[v] : s[v] * inv) + bias[i] : 0.0f;
+    key[v] = ((i < G && x[v] > -INFINITY ? place(f) : kNever) & ~MASK) | id[v];
   }
-  int index = -1;
-  uint32_t its = 0;
-  const int n = k + 2;  // a token has that many lanes
-  choose_exact<LPR, V>(p, l, n, &index, &its);
-  const uint32_t next = (uint32_t)__shfl_down((int)its, 1, LPR);
-  const float a = value(its), b = value(next);
-  const bool close = l + 1 < n && next != 0 && !(a - b > 0x1p-18f + 0x1p-22f * fabsf(a));
-  const int lane = threadIdx.x & 63;
-  const uint64_t mine =
-      (__ballot(close) >> (lane & ~(LPR - 1))) & (LPR == 64 ? ~0ull : (1ull << (LPR & 63)) - 1);
-  // bit j: the j-th and the one after it are close
-  const uint64_t inner = mine & ((1ull << k) - 1);
-  if (!__any(inner != 0)) return l < k ? index : -1;
-  const bool edge = (mine >> (k - 1)) & 1;  // the last choice and the first that was not made
-  const bool whole = edge && ((mine >> k) & 1);
-  if (__any(whole)) {
-    const int all = choose64<B16, LPR, V / 4>(row, bias, G, l, k, sig, top);
+  const uint32_t mine = largest_keys<false, LPR, V>(key, l, k + 2);  // (a token has that many lanes)
+  const bool in = l <= k && mine != 0;
+  const int index = in ? (int)(MASK - (mine & MASK)) : -1;
+  float f = -INFINITY;
+  if (in) {
+    const float own = gate_at<B16>(row, index);
+    f = (sig ? sigmoid(own) : exp_less(own, top) * inv) + bias[index];
+  }
+  // the most that any other can have
+  const uint32_t beyond = (uint32_t)__shfl((int)mine, k + 1, LPR);
+  const float bound = beyond ? value(beyond | MASK) : -INFINITY;
+  int rank = 0;
+  bool close = false, low = false;
+#pragma unroll 1
+  for (int j = 0; j <= k; ++j) {
+    const float o = __shfl(f, j, LPR);
+    const int oi = __shfl(index, j, LPR);
+    rank += o > f || (o == f && oi >= 0 && oi < index);
+    close |= in && oi >= 0 && j != l && !(fabsf(o - f) > 0x1p-18f + 0x1p-22f * fabsf(f));
+  }
+  if (in && rank < k && beyond) low = !(f - bound > 0x1p-18f + 0x1p-22f * fabsf(f));
+  if (__any(low)) {
+    const int all = choose64<B16, LPR, V / 4>(row, bias, G, l, k, sig, top);  // with every lane
     return l < k ? all : -1;
   }
-  const int m = edge ? k + 1 : k;  // candidates
-  const double z = sig ? 1.0 : sum64<B16, LPR, V / 4>(row, G, l, top);
-  double key = -INFINITY;
-  if (l < m && index >= 0) key = score64(gate_at<B16>(row, index), sig, top, z) + (double)bias[index];
-  int rank = 0;
+  if (__any(close)) {
+    const double z = sig ? 1.0 : sum64<B16, LPR, V / 4>(row, G, l, top);
+    double d = -INFINITY;
+    if (in) d = score64(gate_at<B16>(row, index), sig, top, z) + (double)bias[index];
+    rank = 0;
 #pragma unroll 1
-  for (int j = 0; j <= k; ++j) {
-    const double o = __shfl(key, j, LPR);
-    const int oi = __shfl(index, j, LPR);
-    rank += j < m && oi >= 0 && (o > key || (o == key && oi < index));
+    for (int j = 0; j <= k; ++j) {
+      const double o = __shfl(d, j, LPR);
+      const int oi = __shfl(index, j, LPR);
+      rank += o > d || (o == d && oi >= 0 && oi < index);
+    }
   }
-  int out = -1;
-#pragma unroll 1
-  for (int j = 0; j <= k; ++j) {
-    const int r = __shfl(rank, j, LPR), oi = __shfl(index, j, LPR);
-    if (j < m && oi >= 0 && r == l) out = oi;
-  }
+  // to the lane of its rank; lanes without a candidate are behind those with one
+  const int lane = threadIdx.x & 63, to = (lane & ~(LPR - 1)) + (in ? rank : l);
+  const int out = __builtin_amdgcn_ds_permute(4 * to, index);
   return l < k ? out : -1;
 }
 
 // The sums over all workgroups' lines, in their order; the last workgroup to finish adds up the
 // loss, in the order of the experts.
-constexpr int kGateSumExperts = 16;
+constexpr int kGateSumExperts = 8;
 __global__ __launch_bounds__(256) void kg_gate_sum_kernel(GateParams p, int blocks) {
   constexpr int E = kGateSumExperts, S = 256 / E;
   __shared__ double sums[S][E];
@@ -389,8 +415,12 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_kernel(GateParams p) {
     __syncthreads();
   }
   float sums[V];
+  uint32_t id[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) sums[v] = 0.0f;
+  for (int v = 0; v < V; ++v) {
+    sums[v] = 0.0f;
+    id[v] = kIndexBits<B16 && !BIAS, LPR> - (uint32_t)L::at(l, v);
+  }
   const int64_t step = (int64_t)gridDim.x * WAVES * L::ROWS;
   for (int64_t t0 = ((int64_t)blockIdx.x * WAVES + wave) * L::ROWS; t0 < p.T; t0 += step) {
     const bool live = t0 + sub < p.T;
@@ -402,13 +432,13 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_kernel(GateParams p) {
     for (int v = 0; v < V; ++v) s[v] = x[v];
     gate_scores<LPR, V>(s, sig, &top, &inv);
     int index;
-    if constexpr (BIAS) index = choose_biased<B16, LPR, V>(x, s, inv, top, row, p.bias, p.G, l, p.k, sig);
-    else index = choose_logits<B16, LPR, V>(x, l, p.k);
+    if constexpr (BIAS) index = choose_biased<B16, LPR, V>(x, s, id, inv, top, row, p.bias, p.G, l, p.k, sig);
+    else index = choose_logits<B16, LPR, V>(x, id, l, p.k);
     if (l >= p.k) index = -1;
     float w = 0.0f;
     if (index >= 0) {
       const float own = gate_at<B16>(row, index);
-      w = sig ? sigmoid(own) : expf(own - top) * inv;
+      w = sig ? sigmoid(own) : exp_less(own, top) * inv;
     }
     if (norm) w = w / (sum_of<LPR>(w) + kGateTiny);
     if (live && l < p.k) {
@@ -504,7 +534,7 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_bwd_kernel(GateBwdParams
     for (int v = 0; v < V; ++v) s[v] = x[v];
     gate_scores<LPR, V>(s, sig, &top, &inv);
     float chosen = 0.0f, d = dw;
-    if (index >= 0) chosen = sig ? sigmoid(own) : expf(own - top) * inv;
+    if (index >= 0) chosen = sig ? sigmoid(own) : exp_less(own, top) * inv;
     if (norm) {
       const float sum = sum_of<LPR>(chosen) + kGateTiny, mean = sum_of<LPR>(dw * chosen) / sum;
       d = (dw - mean) / sum;
@@ -566,8 +596,11 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_bwd_kernel(GateBwdParams
   }
 }
 
+// Whether a token has 16 lanes. Few tokens of more than 64 experts have 64, so that a lane has fewer
+// of the logits that each step goes through.
+static bool gate_row16(int64_t T, int G) { return G <= 64 || (G <= 256 && T > 1024); }
 static int64_t gate_blocks(int64_t T, int G) {
-  const int64_t rows = kGateThreads / 64 * (G <= 256 ? 4 : 1);
+  const int64_t rows = kGateThreads / 64 * (gate_row16(T, G) ? 4 : 1);
   const int64_t n = (T + rows - 1) / rows;
   return n < 1 ? 1 : n < kGateBlocks ? n : kGateBlocks;
 }
@@ -581,17 +614,15 @@ static bool gate_sizes_taken(int64_t T, int G, int k, int64_t ld) {
 }  // namespace kg
 
 // The kernel of a launch: by type and by how many logits a lane holds.
-#define KG_GATE_PICK(fn, b16, G, ...)                                                          \
-  ((b16) ? ((G) <= 64    ? fn<true, 16, 1 __VA_ARGS__>                                         \
-            : (G) <= 128 ? fn<true, 16, 2 __VA_ARGS__>                                         \
-            : (G) <= 256 ? fn<true, 16, 4 __VA_ARGS__>                                         \
-            : (G) <= 512 ? fn<true, 64, 2 __VA_ARGS__>                                         \
-                         : fn<true, 64, 4 __VA_ARGS__>)                                        \
-         : ((G) <= 64    ? fn<false, 16, 1 __VA_ARGS__>                                        \
-            : (G) <= 128 ? fn<false, 16, 2 __VA_ARGS__>                                        \
-            : (G) <= 256 ? fn<false, 16, 4 __VA_ARGS__>                                        \
-            : (G) <= 512 ? fn<false, 64, 2 __VA_ARGS__>                                        \
-                         : fn<false, 64, 4 __VA_ARGS__>))
+#define KG_GATE_PICK(fn, b16, G, row16, ...)                                                          \
+  ((b16) ? KG_GATE_SIZE(fn, true, G, row16, __VA_ARGS__) : KG_GATE_SIZE(fn, false, G, row16, __VA_ARGS__))
+#define KG_GATE_SIZE(fn, b16, G, row16, ...)            \
+  ((row16) ? ((G) <= 64    ? fn<b16, 16, 1 __VA_ARGS__> \
+              : (G) <= 128 ? fn<b16, 16, 2 __VA_ARGS__> \
+                           : fn<b16, 16, 4 __VA_ARGS__>) \
+           : ((G) <= 256   ? fn<b16, 64, 1 __VA_ARGS__> \
+              : (G) <= 512 ? fn<b16, 64, 2 __VA_ARGS__> \
+                           : fn<b16, 64, 4 __VA_ARGS__>))
 #define KG_GATE_COMMA_TRUE , true
 #define KG_GATE_COMMA_FALSE , false
 
@@ -642,9 +673,9 @@ extern "C" int kg_gate(const void* X, int64_t ldx, const float* bias, int64_t T,
   p.part_psum = stats ? (float*)(p.part_loss + gate_sum_blocks(G)) : nullptr;
   p.part_counts = stats ? (int*)(p.part_psum + blocks * G) : nullptr;
   // (the choice by biased scores holds two more than it makes)
-  const int lanes_for = bias && k + 2 > 16 && G <= 256 ? 257 : G;
-  void (*fn)(GateParams) = bias ? KG_GATE_PICK(kg_gate_kernel, b16, lanes_for, KG_GATE_COMMA_TRUE)
-                                : KG_GATE_PICK(kg_gate_kernel, b16, G, KG_GATE_COMMA_FALSE);
+  const bool row16 = gate_row16(T, G) && !(bias && k + 2 > 16);
+  void (*fn)(GateParams) = bias ? KG_GATE_PICK(kg_gate_kernel, b16, G, row16, KG_GATE_COMMA_TRUE)
+                                : KG_GATE_PICK(kg_gate_kernel, b16, G, row16, KG_GATE_COMMA_FALSE);
   const int rc = launch(fn, blocks, kGateThreads, 0, stream, p);
   if (rc != KG_OK || !stats) return rc;
   return launch(kg_gate_sum_kernel, gate_sum_blocks(G), 256, 0, stream, p, (int)blocks);
@@ -676,9 +707,10 @@ extern "C" int kg_gate_bwd(const void* X, int64_t ldx, const int32_t* idx, const
   p.X = X, p.idx = idx, p.dw = dw, p.counts = counts, p.dloss = dloss, p.dX = dX;
   p.T = T, p.ldx = ldx, p.ldd = ldd, p.coef = (float)coef, p.scale = (float)scale;
   p.G = G, p.k = k, p.flags = flags;
-  const int64_t rows = kGateThreads / 64 * (G <= 256 ? 4 : 1);
+  const bool row16 = gate_row16(T, G);
+  const int64_t rows = kGateThreads / 64 * (row16 ? 4 : 1);
   int64_t blocks = (T + rows - 1) / rows;
   if (blocks > 2 * kGateBlocks) blocks = 2 * kGateBlocks;
-  void (*fn)(GateBwdParams) = KG_GATE_PICK(kg_gate_bwd_kernel, b16, G, );
+  void (*fn)(GateBwdParams) = KG_GATE_PICK(kg_gate_bwd_kernel, b16, G, row16, );
   return launch(fn, blocks, kGateThreads, 0, stream, p);
 }
