@@ -148,17 +148,24 @@ __device__ __forceinline__ float sigmoid(float x) {
 // none), *inv: one over the sum (0 for a token without experts; finite for any sum).
 template <int LPR, int V>
 __device__ __forceinline__ void gate_scores(float (&x)[V], bool sig, float* top, float* inv) {
-  float m = -INFINITY, sum = 0.0f;
-  if (!sig) {
+  float m = 0.0f, sum = 0.0f;
+  if (sig) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = sigmoid(x[v]);
+      sum += x[v];
+    }
+  } else {
+    m = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
     m = max_of<LPR>(m);
     if (m == -INFINITY) m = 0.0f;
-  }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    x[v] = sig ? sigmoid(x[v]) : exp_less(x[v], m);
-    sum += x[v];
+    for (int v = 0; v < V; ++v) {
+      x[v] = exp_less(x[v], m);
+      sum += x[v];
+    }
   }
   sum = sum_of<LPR>(sum);
   *top = m;
@@ -304,10 +311,11 @@ __device__ __forceinline__ int choose_biased(const float (&x)[V], const float (&
                                              bool sig) {
   constexpr uint32_t MASK = kIndexBits<false, LPR>;
   uint32_t key[V];
+  const float factor = sig ? 1.0f : inv;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = Lanes<LPR, V / 4>::at(l, v);
-    const float f = i < G ? (sig ? s[v] : s[v] * inv) + bias[i] : 0.0f;
+    const float f = i < G ? fmaf(s[v], factor, bias[i]) : 0.0f;
     key[v] = ((i < G && x[v] > -INFINITY ? place(f) : kNever) & ~MASK) | id[v];
   }
   const uint32_t mine = largest_keys<false, LPR, V>(key, l, k + 2);  // (a token has that many lanes)
@@ -422,14 +430,21 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_kernel(GateParams p) {
     id[v] = kIndexBits<B16 && !BIAS, LPR> - (uint32_t)L::at(l, v);
   }
   const int64_t step = (int64_t)gridDim.x * WAVES * L::ROWS;
-  for (int64_t t0 = ((int64_t)blockIdx.x * WAVES + wave) * L::ROWS; t0 < p.T; t0 += step) {
+  const int64_t begin = ((int64_t)blockIdx.x * WAVES + wave) * L::ROWS;
+  float ahead[V];
+  auto load = [&](int64_t t0) {
+    const int64_t t = t0 + sub < p.T ? t0 + sub : p.T - 1;
+    gate_load<B16, LPR, C>((const char*)p.X + t * p.ldx * (B16 ? 2 : 4), p.G, l, ahead);
+  };
+  if (begin < p.T) load(begin);
+  for (int64_t t0 = begin; t0 < p.T; t0 += step) {
     const bool live = t0 + sub < p.T;
     const int64_t t = live ? t0 + sub : p.T - 1;
     const void* row = (const char*)p.X + t * p.ldx * (B16 ? 2 : 4);
     float x[V], s[V], top, inv;
-    gate_load<B16, LPR, C>(row, p.G, l, x);
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = x[v];
+    for (int v = 0; v < V; ++v) s[v] = x[v] = ahead[v];
+    if (t0 + step < p.T) load(t0 + step);  // the next tokens' logits are on their way meanwhile
     gate_scores<LPR, V>(s, sig, &top, &inv);
     int index;
     if constexpr (BIAS) index = choose_biased<B16, LPR, V>(x, s, id, inv, top, row, p.bias, p.G, l, p.k, sig);
@@ -552,21 +567,23 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_bwd_kernel(GateBwdParams
       dx[4 * c] = f.x, dx[4 * c + 1] = f.y, dx[4 * c + 2] = f.z, dx[4 * c + 3] = f.w;
     }
     wave_meets();
+    if (sig) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!sig) {
+      for (int v = 0; v < V; ++v) sum += s[v] * inv * even[v];
+      sum = sum_of<LPR>(sum);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        dx[v] = x[v] == -INFINITY ? 0.0f : s[v] * sigmoid(-x[v]) * (dx[v] + (even[v] - sum) * inv);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         s[v] *= inv;
         dx[v] += even[v];
         sum += s[v] * dx[v];
-      } else {
-        sum += s[v] * inv * even[v];
       }
-    }
-    sum = sum_of<LPR>(sum);
+      sum = sum_of<LPR>(sum);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (!sig) dx[v] = s[v] * (dx[v] - sum);
-      else dx[v] = x[v] == -INFINITY ? 0.0f : s[v] * sigmoid(-x[v]) * (dx[v] + (even[v] - sum) * inv);
+      for (int v = 0; v < V; ++v) dx[v] = s[v] * (dx[v] - sum);
     }
     if (!live) continue;
 #pragma unroll
@@ -574,7 +591,7 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_bwd_kernel(GateBwdParams
       const int i = (c * LPR + l) * 4;
       if constexpr (B16) {
         unsigned short* o = (unsigned short*)p.dX + t * p.ldd + i;
-        if (i + 4 <= p.G) {
+        if ((c + 1) * LPR * 4 <= p.G || i + 4 <= p.G) {
           *(h4_any*)o = h4_any{narrow(dx[4 * c]), narrow(dx[4 * c + 1]), narrow(dx[4 * c + 2]),
                                narrow(dx[4 * c + 3])};
         } else {
@@ -584,7 +601,7 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_bwd_kernel(GateBwdParams
         }
       } else {
         float* o = (float*)p.dX + t * p.ldd + i;
-        if (i + 4 <= p.G) {
+        if ((c + 1) * LPR * 4 <= p.G || i + 4 <= p.G) {
           *(f4_any*)o = f4_any{dx[4 * c], dx[4 * c + 1], dx[4 * c + 2], dx[4 * c + 3]};
         } else {
 #pragma unroll
