@@ -39,7 +39,7 @@ struct WParams {
   int tiles_n;
   int lds_rows;      // token rows that the streaming kernel's LDS holds
   int lds_s, lds_z;  // where scales and zero points begin there
-  int split;         // its waves that share the contraction axis of an output: 8 or 4
+  int waves, split;  // waves of a workgroup, and of those that share an output
 };
 
 // Formats: whole numbers by channels per scale, and e2m1.
@@ -145,9 +145,9 @@ __device__ __forceinline__ void meet() {
 
 // ------------------------------------------------------------------------ streaming kernel
 
-// A workgroup computes 16 NJ outputs of one expert for all its rows, as many rows at a time as its
-// LDS holds (16 at most), which come first. Its 8 waves take the blocks of 128 channels in turn,
-// each with D blocks of W under way, and add up in LDS in a fixed order.
+// A workgroup has one expert's rows in LDS, as many at a time as that holds (16 at most), and sets of
+// waves with 16 NJ outputs each; the waves of a set take runs of blocks of 128 channels, each with D
+// blocks of W under way, and add up in LDS in a fixed order.
 //
 // Tokens are the MFMA's rows, outputs its columns: a lane holds one output (of each tile), whose
 // codes and scales it reads itself, so scales need no exchange between lanes. A workgroup's
@@ -157,7 +157,7 @@ __device__ __forceinline__ void meet() {
 // two codes, four channels apart; the tokens' channels are put into the same order). A group's sum of
 // x (16 + q) then loses (16 + z) times the group's sum of x, which an MFMA with ones gives in the
 // lanes that need it, before it is scaled.
-constexpr int kW4Waves = 8;
+constexpr int kMaxSplit = 8;  // waves that share the contraction axis of an output
 
 // Scales that a lane holds per block of 128 channels (e2m1: of its own 32 channels).
 template <int GRP>
@@ -215,13 +215,13 @@ __device__ __forceinline__ constexpr int key_of(int r) {
   return chunk<GRP>(1, 0) == 1 ? r & 15 : (r & 10) | ((r & 1) << 2) | ((r >> 2) & 1);
 }
 
-// `bytes` bytes from memory (at any address) to LDS at smem + at, by all waves of the workgroup: whole
+// `bytes` bytes from memory (at any address) to LDS at smem + at, by all `waves` waves of the workgroup: whole
 // 16-byte units straight there, the last few bytes through registers once those have landed
 // (they would else be zeroed behind them). Up to the next KB is overwritten.
 __device__ __forceinline__ void copy_units(unsigned char* smem, int at, const unsigned char* from,
-                                           int bytes, int w, int lane) {
+                                           int bytes, int w, int waves, int lane) {
   const v4i r = make_rsrc(from, (uint32_t)bytes);
-  for (int x = w; 1024 * x < bytes; x += kW4Waves) {
+  for (int x = w; 1024 * x < bytes; x += waves) {
     const int o = 1024 * x + 16 * lane;
     load16_lds(r, lds_addr(smem) + at + 1024 * x, o + 16 <= bytes ? (uint32_t)o : kOobOffset);
   }
@@ -233,12 +233,13 @@ __device__ __forceinline__ void copy_rest(unsigned char* smem, int at, const uns
 }
 
 template <int GRP, bool SB, int NJ, bool OUTB>
-__global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WParams p) {
+__global__ __launch_bounds__(1024, 4) void kg_fprop_w4_stream_kernel(WParams p) {
   constexpr int N0 = 16 * NJ, NG = kScales<GRP>;
   constexpr int D = NJ == 2 ? 4 : 6, SBYTES = kScaleBytes<GRP, SB>;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int per = p.tiles_n;  // workgroups per expert
-  const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * N0 * (kW4Waves / p.split);
+  const int sets = p.waves / p.split;  // of waves, with outputs of their own
+  const int nth = blockIdx.x / per, n0 = (blockIdx.x - nth * per) * N0 * sets;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, j = lane & 15;
   int64_t row0;
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
   row0 = uniform((int)row0);  // below 2^31
   const int nk = (p.K + 127) / 128, pieces = max(1, (nk + 3) / 4);
   const int kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
-  const int all = min(N0 * (kW4Waves / p.split), p.N - n0);  // outputs of the workgroup
+  const int all = min(N0 * sets, p.N - n0);  // outputs of the workgroup
   const int64_t out0 = (int64_t)g * p.N + n0;
   const unsigned char* sbase = p.sw + out0 * groups * SBYTES;
   const unsigned char* zbase = p.zp + out0 * groups;
@@ -270,8 +271,8 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
   }
   // the outputs' scales and zero points, which lie side by side
   const int sbytes = all * groups * SBYTES, zbytes = zeros ? all * groups : 0;
-  copy_units(smem, p.lds_s, sbase, sbytes, w, lane);
-  if (zeros) copy_units(smem, p.lds_z, zbase, zbytes, w, lane);
+  copy_units(smem, p.lds_s, sbase, sbytes, w, p.waves, lane);
+  if (zeros) copy_units(smem, p.lds_z, zbase, zbytes, w, p.waves, lane);
   for (int r0 = 0; r0 < rows; r0 += p.lds_rows) {
     const int here = min(p.lds_rows, rows - r0);
     // the tokens, a row's 4 blocks of 256 bytes per load of a wave; channels past K are zeros
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
         const int ch = 8 * (j ^ key_of<GRP>(row & 15)) + 128 * (4 * piece + q);
         load16_lds(ar, lds + 1024 * (row * pieces + piece),
                    ch < p.K ? (uint32_t)(row * (int)lda2 + 2 * ch) : kOobOffset);
-        piece += kW4Waves;
+        piece += p.waves;
         while (piece >= pieces) piece -= pieces, ++row;
       }
     }
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
       copy_rest(smem, p.lds_z, zbase, zbytes, threadIdx.x);
     }
     if constexpr (GRP != kE2M1) {
-      for (int c = threadIdx.x; c < here * pieces * 64; c += 64 * kW4Waves) {
+      for (int c = threadIdx.x; c < here * pieces * 64; c += 64 * p.waves) {
         v4i* x = (v4i*)smem + c;
         *x = __builtin_bit_cast(v4i, by_fours(*x));
       }
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
         const float* f = (const float*)(sums + (side * p.split * NJ + i) * 64 + lane) + part;
         x[i] = f[0];
 #pragma unroll
-        for (int v = 1; v < kW4Waves; ++v)
+        for (int v = 1; v < kMaxSplit; ++v)
           if (v < p.split) x[i] += f[v * NJ * 64 * 4];
       }
       const int row = 4 * q + part;
@@ -418,23 +419,29 @@ __global__ __launch_bounds__(64 * kW4Waves, 4) void kg_fprop_w4_stream_kernel(WP
 
 // ---------------------------------------------------------------------------- tiled kernel
 
-// BT tokens x BN outputs per workgroup of 8 waves (WT along the tokens), two LDS stages of 64
-// channels: widened weights, tokens, and whole-number codes' scales. Codes, scales and tokens come
-// into registers D blocks ahead (the compiler counts those loads); during block kb the threads
-// widen block kb + 1 into the other stage, a word between MFMAs.
+// BT tokens x BN outputs per workgroup of 8 waves, two LDS stages of KS times 64 channels: widened
+// weights, tokens, and whole-number codes' scales. Codes, scales and tokens come into registers D
+// blocks ahead (the compiler counts those loads); during block kb the threads widen block kb + 1
+// into the other stage, a word between MFMAs.
+//
+// With KS = 2 each half of the waves (WT of them along the tokens) multiplies one half of a block's
+// channels, and the halves' sums are joined in LDS at the end. A block's time in a small tile is
+// latency, so longer blocks are what makes few tiles fast.
 //
 // Outputs are the MFMA's rows, tokens its columns, as in kg_fprop: by the order in which
 // the outputs are dealt to its rows a lane holds eight neighbouring outputs of one token.
-template <int BT_, int BN_, int WT_, int PER_CU_, int D_>
+template <int BT_, int BN_, int WT_, int KS_, int D_>
 struct WCfg {
-  static constexpr int BT = BT_, BN = BN_, WT = WT_, WN = 8 / WT_, PER_CU = PER_CU_, D = D_;
-  static constexpr int THREADS = 512, TK = 64;
+  static constexpr int BT = BT_, BN = BN_, WT = WT_, KS = KS_, WN = 8 / KS_ / WT_, D = D_;
+  static constexpr int THREADS = 512, TK = 64 * KS;
   static constexpr int TT = BT / WT / 16;  // 16-token tiles of a wave
   static constexpr int NI = BN / WN / 16;  // 16-output tiles of a wave
-  static constexpr int OPW = BN * 128, OPT = BT * 128, STAGE = OPW + OPT + 2 * BN * 4;
-  static constexpr int WORDS = BN / 64;              // of eight codes, of a thread and block
-  static constexpr int UNITS = (BT * 8 + 511) / 512; // of 16 bytes of tokens
-  static_assert(NI % 2 == 0 && (BN == 128 || BN == 256), "whole runs of outputs, whole words");
+  static constexpr int OPW = BN * 128, OPT = BT * 128, PART = OPW + OPT + 2 * BN * 4;
+  static constexpr int STAGE = KS * PART;
+  static constexpr int WORDS = BN * KS / 64;              // of eight codes, of a thread and block
+  static constexpr int UNITS = (BT * 8 * KS + 511) / 512; // of 16 bytes of tokens
+  static_assert(NI % 2 == 0 && (WORDS == 2 || WORDS == 4), "whole runs of outputs, whole words");
+  static_assert((KS - 1) * BT * BN * 4 <= 2 * STAGE, "the halves' sums fit");
 };
 // Row m of MFMA row tile i holds output wrow(i, m) of the wave's.
 __device__ __forceinline__ constexpr int wrow(int i, int m) {
@@ -445,9 +452,9 @@ __device__ __forceinline__ constexpr int key_t(int r) { return r & 7; }
 __device__ __forceinline__ constexpr int key_w(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
 
 template <class C, int GRP, bool SB, bool OUTB>
-__global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(WParams p) {
+__global__ __launch_bounds__(C::THREADS, 2) void kg_fprop_w4_kernel(WParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  constexpr int TT = C::TT, NI = C::NI, D = C::D, BN = C::BN, BT = C::BT;
+  constexpr int TT = C::TT, NI = C::NI, D = C::D, BN = C::BN, BT = C::BT, KS = C::KS;
   constexpr bool INT = GRP != kE2M1;
   constexpr int NG = GRP == 32 ? 2 : 1;  // scales of an output and block (whole numbers)
   int* off = (int*)(smem + 2 * C::STAGE);  // [G + 1]
@@ -463,15 +470,16 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(
   const int nk = (p.K + C::TK - 1) / C::TK, kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
   const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6);
   const int q = lane >> 4, j = lane & 15;
-  const int wt = w % C::WT, wn = w / C::WT;
+  const int hk = w / (8 / KS), wt = w % C::WT, wn = w % (8 / KS) / C::WT;
   const int c0 = 16 * (q ^ (j & 7)), c1 = 16 * ((q + 4) ^ (j & 7));
-  const unsigned char* fragw = smem + (wn * NI * 16 + wrow(0, j)) * 128;
-  const unsigned char* fragt = smem + C::OPW + (wt * TT * 16 + j) * 128;
-  const unsigned char* scales = smem + C::OPW + C::OPT + (wn * NI * 16 + 8 * q) * 4;
+  const unsigned char* own = smem + hk * C::PART;
+  const unsigned char* fragw = own + (wn * NI * 16 + wrow(0, j)) * 128;
+  const unsigned char* fragt = own + C::OPW + (wt * TT * 16 + j) * 128;
+  const unsigned char* scales = own + C::OPW + C::OPT + (wn * NI * 16 + 8 * q) * 4;
   // this thread's codes: words [first, first + WORDS) of eight codes of output `out`
   constexpr int PER_ROW = 512 / BN;
   const int out = t / PER_ROW, first = t % PER_ROW * C::WORDS;
-  const int half = first / 4;  // of the block's channels
+  const int side = first / 8, quarter = first / 4;  // 64 channels, 32 channels of the block
   for (int base = 0; base < total; base += grid) {
     const int idx = base + slot;
     if (idx >= total) break;
@@ -494,22 +502,24 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(
     const unsigned char* zbase = p.zp ? p.zp + out0 * groups : sbase;
     const unsigned char* abase = p.A + (int64_t)row0 * p.lda * 2;
     const int lda2 = (int)(2 * p.lda);
-    const uint32_t woff = (uint32_t)(out * kbytes + 4 * first), soff = (uint32_t)(out * groups + (kPerScale<GRP> == 32 ? half : 0));
+    const uint32_t woff = (uint32_t)(out * kbytes + 4 * first), soff = (uint32_t)(out * groups + (kPerScale<GRP> == 32 ? quarter : GRP == 64 ? side : 0));
     // Ring of the loads. Rows and outputs that do not exist and blocks past the last one read as
     // zeros; so do the tokens' channels past K.
     v4i ax[D][C::UNITS], wx[D];
     uint32_t sx[D], zx[D];
     auto load_tokens = [&](int kb, int d, int x) {
-      const Rsrc ar = rsrc_of(abase + (int64_t)kb * 128,
-                              kb < nk ? (uint32_t)((rows - 1) * lda2 + min(128, 2 * p.K - 128 * kb)) : 0u);
-      const int u = 512 * x + t, c = u & 7;
-      const bool ok = (BT * 8 % 512 == 0 || u < BT * 8) && 64 * kb + 8 * c < p.K;
-      ax[d][x] = load16(ar, ok ? (uint32_t)((u >> 3) * lda2 + 16 * c) : kOobOffset);
+      const int left = min(2 * C::TK, 2 * p.K - 2 * C::TK * kb);
+      const Rsrc ar = rsrc_of(abase + (int64_t)kb * 2 * C::TK,
+                              kb < nk ? (uint32_t)((rows - 1) * lda2 + left) : 0u);
+      const int u = 512 * x + t, c = u % (8 * KS);
+      const bool ok = (BT * 8 * KS % 512 == 0 || u < BT * 8 * KS) && 16 * c < left;
+      ax[d][x] = load16(ar, ok ? (uint32_t)(u / (8 * KS) * lda2 + 16 * c) : kOobOffset);
     };
     auto load_codes = [&](int kb, int d) {
       const bool in = kb < nk;
-      const int n = GRP == 128 ? kb >> 1 : GRP == 64 ? kb : 2 * kb;  // first scale of an output
-      const Rsrc wr = rsrc_of(wbase + kb * 32, in ? (uint32_t)(outs * kbytes - kb * 32) : 0u);
+      const int n = kb * C::TK / kPerScale<GRP>;  // an output's first scale
+      const Rsrc wr = rsrc_of(wbase + kb * (C::TK / 2),
+                              in ? (uint32_t)max(0, outs * kbytes - kb * (C::TK / 2)) : 0u);
       const Rsrc sr = rsrc_of(sbase + n * kScaleBytes<GRP, SB>,
                               in ? (uint32_t)((outs * groups - n) * kScaleBytes<GRP, SB>) : 0u);
       if constexpr (C::WORDS == 4) {
@@ -518,8 +528,9 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(
         const v2i x = load8(wr, woff);
         wx[d] = v4i{x.x, x.y, 0, 0};
       }
-      // (the second half of K's last block may not exist)
-      const uint32_t at = kPerScale<GRP> > 32 || n + half < groups ? soff : kOobOffset / 4;
+      // (the last channels of K's last block may not exist)
+      const bool exists = C::TK * kb + 32 * quarter < p.K;
+      const uint32_t at = exists ? soff : kOobOffset / 4;
       if constexpr (!INT) {
         sx[d] = load1(sr, at);
       } else {
@@ -534,21 +545,23 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(
       for (int tt = 0; tt < TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
     // What this thread writes of block kb, held in slot d, into its stage
     auto put_tokens = [&](int kb, int d, int x) {
-      const int u = 512 * x + t, r = u >> 3;
-      if (BT * 8 % 512 == 0 || u < BT * 8)
-        *(v4i*)(smem + (kb & 1) * C::STAGE + C::OPW + r * 128 + 16 * ((u & 7) ^ key_t(r))) = ax[d][x];
+      const int u = 512 * x + t, r = u / (8 * KS), c = u % (8 * KS);
+      if (BT * 8 * KS % 512 == 0 || u < BT * 8 * KS)
+        *(v4i*)(smem + (kb & 1) * C::STAGE + c / 8 * C::PART + C::OPW + r * 128 +
+                16 * ((c & 7) ^ key_t(r))) = ax[d][x];
     };
     auto put_word = [&](int kb, int d, int n) {
       v8bf v;
       if constexpr (INT) v = eight_less((uint32_t)wx[d][n], p.zp ? (float)zx[d] : 8.f);
       else v = eight_e2m1((uint32_t)wx[d][n], as_float(sx[d] << 23));
-      *(v8bf*)(smem + (kb & 1) * C::STAGE + out * 128 + 16 * ((first + n) ^ key_w(out))) = v;
+      *(v8bf*)(smem + (kb & 1) * C::STAGE + side * C::PART + out * 128 +
+               16 * ((first % 8 + n) ^ key_w(out))) = v;
     };
     auto put_scale = [&](int kb, int d) {
       if constexpr (INT)
         if (first % (GRP == 32 ? 4 : 8) == 0)
-          *(float*)(smem + (kb & 1) * C::STAGE + C::OPW + C::OPT + ((GRP == 32 ? half : 0) * BN + out) * 4) =
-              as_float(SB ? sx[d] << 16 : sx[d]);
+          *(float*)(smem + (kb & 1) * C::STAGE + side * C::PART + C::OPW + C::OPT +
+                    ((GRP == 32 ? quarter % 2 : 0) * BN + out) * 4) = as_float(SB ? sx[d] << 16 : sx[d]);
     };
     v8bf tf[TT][2], wf[2][2];
     v4f sc[3][NG];
@@ -640,10 +653,32 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(
       for (int d = 0; d < D; ++d)
         if (k0 + d < nk) block(k0 + d, (d + 1) % D);
     }
+    if constexpr (KS == 2) {
+      v4f* sums = (v4f*)smem + (w % 4) * NI * TT * 64 + lane;
+      __syncthreads();  // every wave has read the last stage
+      if (hk == 1) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt) sums[(i * TT + tt) * 64] = acc[i][tt];
+      }
+      __syncthreads();
+      if (hk == 0) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt) {
+            const v4f y = sums[(i * TT + tt) * 64];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][tt][r] += y[r];
+          }
+      }
+      __syncthreads();  // the next tile's first stage may take their place
+    }
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
       const int r = (wt * TT + tt) * 16 + j;
-      if (r >= rows) continue;
+      if (r >= rows || hk != 0) continue;
       const int64_t at = (int64_t)(row0 + r) * p.ldd + n0;
 #pragma unroll
       for (int i = 0; i < NI; i += 2) {
@@ -658,7 +693,7 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_fprop_w4_kernel(
 
 struct WLaunch {
   const void* fn;
-  int bt, bn, lds, per_cu;
+  int bt, bn, lds;
 };
 
 // The kernel by type: format, scale type, result type.
@@ -688,8 +723,98 @@ struct TiledOf {
 };
 template <class C>
 static WLaunch w_tiled(int kind, int group, bool outb) {
-  return WLaunch{w_pick<TiledOf<C>::template F>(kind, group, outb), C::BT, C::BN, 2 * C::STAGE,
-                 C::PER_CU};
+  return WLaunch{w_pick<TiledOf<C>::template F>(kind, group, outb), C::BT, C::BN, 2 * C::STAGE};
+}
+
+// Which kernel and tile, by M_total and G (the experts' sizes are known on the device only), from
+// estimates of the time in ns whose figures are measured; every choice is right for every
+// distribution of the rows. Measured in us, equal rows, streaming / 32 x 128 / 64 x 128 / 128 x 128 /
+// 128 x 256 (/ 256 x 256):
+//   e2m1  1 expert, N 4096, K 7168    16 rows 14 / 32 / 39 / 50 / 84, 64 rows 42 / 34 / 39 / 51 / 85
+//         8 of N 2048, K 2048         16 rows each 10 / 13 / 15 / 19 / 28 / 43, 128 rows - / 24 / 18 / 21 / 30 / 45
+//         32 of N 4096, K 7168        4 rows each 74 / 169 / 180 / 208 / 214 / 300,
+//                                     256 rows - / 1111 / 683 / 490 / 490 / 386
+//   whole numbers, 128 per scale, the last 32 experts
+//                                     4 rows each 81 / 217 / 239 / 301 / 292, 256 rows - / 1595 / 938 / 653 / 625
+
+// Streaming: 16 waves on a compute unit, as two workgroups, or as one whose LDS then holds twice the
+// rows. A set has 16 outputs where 32 would leave half of the compute units idle; 8 waves share
+// them, or 4 where that still makes four workgroups for each compute unit.
+struct WStream {
+  int64_t rows, lds, tokens, scales, ns;  // rows 0: it cannot be used
+  int nj, waves, split;
+};
+static WStream w_stream(int64_t M, int G, int N, int K, int cus, int kind, int group, bool zp) {
+  const int64_t live = G < M ? G : M, per_out = K / group, nk = (K + 127) / 128;
+  const int sb = kind == KG_W4_E2M1 ? 1 : kind == KG_W4_INT_BF16 ? 2 : 4;
+  auto kbytes = [](int64_t n) { return (n + 1023) / 1024 * 1024; };
+  const int64_t row_bytes = kbytes(nk * 256);
+  const int64_t most = M < 16 ? M : 16, uneven = G == 1 ? M : (3 * ((M + G - 1) / G) + 1) / 2;
+  const int64_t block_ns = kind == KG_W4_E2M1 ? 400 : group == 32 ? 850 : 600;
+  WStream best;
+  best.rows = 0;
+  best.ns = INT64_MAX;
+  for (int waves = 8; waves <= 16; waves += 8) {
+    WStream s;
+    s.waves = waves;
+    s.nj = live * ((N + 31) / 32) <= cus / 2 ? 1 : 2;
+    s.split = s.nj == 2 && live * ((N + 8 * waves - 1) / (8 * waves)) >= 4 * cus ? 4 : 8;
+    const int bn = 16 * s.nj * waves / s.split;
+    s.scales = kbytes(bn * per_out * sb);
+    const int64_t rest = s.scales + (zp ? kbytes(bn * per_out) : 0);
+    const int64_t room = (waves == 8 ? 79 : 159) * 1024 - rest;
+    s.rows = row_bytes ? room / row_bytes : 16;
+    if (s.rows > most) s.rows = most;
+    if (s.rows < 1) continue;
+    s.tokens = kbytes(s.rows * row_bytes);
+    if (s.tokens < waves * s.nj * 1024) s.tokens = waves * s.nj * 1024;
+    s.lds = s.tokens + rest;
+    // a workgroup's start and end, and a wave's blocks
+    const int64_t wgs = live * ((N + bn - 1) / bn), slots = (int64_t)cus * 16 / waves;
+    const int64_t passes = (uneven + s.rows - 1) / s.rows, blocks = nk / s.split + 1;
+    s.ns = 3000 + passes * ((wgs + slots - 1) / slots) *
+                      (2600 + blocks * block_ns * (wgs * waves > 8 * cus ? 2 : 1));
+    if (s.ns < best.ns) best = s;
+  }
+  return best;
+}
+
+// Tiles: rounds over the compute units times the blocks' time. Of several experts each has a last
+// tile that is half filled on average.
+struct WTile {
+  WLaunch l;
+  int64_t ns;
+};
+static WTile w_tile(int64_t M, int G, int N, int K, int cus, int kind, int group, bool outb) {
+  const bool mx = kind == KG_W4_E2M1;
+  struct {
+    int bt, bn, ns;  // of 128 channels
+  } const tiles[] = {{32, 128, mx ? 500 : 780},
+                     {64, 128, mx ? 630 : 940},
+                     {128, 128, mx ? 830 : 1270},
+                     {128, 256, mx ? 1500 : 2200},
+                     {256, 256, 2350}};
+  const int64_t live = G < M ? G : M;
+  int best = 0;
+  WTile t;
+  t.ns = INT64_MAX;
+  for (int i = 0; i < (mx ? 5 : 4); ++i) {
+    int64_t mt = live == 1 ? (M + tiles[i].bt - 1) / tiles[i].bt * 2 : 2 * M / tiles[i].bt + live;
+    if (mt < 2 * live) mt = 2 * live;
+    const int64_t n = (mt * ((N + tiles[i].bn - 1) / tiles[i].bn) + 1) / 2;
+    const int64_t ns = 4500 + (n + cus - 1) / cus * ((K + 127) / 128 * tiles[i].ns + 1000);
+    if (ns < t.ns) t.ns = ns, best = i;
+  }
+  // (256 x 256 for e2m1 only: with the sums of whole numbers' groups it does not fit the registers)
+  using Large = WCfg<256, 256, 4, 1, 1>;
+  t.l = best == 0   ? w_tiled<WCfg<32, 128, 1, 2, 2>>(kind, group, outb)
+        : best == 1 ? w_tiled<WCfg<64, 128, 2, 2, 2>>(kind, group, outb)
+        : best == 2 ? w_tiled<WCfg<128, 128, 2, 2, 1>>(kind, group, outb)
+        : best == 3 ? w_tiled<WCfg<128, 256, 2, 1, 2>>(kind, group, outb)
+                    : WLaunch{outb ? (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, true>
+                                   : (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, false>,
+                              Large::BT, Large::BN, 2 * Large::STAGE};
+  return t;
 }
 
 // Lets a kernel have all of a compute unit's LDS, once per kernel and device.
@@ -753,55 +878,36 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
   p.N = N;
   p.K = K;
   p.lds_rows = p.lds_s = p.lds_z = 0;
-  p.split = kW4Waves;
-  // Which kernel and tile, by M_total and G (the experts' sizes are known on the device only); every
-  // choice is right for every distribution of the rows.
-  const int64_t avg = (M_total + G - 1) / G, live = G < M_total ? G : M_total;
-  // Streaming: a workgroup's LDS holds scales, zero points and as many rows as fit
-  // A workgroup has 16 outputs where 32 would leave half of the compute units idle, 64 (two sets of
-  // 32, four waves each) where those make four workgroups or more for each compute unit.
-  const bool narrow = live * ((N + 31) / 32) <= cus / 2, wide = live * ((N + 63) / 64) >= 4 * cus;
-  const int bn = narrow ? 16 : wide ? 64 : 32;
-  auto kbytes = [](int64_t n) { return (n + 1023) / 1024 * 1024; };
-  const int64_t row_bytes = kbytes((K + 127) / 128 * 256), per_out = K / group;
-  const int64_t scales_at = kbytes(bn * per_out * sb), zeros_at = zp ? kbytes(bn * per_out) : 0;
-  const int64_t rest = scales_at + zeros_at + 1024;
-  int64_t hold = row_bytes ? (76 * 1024 - rest) / row_bytes : 16;
-  if (hold < 2 * avg && row_bytes) hold = (156 * 1024 - rest) / row_bytes;
-  if (hold > 16) hold = 16;
-  if (hold > M_total) hold = M_total;
+  p.waves = p.split = 8;
   WLaunch l;
   int64_t grid;
-  if (hold > 0 && (2 * avg <= hold || M_total <= hold)) {
-    l.fn = narrow ? w_pick<StreamOf<1>::F>(kind, group, outb) : w_pick<StreamOf<2>::F>(kind, group, outb);
-    l.bn = bn;
-    p.lds_rows = (int)hold;
-    int64_t tokens = kbytes(hold * row_bytes);
-    const int64_t sums = kW4Waves * (narrow ? 1 : 2) * 1024;
-    if (tokens < sums) tokens = sums;
-    p.lds_s = (int)tokens;
-    p.lds_z = (int)(tokens + scales_at);
-    l.lds = (int)(tokens + scales_at + zeros_at);
-    p.tiles_n = (N + l.bn - 1) / l.bn;
+  int threads = 512;
+  const WStream st = w_stream(M_total, G, N, K, cus, kind, group, zp != nullptr);
+  const int64_t live = G < M_total ? G : M_total;
+  const WTile tile = w_tile(M_total, G, N, K, cus, kind, group, outb);
+  if (st.rows > 0 && st.ns <= tile.ns) {
+    const int bn = 16 * st.nj * st.waves / st.split;
+    l.fn = st.nj == 1 ? w_pick<StreamOf<1>::F>(kind, group, outb) : w_pick<StreamOf<2>::F>(kind, group, outb);
+    l.lds = (int)st.lds;
+    p.lds_rows = (int)st.rows;
+    p.waves = st.waves, p.split = st.split;
+    threads = 64 * st.waves;
+    p.lds_s = (int)st.tokens;
+    p.lds_z = (int)(st.tokens + st.scales);
+    p.tiles_n = (N + bn - 1) / bn;
     grid = live * p.tiles_n;
-    if (grid > INT32_MAX / 512) return KG_ERR_UNSUPPORTED;
+    if (grid > INT32_MAX / 1024) return KG_ERR_UNSUPPORTED;
   } else {
-    using Large = WCfg<256, 256, 4, 1, 1>;
-    l = avg <= 32    ? w_tiled<WCfg<32, 256, 1, 2, 2>>(kind, group, outb)
-        : avg <= 64  ? w_tiled<WCfg<64, 128, 2, 2, 2>>(kind, group, outb)
-        : avg <= 128 ? w_tiled<WCfg<128, 128, 2, 1, 2>>(kind, group, outb)
-        : mx && avg > 256 ? WLaunch{outb ? (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, true> : (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, false>, Large::BT, Large::BN, 2 * Large::STAGE, 1}
-                     : w_tiled<WCfg<128, 256, 2, 1, 2>>(kind, group, outb);
+    l = tile.l;
     l.lds += 2 * (G + 1) * 4;
     p.tiles_n = (N + l.bn - 1) / l.bn;
     const int64_t max_items = (M_total / l.bt + G) * (int64_t)p.tiles_n;
     if (max_items > INT32_MAX - 4096) return KG_ERR_UNSUPPORTED;  // (indexes pass it by a grid)
-    const int64_t at_once = (int64_t)cus * l.per_cu;
-    grid = max_items < at_once ? max_items : at_once;
+    grid = max_items < cus ? max_items : cus;
   }
   if (!w_lds_allowed(l.fn, dev)) return KG_ERR_HIP;
   void* args[] = {&p};
-  return hipLaunchKernel(l.fn, dim3((unsigned)grid), dim3(512), args, (size_t)l.lds,
+  return hipLaunchKernel(l.fn, dim3((unsigned)grid), dim3((unsigned)threads), args, (size_t)l.lds,
                          (hipStream_t)stream) == hipSuccess
              ? KG_OK
              : KG_ERR_HIP;

@@ -106,6 +106,16 @@ def test_one_row_of_long_ones(kind, group, G, M):
     check(A, W, sw, zp, m, group, torch.float32)
 
 
+@pytest.mark.parametrize("kind,group", KINDS)
+@pytest.mark.parametrize("G,N,K,total", [(60, 2080, 256, 80), (70, 4200, 128, 300), (33, 4100, 640, 33), (200, 1030, 128, 1500)])
+def test_many_workgroups(kind, group, G, N, K, total):
+    """More workgroups than compute units hold at once, in which several sets of outputs share rows."""
+    gen = torch.Generator().manual_seed(G)
+    ms = torch.bincount(torch.randint(0, G, (total,), generator=gen), minlength=G).tolist()
+    A, W, sw, zp, m = make(ms, N, K, group, kind, G)
+    check(A, W, sw, zp, m, group, torch.bfloat16 if kind == "bf16" else torch.float32)
+
+
 def test_zero_points_past_fifteen():
     A, W, sw, zp, m = make([5, 70], 40, 256, 64, "f32", 1)
     zp.copy_(torch.arange(zp.numel(), device="cuda").view(zp.shape) % 256)
