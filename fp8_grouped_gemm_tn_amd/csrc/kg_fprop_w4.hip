@@ -730,16 +730,19 @@ static WLaunch w_tiled(int kind, int group, bool outb) {
 // estimates of the time in ns whose figures are measured; every choice is right for every
 // distribution of the rows. Measured in us, equal rows, streaming / 32 x 128 / 64 x 128 / 128 x 128 /
 // 128 x 256 (/ 256 x 256):
-//   e2m1  1 expert, N 4096, K 7168    16 rows 14 / 32 / 39 / 50 / 84, 64 rows 42 / 34 / 39 / 51 / 85
-//         8 of N 2048, K 2048         16 rows each 10 / 13 / 15 / 19 / 28 / 43, 128 rows - / 24 / 18 / 21 / 30 / 45
-//         32 of N 4096, K 7168        4 rows each 74 / 169 / 180 / 208 / 214 / 300,
-//                                     256 rows - / 1111 / 683 / 490 / 490 / 386
+//   e2m1  1 expert, N 4096, K 7168    16 rows 18 / 32 / 39 / 49 / 83, 64 rows 56 / 34 / 39 / 50 / 85
+//         8 of N 2048, K 2048         16 rows each 10 / 13 / 15 / 19 / 28 / 43, 128 rows 49 / 24 / 18 / 21 / 30 / 45
+//         32 of N 4096, K 7168        4 rows each 101 / 171 / 182 / 208 / 216 / 304,
+//                                     256 rows - / 1127 / 695 / 504 / 517 / 397
 //   whole numbers, 128 per scale, the last 32 experts
-//                                     4 rows each 81 / 217 / 239 / 301 / 292, 256 rows - / 1595 / 938 / 653 / 625
+//                                     4 rows each 109 / 231 / 241 / 295 / 287, 256 rows - / 1588 / 940 / 672 / 663
+// (The estimates take experts' rows to be uneven, so at equal rows the next larger tile may be taken.)
 
 // Streaming: 16 waves on a compute unit, as two workgroups, or as one whose LDS then holds twice the
-// rows. A set has 16 outputs where 32 would leave half of the compute units idle; 8 waves share
-// them, or 4 where that still makes four workgroups for each compute unit.
+// rows (8 rows of 8 experts, N 4096, K 7168, e2m1: 42 us as two, 24 as one; 2 rows: 22 and 23). A set
+// has 16 outputs where 32 would leave half of the compute units idle (1 row of 1 expert: 6.9 us with
+// 16, 8.3 with 32; 2 rows of 8 experts: 34 and 27). 8 waves share them, or 4 where that still fills
+// every compute unit (2 rows of 8 experts: 27 us with 8, 22 with 4; of 1 expert: 8.3 and 11).
 struct WStream {
   int64_t rows, lds, tokens, scales, ns;  // rows 0: it cannot be used
   int nj, waves, split;
@@ -758,7 +761,7 @@ static WStream w_stream(int64_t M, int G, int N, int K, int cus, int kind, int g
     WStream s;
     s.waves = waves;
     s.nj = live * ((N + 31) / 32) <= cus / 2 ? 1 : 2;
-    s.split = s.nj == 2 && live * ((N + 8 * waves - 1) / (8 * waves)) >= 4 * cus ? 4 : 8;
+    s.split = s.nj == 2 && live * ((N + 63) / 64) >= 2 * cus ? 4 : 8;
     const int bn = 16 * s.nj * waves / s.split;
     s.scales = kbytes(bn * per_out * sb);
     const int64_t rest = s.scales + (zp ? kbytes(bn * per_out) : 0);
