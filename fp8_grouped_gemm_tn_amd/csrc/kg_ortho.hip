@@ -36,7 +36,7 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr float kScaleA = 0x1p13f, kScaleB = 0x1p13f, kLow = 0x1p11f;
-constexpr int kNormChunks = 64;  // partial sums of squares per matrix
+constexpr int kNormChunks = 256;  // partial sums of squares per matrix, at most
 constexpr int kOrthoMax = 1 << 16;
 
 struct OParams {
@@ -50,42 +50,61 @@ struct OParams {
   int G, R, C, n, m, np, mp, ldn, ldm;
   int b16, wide, tiles_i, tiles_j, per;  // per: tiles of a matrix
   int low_in, low_out;
+  int chunks;
 };
 
-__device__ __forceinline__ float u_at(const OParams& p, int64_t i) {
-  return p.b16 ? __builtin_bit_cast(float, (uint32_t)((const unsigned short*)p.U)[i] << 16)
-               : ((const float*)p.U)[i];
+// Eight neighbours of U, of which the first `n` are there; the rest are zeros.
+__device__ __forceinline__ void u_eight(const OParams& p, int64_t at, int n, float* x) {
+  typedef unsigned short h8 __attribute__((ext_vector_type(8), aligned(2)));
+  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+  if (p.b16) {
+    const unsigned short* u = (const unsigned short*)p.U + at;
+    h8 h = {};
+    if (n >= 8) {
+      h = *(const h8*)u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) h[e] = u[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_bit_cast(float, (uint32_t)h[e] << 16);
+  } else {
+    const float* u = (const float*)p.U + at;
+    f4 f[2] = {};
+    if (n >= 8) {
+      f[0] = *(const f4*)u;
+      f[1] = *(const f4*)(u + 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) f[e >> 2][e & 3] = u[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = f[e >> 2][e & 3];
+  }
 }
 
 // ---------------------------------------------------------------------------- norm, first X
 
 // Sums of squares in 64 bits (fp32 squares of gradients may leave its range), in a fixed order.
+// 8 x 4096 x 7168 bf16: 96 us, 4.9 TB/s.
+constexpr int kNormStep = 8 * 256;
+__host__ __device__ constexpr int64_t norm_chunk(int64_t size) {
+  const int64_t even = (size + kNormChunks - 1) / kNormChunks;
+  return (even + 2 * kNormStep - 1) / (2 * kNormStep) * (2 * kNormStep);
+}
 __global__ __launch_bounds__(256) void kg_ortho_norm_kernel(OParams p) {
   __shared__ double sums[4];
-  const int64_t size = (int64_t)p.R * p.C, base = (int64_t)blockIdx.y * size;
-  const int64_t per = (size + kNormChunks * 1024 - 1) / (kNormChunks * 1024) * 1024;
+  const int64_t size = (int64_t)p.R * p.C, base = (int64_t)blockIdx.y * size, per = norm_chunk(size);
   const int64_t from = blockIdx.x * per, to = from + per < size ? from + per : size;
   double s = 0;
-  int64_t i = from + 4 * threadIdx.x;
-  for (; i + 4 <= to; i += 1024) {
-    float x[4];
-    if (p.b16) {
-      typedef unsigned short h4 __attribute__((ext_vector_type(4), aligned(2)));
-      const h4 h = *(const h4*)((const unsigned short*)p.U + base + i);
+#pragma unroll 4
+  for (int64_t i = from + 8 * threadIdx.x; i < to; i += kNormStep) {
+    float x[8];
+    u_eight(p, base + i, to - i < 8 ? (int)(to - i) : 8, x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = __builtin_bit_cast(float, (uint32_t)h[e] << 16);
-    } else {
-      typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
-      const f4 f = *(const f4*)((const float*)p.U + base + i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = f[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s = fma((double)x[e], (double)x[e], s);
-  }
-  for (; i < to && i < from + per; ++i) {
-    const double x = u_at(p, base + i);
-    s = fma(x, x, s);
+    for (int e = 0; e < 8; ++e) s = fma((double)x[e], (double)x[e], s);
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
@@ -96,71 +115,90 @@ __global__ __launch_bounds__(256) void kg_ortho_norm_kernel(OParams p) {
 }
 
 // X and X^T of U / |U|, scaled, with their low halves; zeros in the padding. One 64 x 64 tile
-// per workgroup, turned in LDS.
+// per workgroup, turned in LDS (16-byte chunk c of a row in slot c ^ its key, as the reads that
+// turn it take four neighbouring rows at once). Memory bounds it: 8 x 4096 x 7168 bf16 370 us, 5.1 TB/s.
 __global__ __launch_bounds__(256) void kg_ortho_init_kernel(OParams p) {
-  __shared__ unsigned short hi[64][72], lo[64][72];
+  __shared__ __attribute__((aligned(16))) unsigned char lds[2][64 * 128];  // X, low halves
   __shared__ double inv_s;
   const int g = blockIdx.y, t = threadIdx.x;
+  // rows and columns of U, and of the padded matrix
+  const int cp = p.wide ? p.mp : p.np;
+  const int across = cp / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
+  const int64_t base = (int64_t)g * p.R * p.C;
+  const int r = t >> 3, c = t & 7;
+  float x[2][8];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int row = r0 + r + 32 * half, col = c0 + 8 * c;
+    u_eight(p, base + (int64_t)row * p.C + col, row < p.R ? p.C - col : 0, x[half]);
+  }
   if (t < 64) {
-    double s = p.parts[g * kNormChunks + t];
+    double s = 0;
+    for (int i = t; i < p.chunks; i += 64) s += p.parts[g * kNormChunks + i];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
     if (t == 0) inv_s = s > 0 ? (double)p.cx / sqrt(s) : s == 0 ? 0.0 : s;  // NaN stays
   }
   __syncthreads();
   const double inv = inv_s;
-  // rows and columns of U, and of the padded matrix
-  const int rp = p.wide ? p.np : p.mp, cp = p.wide ? p.mp : p.np;
-  const int across = cp / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
-  const int64_t base = (int64_t)g * p.R * p.C;
   // direct: the order of U's rows; turned: the other one
   unsigned short* direct = p.wide ? p.X + g * p.sx : p.XT + g * p.sxt;
   unsigned short* turned = p.wide ? p.XT + g * p.sxt : p.X + g * p.sx;
   unsigned short* low = p.LO + g * p.sxt;  // in the order of X^T
   const int ldd = p.wide ? p.ldm : p.ldn, ldt = p.wide ? p.ldn : p.ldm;
-  const int r = t >> 2, c = (t & 3) * 16;
-  v8h h[2], l[2];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const bool in = r0 + r < p.R && c0 + c + e < p.C;
-    const float v =
-        in ? (float)((double)u_at(p, base + (int64_t)(r0 + r) * p.C + c0 + c + e) * inv) : 0.f;
-    const _Float16 top = (_Float16)v;
-    const _Float16 rest = (_Float16)((v - (float)top) * kLow);
-    h[e >> 3][e & 7] = top;
-    l[e >> 3][e & 7] = rest;
-    hi[c + e][r] = __builtin_bit_cast(unsigned short, top);
-    lo[c + e][r] = __builtin_bit_cast(unsigned short, rest);
-  }
-  const int64_t at = (int64_t)(r0 + r) * ldd + c0 + c;
-  *(v8h*)(direct + at) = h[0];
-  *(v8h*)(direct + at + 8) = h[1];
-  if (!p.wide) {
-    *(v8h*)(low + at) = l[0];
-    *(v8h*)(low + at + 8) = l[1];
+  for (int half = 0; half < 2; ++half) {
+    const int row = r + 32 * half;
+    v8h h, l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = (float)((double)x[half][e] * inv);
+      h[e] = (_Float16)v;
+      l[e] = (_Float16)((v - (float)h[e]) * kLow);
+    }
+    const int slot = row * 128 + 16 * (c ^ (row & 7));
+    *(v8h*)(lds[0] + slot) = h;
+    const int64_t at = (int64_t)(r0 + row) * ldd + c0 + 8 * c;
+    *(v8h*)(direct + at) = h;
+    if (p.wide) *(v8h*)(lds[1] + slot) = l;
+    else *(v8h*)(low + at) = l;
   }
   __syncthreads();
-  const int64_t to = (int64_t)(c0 + r) * ldt + r0 + c;
-  *(v4i*)(turned + to) = *(const v4i*)&hi[r][c];
-  *(v4i*)(turned + to + 8) = *(const v4i*)&hi[r][c + 8];
-  if (p.wide) {
-    *(v4i*)(low + to) = *(const v4i*)&lo[r][c];
-    *(v4i*)(low + to + 8) = *(const v4i*)&lo[r][c + 8];
+  // wave w turns 16 columns: lane c of 16 gets column c of 4 rows per read
+  const int w = t >> 6, lane = t & 63, jl = lane & 15, c4 = lane & 3;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (which == 1 && !p.wide) break;
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb) {
+      const int j = 32 * jb + 8 * (lane >> 4);
+      v4bf half[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int row = j + 4 * s + (jl >> 2);
+        half[s] = tr16(lds[which] + row * 128 + 16 * ((2 * w + (c4 >> 1)) ^ (row & 7)) + 8 * (c4 & 1));
+      }
+      const v2i a = __builtin_bit_cast(v2i, half[0]), b = __builtin_bit_cast(v2i, half[1]);
+      unsigned short* to = which == 0 ? turned : low;
+      *(v4i*)(to + (int64_t)(c0 + 16 * w + jl) * ldt + r0 + j) = v4i{a.x, a.y, b.x, b.y};
+    }
   }
 }
 
 // ------------------------------------------------------------------------------- products
 
-// BS x BS results per workgroup of 8 waves (4 along j, 2 along i), two LDS stages of 64 k (128
-// bytes) of BS rows of P and of Q. The loop is kg_fprop's: Q's fragments are read a block ahead, loads go
-// straight to LDS and are spread over the MFMAs, waits count them.
-template <int BS_, int PER_CU_>
+// BS x BS results per workgroup, LDS stages of 64 k (128 bytes) of BS rows of P and of Q. Loads go
+// straight to LDS, waits count them. With 8 waves (4 along j, 2 along i) and two stages the loop is
+// kg_fprop's: Q's fragments are read a block ahead, loads are spread over the MFMAs. With 4 waves, for
+// products of few tiles, what counts is how much is under way: three blocks, and what the end needs.
+template <int BS_, int PER_CU_, int WAVES_ = 8, int STAGES_ = 2>
 struct OCfg {
-  static constexpr int BS = BS_, PER_CU = PER_CU_, THREADS = 512, WT = 4, WN = 2, TK = 64;
+  static constexpr int BS = BS_, PER_CU = PER_CU_, WAVES = WAVES_, STAGES = STAGES_, TK = 64;
+  static constexpr int THREADS = 64 * WAVES, WT = WAVES / 2, WN = 2;
   static constexpr int TT = BS / WT / 16, NI = BS / WN / 16;
   static constexpr int OPW = BS * 128, STAGE = 2 * OPW;
-  static constexpr int LW = BS / 64, LOADS = 2 * LW;
-  static_assert(NI % 2 == 0 && TT * 16 * NI * 16 * 2 * 8 <= 2 * STAGE, "a wave's results fit in LDS");
+  static constexpr int LW = BS / (8 * WAVES), LOADS = 2 * LW;
+  static_assert(NI % 2 == 0 && BS * BS * 2 <= STAGES * STAGE, "a wave's results fit in LDS");
 };
 
 // (as in kg_fprop: row m of MFMA row tile i holds result row orow(i, m) of the wave's, so a
@@ -209,12 +247,13 @@ __device__ __forceinline__ void triangle(int idx, int T, int* I, int* J) {
 }
 
 template <class C, int MODE>
-__global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_ortho_kernel(OParams p) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho_kernel(OParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   constexpr int TT = C::TT, NI = C::NI;
   constexpr bool SYM = MODE == kGram || MODE == kPoly;
   const int total = p.G * p.per, grid = gridDim.x, b = blockIdx.x;
-  const int slot = (grid % 8 == 0 && total > grid) ? (b % 8) * (grid / 8) + b / 8 : b;
+  // neighbouring tiles on one XCD (workgroups go round the eight): its L2 holds what they share
+  const int slot = grid % 8 == 0 ? (b % 8) * (grid / 8) + b / 8 : b;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int q = lane >> 4, jl = lane & 15;
   const int wt = w % C::WT, wn = w / C::WT;
@@ -252,12 +291,13 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_ortho_kernel(OPa
     // rows that the matrix lacks and blocks past the last one read as zeros
     auto load_p = [&](int kb, int x) {
       load16_lds(make_rsrc(Pb + (int64_t)kb * 128, kb < nk ? pbytes : 0u),
-                 lds + (kb & 1) * C::STAGE + 1024 * (w + 8 * x), offp + (uint32_t)(64 * x * ld * 2));
+                 lds + kb % C::STAGES * C::STAGE + 1024 * (w + C::WAVES * x),
+                 offp + (uint32_t)(8 * C::WAVES * x * ld * 2));
     };
     auto load_q = [&](int kb, int x) {
       load16_lds(make_rsrc(Qb + (int64_t)kb * 128, kb < nk ? qbytes : 0u),
-                 lds + (kb & 1) * C::STAGE + C::OPW + 1024 * (w + 8 * x),
-                 offq + (uint32_t)(64 * x * ld * 2));
+                 lds + kb % C::STAGES * C::STAGE + C::OPW + 1024 * (w + C::WAVES * x),
+                 offq + (uint32_t)(8 * C::WAVES * x * ld * 2));
     };
     v4f acc[NI][TT];
 #pragma unroll
@@ -266,51 +306,111 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_ortho_kernel(OPa
       for (int tt = 0; tt < TT; ++tt) acc[i][tt] = v4f{0.f, 0.f, 0.f, 0.f};
     v8h qf[TT][2], pf[2][2];
     auto read_q = [&](int kb, int tt) {
-      const unsigned char* r = fragq + (kb & 1) * C::STAGE + 16 * tt * 128;
+      const unsigned char* r = fragq + kb % C::STAGES * C::STAGE + 16 * tt * 128;
       qf[tt][0] = *(const v8h*)(r + c0);
       qf[tt][1] = *(const v8h*)(r + c1);
     };
     auto read_p = [&](int kb, int i) {
-      const unsigned char* r = fragp + (kb & 1) * C::STAGE + orow(i, 0) * 128;
+      const unsigned char* r = fragp + kb % C::STAGES * C::STAGE + orow(i, 0) * 128;
       pf[i & 1][0] = *(const v8h*)(r + c0);
       pf[i & 1][1] = *(const v8h*)(r + c1);
     };
+    // what the end of a result needs, early where there are registers for it
+    const int iw = i0 + wn * NI * 16, jw = j0 + wt * TT * 16;
+    struct Ends {
+      v8h a, l;
+      float di[8], dj;
+    };
+    auto ends = [&](int tt, int i2) {
+      const int j = jw + 16 * tt + jl, i = iw + 32 * i2 + 8 * q;
+      const bool in = j < rows_j && i < p.np;
+      const int64_t at = (int64_t)j * p.ldn + i;
+      Ends e;
+      e.a = e.l = v8h{};
+      e.dj = 0.f;
+      if (in) {
+        if constexpr (MODE == kPoly) {
+          e.a = *(const v8h*)(p.A + g * p.sa + at);
+          e.dj = p.dA[g * p.np + j];
+        } else if constexpr (MODE != kGram) {
+          e.a = *(const v8h*)(p.XT + g * p.sxt + at);
+          if (p.low_in) e.l = *(const v8h*)(p.LO + g * p.sxt + at);
+        }
+      }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+      for (int x = 0; x < 8; ++x)
+        e.di[x] = MODE != kGram && in ? (MODE == kPoly ? p.dA : p.dB)[g * p.np + i + x] : 0.f;
+      return e;
+    };
+    constexpr bool EARLY = C::STAGES > 2;
+    Ends early[EARLY ? TT : 1][EARLY ? NI / 2 : 1];
+    if constexpr (EARLY) {
 #pragma unroll
-      for (int x = 0; x < C::LW; ++x) load_q(kb, x);
+      for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-      for (int x = 0; x < C::LW; ++x) load_p(kb, x);
-    }
-    o_meet<C::LOADS>();
+        for (int i2 = 0; i2 < NI / 2; ++i2) early[tt][i2] = ends(tt, i2);
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt) read_q(0, tt);
-    o_meet<C::LOADS>();
-    for (int kb = 0; kb < nk; ++kb) {
-      constexpr int S = NI * 2 * TT, LASTI = S - 2 * TT;  // MFMAs of a block, and before the last i
-      read_p(kb, 0);
-#pragma unroll
-      for (int u = 0; u < S; ++u) {
-        const int i = u / (2 * TT), h = u / TT % 2, tt = u % TT;
-        // Q's next block is there, P's block has been read by every wave
-        if (u == LASTI) o_meet<C::LOADS>();
-        if (h == 0 && tt == 0 && i + 1 < NI) read_p(kb, i + 1);
-        acc[i][tt] = mfma_f16(pf[i & 1][h], qf[tt][h], acc[i][tt]);
-        if (i == NI - 1 && h == 1) read_q(kb + 1, tt);  // (past the last block: not used)
+      for (int kb = 0; kb < C::STAGES - 1; ++kb)
 #pragma unroll
         for (int x = 0; x < C::LW; ++x) {
-          if (x * LASTI / C::LW == u) load_q(kb + 2, x);
-          if (LASTI + x * 2 * TT / C::LW == u) load_p(kb + 2, x);
+          load_q(kb, x);
+          load_p(kb, x);
         }
-        __builtin_amdgcn_sched_barrier(0);
+      for (int kb = 0; kb < nk; ++kb) {
+        // block kb is there, block kb - 1 has been read by every wave
+        o_meet<(C::STAGES - 2) * C::LOADS>();
+#pragma unroll
+        for (int x = 0; x < C::LW; ++x) {
+          load_q(kb + C::STAGES - 1, x);
+          load_p(kb + C::STAGES - 1, x);
+        }
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) read_q(kb, tt);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          read_p(kb, i);
+#pragma unroll
+          for (int u = 0; u < 2 * TT; ++u)
+            acc[i][u % TT] = mfma_f16(pf[i & 1][u / TT], qf[u % TT][u / TT], acc[i][u % TT]);
+        }
       }
-      // P's next block is there, Q's has been read by every wave
+    } else {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int x = 0; x < C::LW; ++x) load_q(kb, x);
+#pragma unroll
+        for (int x = 0; x < C::LW; ++x) load_p(kb, x);
+      }
       o_meet<C::LOADS>();
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) read_q(0, tt);
+      o_meet<C::LOADS>();
+      for (int kb = 0; kb < nk; ++kb) {
+        constexpr int S = NI * 2 * TT, LASTI = S - 2 * TT;  // MFMAs of a block, and before the last i
+        read_p(kb, 0);
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+          const int i = u / (2 * TT), h = u / TT % 2, tt = u % TT;
+          // Q's next block is there, P's block has been read by every wave
+          if (u == LASTI) o_meet<C::LOADS>();
+          if (h == 0 && tt == 0 && i + 1 < NI) read_p(kb, i + 1);
+          acc[i][tt] = mfma_f16(pf[i & 1][h], qf[tt][h], acc[i][tt]);
+          if (i == NI - 1 && h == 1) read_q(kb + 1, tt);  // (past the last block: not used)
+#pragma unroll
+          for (int x = 0; x < C::LW; ++x) {
+            if (x * LASTI / C::LW == u) load_q(kb + 2, x);
+            if (LASTI + x * 2 * TT / C::LW == u) load_p(kb + 2, x);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        // P's next block is there, Q's has been read by every wave
+        o_meet<C::LOADS>();
+      }
     }
     // No load is under way into the LDS that turns the results.
     o_meet<0>();
     unsigned char* turn = smem + w * (TT * 16 * NI * 16 * 2);  // [j][i] of this wave
-    const int iw = i0 + wn * NI * 16, jw = j0 + wt * TT * 16;
     const bool mirror = !SYM || I != J;
     unsigned short* out = MODE == kGram   ? p.A + g * p.sa
                           : MODE == kPoly ? p.B + g * p.sa
@@ -335,34 +435,20 @@ __global__ __launch_bounds__(C::THREADS, 2 * C::PER_CU) void kg_ortho_kernel(OPa
             o[e] = (_Float16)v[e];
           }
         } else if constexpr (MODE == kPoly) {
-          v8h a = {};
-          float di[8], dj = 0.f;
-          if (in) {
-            a = *(const v8h*)(p.A + g * p.sa + at);
-            dj = p.dA[g * p.np + j];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) di[e] = in ? p.dA[g * p.np + i + e] : 0.f;
+          const Ends end = EARLY ? early[EARLY ? tt : 0][EARLY ? i2 : 0] : ends(tt, i2);
           constexpr float fb = kScaleB / kScaleA * kNsB, fc = kScaleB / (kScaleA * kScaleA) * kNsC;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float x = (float)a[e];
-            v[e] = fmaf(fc, fmaf(di[e] + dj, x, v[e]), fb * (i + e == j ? x + dj : x));
+            const float x = (float)end.a[e];
+            v[e] = fmaf(fc, fmaf(end.di[e] + end.dj, x, v[e]), fb * (i + e == j ? x + end.dj : x));
             o[e] = (_Float16)v[e];
           }
         } else {
-          v8h x = {}, l = {};
-          float di[8];
-          if (in) {
-            x = *(const v8h*)(p.XT + g * p.sxt + at);
-            if (p.low_in) l = *(const v8h*)(p.LO + g * p.sxt + at);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) di[e] = in ? p.dB[g * p.np + i + e] : 0.f;
+          const Ends end = EARLY ? early[EARLY ? tt : 0][EARLY ? i2 : 0] : ends(tt, i2);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float st = fmaf((float)l[e], 1 / kLow, (float)x[e]);
-            v[e] = fmaf(kNsA + di[e] / kScaleB, st, v[e] / kScaleB);
+            const float st = fmaf((float)end.l[e], 1 / kLow, (float)end.a[e]);
+            v[e] = fmaf(kNsA + end.di[e] / kScaleB, st, v[e] / kScaleB);
             if constexpr (MODE == kStep) o[e] = (_Float16)v[e];
             else o[e] = __builtin_bit_cast(_Float16, (__bf16)(v[e] / p.cx));
           }
@@ -489,7 +575,7 @@ static bool o_taken(int G, int R, int C) {
 
 template <class C, int MODE>
 static int o_launch(OParams& p, int cus, int dev, void* stream) {
-  constexpr int LDS = 2 * C::STAGE;
+  constexpr int LDS = C::STAGES * C::STAGE;
   static std::mutex mu;
   static bool set[64];
   {
@@ -506,18 +592,31 @@ static int o_launch(OParams& p, int cus, int dev, void* stream) {
   const int64_t per = SYM ? (int64_t)p.tiles_i * (p.tiles_i + 1) / 2 : (int64_t)p.tiles_i * p.tiles_j;
   if (per * p.G > INT32_MAX - 4096) return KG_ERR_UNSUPPORTED;
   p.per = (int)per;
-  const int64_t most = (int64_t)cus * C::PER_CU;
-  return launch(kg_ortho_kernel<C, MODE>, per * p.G < most ? per * p.G : most, C::THREADS, LDS,
+  const int64_t most = (int64_t)cus * C::PER_CU, all = (per * p.G + 7) / 8 * 8;
+  return launch(kg_ortho_kernel<C, MODE>, all < most ? all : most, C::THREADS, LDS,
                 stream, p);
 }
 
-// Tiles of 256 where they give every compute unit one, else of 128.
+// A product's tiles, by the rounds that each size takes (256: one workgroup on a compute unit, 128:
+// two, 64: three; 128's rounds in halves, as a workgroup alone on its compute unit is faster).
+// Measured in us, 256 / 128 / 64, for n, m, matrices:
+//   A    832, 1024, 3     28 / 12 / 10        B X   832, 1024, 3     45 / 17 / 16
+//        2048, 2048, 1    47 / 19 / 24              256, 1024, 32    37 / 23 / 27
+//        4096, 4096, 1    94 / 91 / 126             1536, 2048, 4    65 / 73 / 77
+//        2048, 7168, 8   332 / 329 / -              2048, 7168, 8   624 / 748 / -
+//        4096, 7168, 8   874 / 1060 / -             4096, 7168, 8  1884 / 2750 / -
 template <int MODE>
 static int o_product(OParams& p, int cus, int dev, void* stream) {
   constexpr bool SYM = MODE == kGram || MODE == kPoly;
-  const int64_t ti = (p.np + 255) / 256, tj = (p.mp + 255) / 256;
-  if (p.G * (SYM ? ti * (ti + 1) / 2 : ti * tj) >= cus / 2)
-    return o_launch<OCfg<256, 1>, MODE>(p, cus, dev, stream);
+  auto tiles = [&](int bs) {
+    const int64_t ti = (p.np + bs - 1) / bs, tj = (p.mp + bs - 1) / bs;
+    return p.G * (SYM ? ti * (ti + 1) / 2 : ti * tj);
+  };
+  const int blocks = (MODE == kGram ? p.mp : p.np) / 64;
+  if (tiles(64) <= (blocks <= 16 ? 3 : 2) * cus)
+    return o_launch<OCfg<64, 3, 4, 3>, MODE>(p, cus, dev, stream);
+  const int64_t r256 = (tiles(256) + cus - 1) / cus, halves = (tiles(128) + cus - 1) / cus;
+  if (31 * r256 <= 10 * halves) return o_launch<OCfg<256, 1>, MODE>(p, cus, dev, stream);
   return o_launch<OCfg<128, 2>, MODE>(p, cus, dev, stream);
 }
 
@@ -564,7 +663,9 @@ extern "C" int kg_orthogonalize(const void* U, void* O, int G, int R, int C, int
   p.ldn = s.ldn, p.ldm = s.ldm;
   p.b16 = type == KG_ROWS_BF16, p.wide = R <= C;
   p.XT = (unsigned short*)(ws + s.xt[0]), p.XN = (unsigned short*)(ws + s.xt[1]);
-  int rc = launch2(kg_ortho_norm_kernel, kNormChunks, G, 256, 0, stream, p);
+  const int64_t chunk = norm_chunk((int64_t)R * C);
+  p.chunks = (int)(((int64_t)R * C + chunk - 1) / chunk);
+  int rc = launch2(kg_ortho_norm_kernel, p.chunks, G, 256, 0, stream, p);
   if (rc == KG_OK)
     rc = launch2(kg_ortho_init_kernel, (int64_t)(s.np / 64) * (s.mp / 64), G, 256, 0, stream, p);
   for (int t = 0; t < steps && rc == KG_OK; ++t) {
