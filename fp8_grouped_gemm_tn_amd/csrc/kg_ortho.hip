@@ -24,6 +24,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "kg_device.h"
@@ -51,6 +52,7 @@ struct OParams {
   int b16, wide, tiles_i, tiles_j, per;  // per: tiles of a matrix
   int low_in, low_out;
   int chunks;
+  int first, count, quarter;  // tiles of this launch; whether each is a quarter of one twice as large
 };
 
 // Eight neighbours of U, of which the first `n` are there; the rest are zeros.
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   constexpr int TT = C::TT, NI = C::NI;
   constexpr bool SYM = MODE == kGram || MODE == kPoly;
-  const int total = p.G * p.per, grid = gridDim.x, b = blockIdx.x;
+  const int total = p.count, grid = gridDim.x, b = blockIdx.x;
   // neighbouring tiles on one XCD (workgroups go round the eight): its L2 holds what they share
   const int slot = grid % 8 == 0 ? (b % 8) * (grid / 8) + b / 8 : b;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
@@ -268,8 +270,8 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
   const uint32_t offp = (uint32_t)(lr * ld * 2 + 16 * ((lane & 7) ^ okey_p(lr)));
   const uint32_t offq = (uint32_t)(lr * ld * 2 + 16 * ((lane & 7) ^ okey_q(lr)));
   for (int base = 0; base < total; base += grid) {
-    const int idx = base + slot;
-    if (idx >= total) break;
+    if (base + slot >= total) break;
+    const int idx = p.first + (p.quarter ? (base + slot) >> 2 : base + slot);
     const int g = idx / p.per;
     int I, J;
     if constexpr (SYM) {
@@ -278,6 +280,10 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
       const int r = idx - g * p.per, per_panel = 4 * p.tiles_j, panel = r / per_panel;
       const int wi = r - panel * per_panel, pm = min(4, p.tiles_i - 4 * panel);
       I = 4 * panel + wi % pm, J = wi / pm;
+    }
+    if (p.quarter) {
+      I = 2 * I + ((base + slot) >> 1 & 1), J = 2 * J + ((base + slot) & 1);
+      if ((SYM && I < J) || I * C::BS >= p.np || J * C::BS >= rows_j) continue;
     }
     const int i0 = uniform(I) * C::BS, j0 = uniform(J) * C::BS;
     const unsigned short* P = MODE == kGram   ? p.X + g * p.sx
@@ -586,14 +592,8 @@ static int o_launch(OParams& p, int cus, int dev, void* stream) {
       return KG_ERR_HIP;
     set[dev] = true;
   }
-  constexpr bool SYM = MODE == kGram || MODE == kPoly;
-  p.tiles_i = (p.np + C::BS - 1) / C::BS;
-  p.tiles_j = SYM ? p.tiles_i : (p.mp + C::BS - 1) / C::BS;
-  const int64_t per = SYM ? (int64_t)p.tiles_i * (p.tiles_i + 1) / 2 : (int64_t)p.tiles_i * p.tiles_j;
-  if (per * p.G > INT32_MAX - 4096) return KG_ERR_UNSUPPORTED;
-  p.per = (int)per;
-  const int64_t most = (int64_t)cus * C::PER_CU, all = (per * p.G + 7) / 8 * 8;
-  return launch(kg_ortho_kernel<C, MODE>, all < most ? all : most, C::THREADS, LDS,
+  return launch(kg_ortho_kernel<C, MODE>,
+                std::min<int64_t>((p.count + 7) / 8 * 8, (int64_t)cus * C::PER_CU), C::THREADS, LDS,
                 stream, p);
 }
 
@@ -605,18 +605,36 @@ static int o_launch(OParams& p, int cus, int dev, void* stream) {
 //        4096, 4096, 1    94 / 91 / 126             1536, 2048, 4    65 / 73 / 77
 //        2048, 7168, 8   332 / 329 / -              2048, 7168, 8   624 / 748 / -
 //        4096, 7168, 8   874 / 1060 / -             4096, 7168, 8  1884 / 2750 / -
+// Where 256's last round is less than half full, its tiles are quartered instead: 4096, 7168, 8
+// has 4 rounds and 64 tiles (A 884 -> 790 us, A A 578 -> 517).
 template <int MODE>
 static int o_product(OParams& p, int cus, int dev, void* stream) {
   constexpr bool SYM = MODE == kGram || MODE == kPoly;
   auto tiles = [&](int bs) {
-    const int64_t ti = (p.np + bs - 1) / bs, tj = (p.mp + bs - 1) / bs;
-    return p.G * (SYM ? ti * (ti + 1) / 2 : ti * tj);
+    p.tiles_i = (p.np + bs - 1) / bs, p.tiles_j = SYM ? p.tiles_i : (p.mp + bs - 1) / bs;
+    const int64_t per = SYM ? (int64_t)p.tiles_i * (p.tiles_i + 1) / 2 : (int64_t)p.tiles_i * p.tiles_j;
+    p.per = (int)per, p.count = (int)(per * p.G);
+    return per * p.G;
   };
+  p.first = p.quarter = 0;
+  const int64_t n64 = tiles(64), n128 = tiles(128);
+  if (n128 > INT32_MAX / 4 - 4096) return KG_ERR_UNSUPPORTED;
   const int blocks = (MODE == kGram ? p.mp : p.np) / 64;
-  if (tiles(64) <= (blocks <= 16 ? 3 : 2) * cus)
+  if (n64 <= (blocks <= 16 ? 3 : 2) * cus) {
+    tiles(64);
     return o_launch<OCfg<64, 3, 4, 3>, MODE>(p, cus, dev, stream);
-  const int64_t r256 = (tiles(256) + cus - 1) / cus, halves = (tiles(128) + cus - 1) / cus;
-  if (31 * r256 <= 10 * halves) return o_launch<OCfg<256, 1>, MODE>(p, cus, dev, stream);
+  }
+  const int64_t n256 = tiles(256), rest = n256 % cus, halves = (n128 + cus - 1) / cus;
+  if (n256 >= cus && rest > 0 && rest <= cus / 2) {
+    p.count = (int)(n256 - rest);
+    const int rc = o_launch<OCfg<256, 1>, MODE>(p, cus, dev, stream);
+    if (rc != KG_OK) return rc;
+    p.first = p.count, p.count = (int)(4 * rest), p.quarter = 1;
+    return o_launch<OCfg<128, 2>, MODE>(p, cus, dev, stream);
+  }
+  if (31 * ((n256 + cus - 1) / cus) <= 10 * halves)
+    return o_launch<OCfg<256, 1>, MODE>(p, cus, dev, stream);
+  tiles(128);
   return o_launch<OCfg<128, 2>, MODE>(p, cus, dev, stream);
 }
 
