@@ -321,40 +321,39 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
       pf[i & 1][0] = *(const v8h*)(r + c0);
       pf[i & 1][1] = *(const v8h*)(r + c1);
     };
-    // what the end of a result needs, early where there are registers for it
+    // What the ends of results need: before the products where there are registers for it, else
+    // each column tile's before the one before it is stored (a wait for loads is one for all
+    // stores that went before them).
     const int iw = i0 + wn * NI * 16, jw = j0 + wt * TT * 16;
-    struct Ends {
-      v8h a, l;
-      float di[8], dj;
-    };
-    auto ends = [&](int tt, int i2) {
-      const int j = jw + 16 * tt + jl, i = iw + 32 * i2 + 8 * q;
-      const bool in = j < rows_j && i < p.np;
-      const int64_t at = (int64_t)j * p.ldn + i;
-      Ends e;
-      e.a = e.l = v8h{};
-      e.dj = 0.f;
-      if (in) {
+    constexpr bool EARLY = C::STAGES > 2;
+    static_assert(!EARLY || TT == 2);
+    v8h ea[2][NI / 2], el[2][NI / 2];  // A or X; low halves
+    float dj[2];
+    auto fetch = [&](int tt) {
+      const int j = jw + 16 * tt + jl;
+#pragma unroll
+      for (int i2 = 0; i2 < NI / 2; ++i2) {
+        const int i = iw + 32 * i2 + 8 * q;
+        const bool in = j < rows_j && i < p.np;
+        const int64_t at = (int64_t)j * p.ldn + i;
+        ea[tt & 1][i2] = el[tt & 1][i2] = v8h{};
         if constexpr (MODE == kPoly) {
-          e.a = *(const v8h*)(p.A + g * p.sa + at);
-          e.dj = p.dA[g * p.np + j];
+          if (in) ea[tt & 1][i2] = *(const v8h*)(p.A + g * p.sa + at);
         } else if constexpr (MODE != kGram) {
-          e.a = *(const v8h*)(p.XT + g * p.sxt + at);
-          if (p.low_in) e.l = *(const v8h*)(p.LO + g * p.sxt + at);
+          if (in) ea[tt & 1][i2] = *(const v8h*)(p.XT + g * p.sxt + at);
+          if (in && p.low_in) el[tt & 1][i2] = *(const v8h*)(p.LO + g * p.sxt + at);
         }
       }
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        e.di[x] = MODE != kGram && in ? (MODE == kPoly ? p.dA : p.dB)[g * p.np + i + x] : 0.f;
-      return e;
+      if constexpr (MODE == kPoly) dj[tt & 1] = j < p.np ? p.dA[g * p.np + j] : 0.f;
     };
-    constexpr bool EARLY = C::STAGES > 2;
-    Ends early[EARLY ? TT : 1][EARLY ? NI / 2 : 1];
+    // the diagonals' roundings of the tile's rows i, to LDS behind the stages
+    float* dis = (float*)(smem + C::STAGES * C::STAGE);
+    float di_mine = 0.f;
+    if (MODE != kGram && (int)threadIdx.x < C::BS && i0 + (int)threadIdx.x < p.np)
+      di_mine = (MODE == kPoly ? p.dA : p.dB)[g * p.np + i0 + threadIdx.x];
     if constexpr (EARLY) {
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-        for (int i2 = 0; i2 < NI / 2; ++i2) early[tt][i2] = ends(tt, i2);
+      for (int tt = 0; tt < TT; ++tt) fetch(tt);
 #pragma unroll
       for (int kb = 0; kb < C::STAGES - 1; ++kb)
 #pragma unroll
@@ -414,8 +413,10 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
         o_meet<C::LOADS>();
       }
     }
+    if (MODE != kGram && threadIdx.x < C::BS) dis[threadIdx.x] = di_mine;
     // No load is under way into the LDS that turns the results.
     o_meet<0>();
+    if constexpr (!EARLY) fetch(0);
     unsigned char* turn = smem + w * (TT * 16 * NI * 16 * 2);  // [j][i] of this wave
     const bool mirror = !SYM || I != J;
     unsigned short* out = MODE == kGram   ? p.A + g * p.sa
@@ -424,6 +425,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
       const int j = jw + 16 * tt + jl;
+      if (!EARLY && tt + 1 < TT) fetch(tt + 1);
 #pragma unroll
       for (int i2 = 0; i2 < NI / 2; ++i2) {
         const int i = iw + 32 * i2 + 8 * q;
@@ -441,20 +443,22 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
             o[e] = (_Float16)v[e];
           }
         } else if constexpr (MODE == kPoly) {
-          const Ends end = EARLY ? early[EARLY ? tt : 0][EARLY ? i2 : 0] : ends(tt, i2);
+          const v8h a = ea[tt & 1][i2];
+          const float* di = dis + (i - i0);
           constexpr float fb = kScaleB / kScaleA * kNsB, fc = kScaleB / (kScaleA * kScaleA) * kNsC;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float x = (float)end.a[e];
-            v[e] = fmaf(fc, fmaf(end.di[e] + end.dj, x, v[e]), fb * (i + e == j ? x + end.dj : x));
+            const float x = (float)a[e], d = dj[tt & 1];
+            v[e] = fmaf(fc, fmaf(di[e] + d, x, v[e]), fb * (i + e == j ? x + d : x));
             o[e] = (_Float16)v[e];
           }
         } else {
-          const Ends end = EARLY ? early[EARLY ? tt : 0][EARLY ? i2 : 0] : ends(tt, i2);
+          const v8h a = ea[tt & 1][i2], l = el[tt & 1][i2];
+          const float* di = dis + (i - i0);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float st = fmaf((float)end.l[e], 1 / kLow, (float)end.a[e]);
-            v[e] = fmaf(kNsA + end.di[e] / kScaleB, st, v[e] / kScaleB);
+            const float st = fmaf((float)l[e], 1 / kLow, (float)a[e]);
+            v[e] = fmaf(kNsA + di[e] / kScaleB, st, v[e] / kScaleB);
             if constexpr (MODE == kStep) o[e] = (_Float16)v[e];
             else o[e] = __builtin_bit_cast(_Float16, (__bf16)(v[e] / p.cx));
           }
@@ -581,7 +585,7 @@ static bool o_taken(int G, int R, int C) {
 
 template <class C, int MODE>
 static int o_launch(OParams& p, int cus, int dev, void* stream) {
-  constexpr int LDS = C::STAGES * C::STAGE;
+  constexpr int LDS = C::STAGES * C::STAGE + C::BS * 4;
   static std::mutex mu;
   static bool set[64];
   {
