@@ -283,7 +283,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
     }
     if (p.quarter) {
       I = 2 * I + ((base + slot) >> 1 & 1), J = 2 * J + ((base + slot) & 1);
-      if ((SYM && I < J) || I * C::BS >= p.np || J * C::BS >= rows_j) continue;
+      if ((SYM && I > J) || I * C::BS >= p.np || J * C::BS >= rows_j) continue;
     }
     const int i0 = uniform(I) * C::BS, j0 = uniform(J) * C::BS;
     const unsigned short* P = MODE == kGram   ? p.X + g * p.sx

@@ -96,6 +96,22 @@ def test_large_tiles(G, R, C):
         near(o[g], (x.t() if R > C else x).cpu())
 
 
+@pytest.mark.parametrize("G,R,C", [(30, 800, 1000), (26, 1000, 800), (17, 800, 1100), (17, 1100, 800), (101, 500, 700)])
+def test_last_rounds(G, R, C):
+    """Numbers of tiles a little above a multiple of the compute units, whose last ones are done as smaller
+    ones; every matrix."""
+    gen = torch.Generator("cuda").manual_seed(G)
+    us = torch.randn((G, R, C), generator=gen, device="cuda").to(torch.bfloat16)
+    o = kg.kg_orthogonalize(us)
+    for g in range(G):
+        x = us[g].double()
+        x = x / x.norm()
+        x = x.t() if R > C else x
+        for _ in range(5):
+            a = x @ x.t()
+            x = NS_A * x + (NS_B * a + NS_C * (a @ a)) @ x
+        near(o[g], (x.t() if R > C else x).cpu())
+
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 def test_steps(steps):
