@@ -55,36 +55,45 @@ struct OParams {
   int first, count, quarter;  // tiles of this launch; whether each is a quarter of one twice as large
 };
 
-// Eight neighbours of U, of which the first `n` are there; the rest are zeros.
-__device__ __forceinline__ void u_eight(const OParams& p, int64_t at, int n, float* x) {
-  typedef unsigned short h8 __attribute__((ext_vector_type(8), aligned(2)));
-  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
-  if (p.b16) {
-    const unsigned short* u = (const unsigned short*)p.U + at;
-    h8 h = {};
-    if (n >= 8) {
-      h = *(const h8*)u;
+// Eight neighbours of U from element `at`, of which the first `n` count; the rest are zeros. Loaded as they lie
+// (also what follows, up to U's end), so that several loads are under way before the first is used.
+struct Eight {
+  v4i a, b;
+};
+__device__ __forceinline__ Eight u_load(const OParams& p, int64_t at, int n) {
+  typedef int v4i_any __attribute__((ext_vector_type(4), aligned(2)));
+  Eight x = {};
+  if (n > 0) {
+    if (at + 8 <= (int64_t)p.G * p.R * p.C) {
+      const char* u = (const char*)p.U + at * (p.b16 ? 2 : 4);
+      x.a = *(const v4i_any*)u;
+      if (!p.b16) x.b = *(const v4i_any*)(u + 16);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) h[e] = u[e];
+      for (int e = 0; e < 8; ++e) {
+        if (e >= n) continue;
+        if (p.b16) x.a[e >> 1] |= (int)((const unsigned short*)p.U)[at + e] << (16 * (e & 1));
+        else (e < 4 ? x.a : x.b)[e & 3] = ((const int*)p.U)[at + e];
+      }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_bit_cast(float, (uint32_t)h[e] << 16);
-  } else {
-    const float* u = (const float*)p.U + at;
-    f4 f[2] = {};
-    if (n >= 8) {
-      f[0] = *(const f4*)u;
-      f[1] = *(const f4*)(u + 4);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) f[e >> 2][e & 3] = u[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = f[e >> 2][e & 3];
   }
+  return x;
+}
+__device__ __forceinline__ void u_values(const OParams& p, const Eight& u, int n, float* x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int two = u.a[e >> 1], one = (e < 4 ? u.a : u.b)[e & 3];
+    const int bits = !p.b16 ? one : e & 1 ? two & (int)0xFFFF0000 : two << 16;
+    x[e] = e < n ? __builtin_bit_cast(float, bits) : 0.f;
+  }
+}
+
+// x times inv, rounded to fp32. (Left alone, the compiler rounds 64 bits straight to fp16 behind it, in
+// some 25 instructions: the card has no such conversion.)
+__device__ __forceinline__ float scaled(float x, double inv) {
+  float v = (float)((double)x * inv);
+  asm("" : "+v"(v));
+  return v;
 }
 
 // ---------------------------------------------------------------------------- norm, first X
@@ -103,8 +112,9 @@ __global__ __launch_bounds__(256) void kg_ortho_norm_kernel(OParams p) {
   double s = 0;
 #pragma unroll 4
   for (int64_t i = from + 8 * threadIdx.x; i < to; i += kNormStep) {
+    const int n = to - i < 8 ? (int)(to - i) : 8;
     float x[8];
-    u_eight(p, base + i, to - i < 8 ? (int)(to - i) : 8, x);
+    u_values(p, u_load(p, base + i, n), n, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = fma((double)x[e], (double)x[e], s);
   }
@@ -128,11 +138,13 @@ __global__ __launch_bounds__(256) void kg_ortho_init_kernel(OParams p) {
   const int across = cp / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
   const int64_t base = (int64_t)g * p.R * p.C;
   const int r = t >> 3, c = t & 7;
-  float x[2][8];
+  Eight raw[2];
+  int left[2];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int row = r0 + r + 32 * half, col = c0 + 8 * c;
-    u_eight(p, base + (int64_t)row * p.C + col, row < p.R ? p.C - col : 0, x[half]);
+    left[half] = row < p.R ? p.C - col : 0;
+    raw[half] = u_load(p, base + (int64_t)row * p.C + col, left[half]);
   }
   if (t < 64) {
     double s = 0;
@@ -151,10 +163,12 @@ __global__ __launch_bounds__(256) void kg_ortho_init_kernel(OParams p) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int row = r + 32 * half;
+    float x[8];
+    u_values(p, raw[half], left[half], x);
     v8h h, l;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float v = (float)((double)x[half][e] * inv);
+      const float v = scaled(x[e], inv);
       h[e] = (_Float16)v;
       l[e] = (_Float16)((v - (float)h[e]) * kLow);
     }
@@ -545,6 +559,322 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES / 4 * C::PER_CU) void kg_ortho
   }
 }
 
+// ---------------------------------------------------------------------- small matrices
+
+// A matrix with a short axis of up to 128 whose X fits in LDS, from U to O in one workgroup: the 17
+// launches of the other way take 3 to 5 us each however small their matrices are. X [NP][mp] lies in
+// LDS as fp16, A and then B [NP][NP] beside it. A wave owns every eighth tile of 16 columns of X, whose
+// state stays in its registers in fp32; X's other order is read by the transposing reads. A and
+// A A: wave w % NI has the tiles (i, i + d), d = 0 .. NI / 2, round the end, so each pair of
+// rows meets once (twice at d = NI / 2); with NI < 8 the waves share m and add up in LDS, in order.
+// In us, here and by launches: 4 of 24 x 24 13 and 56, 8 of 64 x 256 25 and 63, 8 of 32 x 2048 54
+// and 99, 8 of 128 x 384 65 and 72, 300 of 100 x 380 135 and 495. What bounds it: of 65, the norm takes 4,
+// U's two ways into LDS 16, a step 8, half of it B X, which reads B anew for every column tile.
+
+// Column tiles of a wave: 128 registers of state (n > 64, where the sums take twice as many, 96)
+template <int NI>
+constexpr int kSmallTiles = NI == 8 ? 3 : 32 / NI;
+struct SmallLds {
+  int a, da, db, parts, total;  // byte offsets
+};
+__host__ __device__ constexpr SmallLds small_lds(int ni, int mp) {
+  SmallLds s{};
+  const int np = 16 * ni, lda = np < 64 ? 64 : np;
+  s.a = np * mp * 2;
+  s.da = s.a + np * lda * 2;
+  s.db = s.da + np * 4;
+  s.parts = s.db + np * 4;
+  s.total = s.parts + (ni < 8 ? (8 - ni) * (ni / 2 + 1) * 1024 : 64);  // (and the norm's sums before)
+  return s;
+}
+
+template <int NI>
+__global__ __launch_bounds__(512, 2) void kg_ortho_small_kernel(OParams p, int steps) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int NP = 16 * NI, LDA = NP < 64 ? 64 : NP, TJ = kSmallTiles<NI>, D = NI / 2 + 1;
+  constexpr int GROUPS = 8 / NI, PAIR = NI == 2 ? 2 : 1;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  const int q = lane >> 4, jl = lane & 15, mp = p.mp, g = blockIdx.x;
+  const SmallLds at = small_lds(NI, mp);
+  unsigned char *X = smem, *A = smem + at.a;
+  float *dA = (float*)(smem + at.da), *dB = (float*)(smem + at.db);
+  const int64_t base = (int64_t)g * p.R * p.C;
+  // f(row, c, values) for U's units of eight elements 8 c .. of a row, four of them under way
+  const int units_row = (p.C + 7) / 8, units = p.R * units_row;
+  const int row0 = threadIdx.x / units_row, c0 = threadIdx.x - row0 * units_row;
+  const int rows_on = 512 / units_row, on = 512 - rows_on * units_row;  // the next unit of a thread
+  auto each = [&](auto f) {
+    int row = row0, c = c0;
+    for (int u = threadIdx.x; u < units; u += 4 * 512) {
+      Eight raw[4];
+      int rows[4], cs[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        rows[s] = row, cs[s] = c;
+        raw[s] = u_load(p, base + (int64_t)row * p.C + 8 * c, row < p.R ? p.C - 8 * c : 0);
+        row += rows_on, c += on;
+        if (c >= units_row) c -= units_row, ++row;
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        float x[8];
+        u_values(p, raw[s], p.C - 8 * cs[s], x);
+        if (rows[s] < p.R) f(rows[s], cs[s], x);
+      }
+    }
+  };
+  double sum = 0;
+  each([&](int, int, const float* x) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fma((double)x[e], (double)x[e], sum);
+  });
+  for (int c = threadIdx.x; c < NP * mp / 8; c += 512) *(v4i*)(X + 16 * c) = v4i{0, 0, 0, 0};
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+  double* sums = (double*)(smem + at.parts);
+  if (lane == 0) sums[w] = sum;
+  __syncthreads();
+  sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += sums[i];
+  const double inv = sum > 0 ? (double)p.cx / sqrt(sum) : sum == 0 ? 0.0 : sum;  // NaN stays
+  // X [16 it + jl][16 (w + 8 t) + 4 q + r] is st[t][it][r], its fp16 value in LDS: 16-byte chunk c of
+  // a row in slot c ^ (row & 7)
+  v4f st[TJ][NI];
+  typedef unsigned short v4u16 __attribute__((ext_vector_type(4)));
+  auto place = [&](int t, int it) {
+    return (v4u16*)(X + (16 * it + jl) * mp * 2 +
+                    16 * ((2 * (w + 8 * t) + (q >> 1)) ^ (jl & 7)) + 8 * (q & 1));
+  };
+  auto put = [&](int t) {
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+      v4u16 o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = __builtin_bit_cast(unsigned short, (_Float16)st[t][it][r]);
+      *place(t, it) = o;
+    }
+  };
+  // U over its norm comes into the registers through X's place: first what its fp16 values lack, then
+  // those, which stay there
+  v4u16 low[TJ][NI];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    each([&](int row, int c, const float* x) {
+      v8h h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = scaled(x[e], inv);
+        h[e] = (_Float16)v;
+        if (half == 0) h[e] = (_Float16)((v - (float)h[e]) * kLow);
+      }
+      if (p.wide) {
+        *(v8h*)(X + row * mp * 2 + 16 * (c ^ (row & 7))) = h;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // (NP is a multiple of 8)
+          *(_Float16*)(X + (8 * c + e) * mp * 2 + 16 * ((row >> 3) ^ e) + 2 * (row & 7)) = h[e];
+      }
+    });
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TJ; ++t)
+#pragma unroll
+      for (int it = 0; it < NI; ++it) {
+        v4u16 o = {};
+        if (16 * (w + 8 * t) < mp) o = *place(t, it);
+        if (half == 0) {
+          low[t][it] = o;
+          continue;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const unsigned short hi = o[r], lo = low[t][it][r];
+          st[t][it][r] = fmaf((float)__builtin_bit_cast(_Float16, lo), 1 / kLow,
+                              (float)__builtin_bit_cast(_Float16, hi));
+        }
+      }
+    if (half == 0) __syncthreads();
+  }
+  auto x_row = [&](int i, int kb) {
+    return *(const v8h*)(X + (16 * i + jl) * mp * 2 + 16 * ((4 * kb + q) ^ (jl & 7)));
+  };
+  auto a_row = [&](int i, int kb) {
+    return *(const v8h*)(A + (16 * i + jl) * LDA * 2 + 16 * ((4 * kb + q) ^ (jl & 7)));
+  };
+  // a tile of A or B, [16 i + jl][16 j + 4 q + r], in both orders where no other wave has it
+  const int i = w % NI, grp = w / NI;
+  auto put_a = [&](int d, const v4f& v) {
+    typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+    const int j = (i + d) % NI;
+    v4h o;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = (_Float16)v[r];
+    *(v4h*)(A + (16 * i + jl) * LDA * 2 + 16 * ((2 * j + (q >> 1)) ^ (jl & 7)) + 8 * (q & 1)) = o;
+    if (d > 0 && d < NI / 2) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 4 * q + r;
+        *(_Float16*)(A + (16 * j + row) * LDA * 2 + 16 * ((2 * i + (jl >> 3)) ^ (row & 7)) +
+                     2 * (jl & 7)) = o[r];
+      }
+    }
+  };
+  for (int step = 0; step < steps; ++step) {
+    __syncthreads();  // X is there, B has been read
+    v4f acc[D], a[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int kb = grp; kb < mp / 32; kb += GROUPS) {
+      const v8h own = x_row(i, kb);
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        acc[d] = mfma_f16(d == 0 ? own : x_row((i + d) % NI, kb), own, acc[d]);
+    }
+    if constexpr (GROUPS > 1) {
+      v4f* parts = (v4f*)(smem + at.parts);
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (grp > 0) parts[((w - NI) * D + d) * 64 + lane] = acc[d];
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int s = 0; s < GROUPS - 1; ++s)
+          if (grp == 0) acc[d] += parts[((s * NI + i) * D + d) * 64 + lane];
+    }
+    const float sa = kScaleA / (p.cx * p.cx);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[d][r] *= sa;
+        a[d][r] = (float)(_Float16)acc[d][r];
+      }
+    if (grp == 0) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) put_a(d, acc[d]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (4 * q + r == jl) dA[16 * i + jl] = acc[0][r] - a[0][r];
+    }
+    __syncthreads();  // A is there
+#pragma unroll
+    for (int d = 0; d < D; ++d) acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (grp == 0) {
+#pragma unroll
+      for (int kb = 0; kb < NP / 32; ++kb) {
+        const v8h own = a_row(i, kb);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+          acc[d] = mfma_f16(d == 0 ? own : a_row((i + d) % NI, kb), own, acc[d]);
+      }
+    }
+    __syncthreads();  // A has been read
+    if (grp == 0) {
+      constexpr float fb = kScaleB / kScaleA * kNsB, fc = kScaleB / (kScaleA * kScaleA) * kNsC;
+      const float di = dA[16 * i + jl];
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const v4f dj = *(const v4f*)(dA + 16 * ((i + d) % NI) + 4 * q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool diag = d == 0 && 4 * q + r == jl;
+          acc[d][r] = fmaf(fc, fmaf(di + dj[r], a[d][r], acc[d][r]),
+                           fb * (diag ? a[d][r] + di : a[d][r]));
+          if (diag) dB[16 * i + jl] = acc[d][r] - (float)(_Float16)acc[d][r];
+        }
+        put_a(d, acc[d]);
+      }
+    }
+    __syncthreads();  // B is there
+    float own[NI];
+#pragma unroll
+    for (int it = 0; it < NI; ++it) own[it] = kNsA + dB[16 * it + jl] / kScaleB;
+#pragma unroll
+    for (int t = 0; t < TJ; t += PAIR) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (16 * (w + 8 * t) >= mp) break;
+      v4f y[PAIR][NI];
+#pragma unroll
+      for (int b = 0; b < PAIR; ++b)
+#pragma unroll
+        for (int it = 0; it < NI; ++it) y[b][it] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < NP / 32; ++kb) {
+        v8h x[PAIR];
+#pragma unroll
+        for (int b = 0; b < PAIR; ++b) {
+          // (a tile past the last one, which is not kept, reads the last one's columns)
+          const int jt = min(w + 8 * (t + b), mp / 16 - 1), c = 2 * jt + ((lane & 3) >> 1);
+          v4bf half[2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int row = 32 * kb + 8 * q + 4 * s + (jl >> 2);
+            half[s] = tr16(X + row * mp * 2 + 16 * (c ^ (row & 7)) + 8 * (lane & 1));
+          }
+          const v2i lo = __builtin_bit_cast(v2i, half[0]), hi = __builtin_bit_cast(v2i, half[1]);
+          x[b] = __builtin_bit_cast(v8h, v4i{lo.x, lo.y, hi.x, hi.y});
+        }
+#pragma unroll
+        for (int it = 0; it < NI; ++it) {
+          const v8h bf = a_row(it, kb);
+#pragma unroll
+          for (int b = 0; b < PAIR; ++b) y[b][it] = mfma_f16(x[b], bf, y[b][it]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < PAIR; ++b) {
+#pragma unroll
+        for (int it = 0; it < NI; ++it)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            st[t + b][it][r] = fmaf(own[it], st[t + b][it][r], y[b][it][r] / kScaleB);
+        if (step + 1 < steps && 16 * (w + 8 * (t + b)) < mp) put(t + b);
+      }
+    }
+  }
+  // the results leave through X's place as well (which the wave alone read last)
+  const float out = 1 / p.cx;  // a power of two
+#pragma unroll
+  for (int t = 0; t < TJ; ++t)
+    if (16 * (w + 8 * t) < mp) {
+#pragma unroll
+      for (int it = 0; it < NI; ++it) {
+        v4u16 o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          o[r] = __builtin_bit_cast(unsigned short, (__bf16)(st[t][it][r] * out));
+        *place(t, it) = o;
+      }
+    }
+  __syncthreads();
+  for (int row = row0, c = c0; row < p.R;) {
+    const int n = p.C - 8 * c;
+    typedef unsigned short h8 __attribute__((ext_vector_type(8), aligned(2)));
+    h8 o;
+    if (p.wide) {
+      o = *(const h8*)(X + row * mp * 2 + 16 * (c ^ (row & 7)));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o[e] = *(const unsigned short*)(X + (8 * c + e) * mp * 2 + 16 * ((row >> 3) ^ e) +
+                                        2 * (row & 7));
+    }
+    unsigned short* d = p.O + base + (int64_t)row * p.C + 8 * c;
+    if (n >= 8) {
+      *(h8*)d = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) d[e] = o[e];
+    }
+    row += rows_on, c += on;
+    if (c >= units_row) c -= units_row, ++row;
+  }
+}
+
 struct OSizes {
   int n, m, np, mp, ldn, ldm;
   int64_t sx, sxt, sa;
@@ -642,6 +972,30 @@ static int o_product(OParams& p, int cus, int dev, void* stream) {
   return o_launch<OCfg<128, 2>, MODE>(p, cus, dev, stream);
 }
 
+// The small kernel's row tiles, 0 where it does not fit or is slower: by columns of U, n > 64, its LDS
+// stores meet in the banks, so a few long ones of those are left to the launches (8 of 384 x 128:
+// 85 us, 71 there; 8 of 128 x 384: 65 and 72; 300 of 100 x 380: 135 and 495).
+static int small_rows(const OParams& p) {
+  const int ni = p.n <= 32 ? 2 : p.n <= 64 ? 4 : 8, mp = p.mp;
+  const int tiles = ni == 2 ? kSmallTiles<2> : ni == 4 ? kSmallTiles<4> : kSmallTiles<8>;
+  if (p.n > 128 || mp > 128 * tiles || small_lds(ni, mp).total > 160 * 1024) return 0;
+  return ni == 8 && !p.wide && mp > 256 && p.G <= 16 ? 0 : ni;
+}
+template <int NI>
+static int small_launch(OParams& p, int steps, int dev, void* stream) {
+  static std::mutex mu;
+  static bool set[64];
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!set[dev] && hipFuncSetAttribute((const void*)kg_ortho_small_kernel<NI>,
+                                         hipFuncAttributeMaxDynamicSharedMemorySize,
+                                         160 * 1024) != hipSuccess)
+      return KG_ERR_HIP;
+    set[dev] = true;
+  }
+  return launch(kg_ortho_small_kernel<NI>, p.G, 512, small_lds(NI, p.mp).total, stream, p, steps);
+}
+
 }  // namespace kg
 
 extern "C" int64_t kg_orthogonalize_workspace_bytes(int G, int R, int C) {
@@ -685,6 +1039,13 @@ extern "C" int kg_orthogonalize(const void* U, void* O, int G, int R, int C, int
   p.ldn = s.ldn, p.ldm = s.ldm;
   p.b16 = type == KG_ROWS_BF16, p.wide = R <= C;
   p.XT = (unsigned short*)(ws + s.xt[0]), p.XN = (unsigned short*)(ws + s.xt[1]);
+  // (a workgroup of the small kernel writes its matrix while others may still read theirs)
+  const bool apart = G == 1 || (U == O && e == 2) || !ranges_overlap(U, count * e, O, count * 2);
+  const int rows = apart ? small_rows(p) : 0;
+  if (rows)
+    return rows == 2   ? small_launch<2>(p, steps, dev, stream)
+           : rows == 4 ? small_launch<4>(p, steps, dev, stream)
+                       : small_launch<8>(p, steps, dev, stream);
   const int64_t chunk = norm_chunk((int64_t)R * C);
   p.chunks = (int)(((int64_t)R * C + chunk - 1) / chunk);
   int rc = launch2(kg_ortho_norm_kernel, p.chunks, G, 256, 0, stream, p);

@@ -113,6 +113,41 @@ def test_last_rounds(G, R, C):
         near(o[g], (x.t() if R > C else x).cpu())
 
 
+@pytest.mark.parametrize("G,n,m", [(3, 1, 2048), (2, 7, 30), (5, 32, 32), (2, 32, 2048), (2, 32, 2049),
+                                   (2, 33, 100), (40, 64, 1024), (2, 64, 1025), (3, 50, 999), (2, 65, 66),
+                                   (3, 128, 384), (2, 128, 385), (300, 100, 380), (2, 129, 300)])
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_small(G, n, m, tall, dtype):
+    """Matrices of a workgroup each, and the first ones past that."""
+    R, C = (m, n) if tall else (n, m)
+    us = torch.stack([update(R, C, 7 * G + g, "channels" if g % 2 else "noise", dtype) for g in range(min(G, 4))])
+    us = us.repeat(-(-G // 4), 1, 1)[:G].contiguous() if G > 4 else us
+    guard = torch.full((G * R * C + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = guard[32:-32].view(G, R, C)
+    kg.kg_orthogonalize(us, o)
+    assert (guard[:32] == 7).all() and (guard[-32:] == 7).all()
+    for g in range(min(G, 4)):
+        near(o[g], steps64(us[g]))
+    for g in range(4, G):
+        assert torch.equal(o[g], o[g % 4])
+
+
+def test_small_shifted_over_its_inputs():
+    """The result lies over the inputs of other matrices."""
+    us = torch.stack([update(40, 96, g) for g in range(6)])
+    want = kg.kg_orthogonalize(us)
+    for shift in (0, 40 * 96 * 3 + 8):
+        space = torch.zeros(us.numel() * 4 + 64 * 1024, dtype=torch.uint8, device="cuda")
+        u = space[1024:1024 + us.numel() * 4].view(torch.float32).view(us.shape)
+        u.copy_(us)
+        o = space[1024 + 2 * shift:][:us.numel() * 2].view(torch.bfloat16).view(us.shape)
+        kg.kg_orthogonalize(u, o)
+        for g in range(6):
+            near(o[g], steps64(us[g]))
+            assert (o[g].float() - want[g].float()).abs().max() <= 2.0 ** -6
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 def test_steps(steps):
     u = update(150, 100, steps)
