@@ -235,6 +235,32 @@ def test_on_a_stream_and_in_a_graph():
         assert torch.equal(got, kg.kg_orthogonalize(u))
 
 
+def test_small_ones_in_a_graph_and_on_two_streams():
+    """One launch each: in a captured graph whose workspace eager calls share, in turn, and at once on two streams."""
+    us = torch.stack([update(60, 300, i, dtype=torch.bfloat16) for i in range(5)])
+    want = kg.kg_orthogonalize(us)
+    for g in range(5):
+        near(want[g], steps64(us[g]))
+    ws, got = kg.new_orthogonalize_workspace(5, 60, 300, "cuda"), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kg.kg_orthogonalize(us, got, ws=ws)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        assert torch.equal(got, want)
+        assert torch.equal(kg.kg_orthogonalize(us, ws=ws), want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[kg.kg_orthogonalize(us, stream=s) for s in streams] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for two in outs for o in two)
+    # in place
+    same = us.clone()
+    kg.kg_orthogonalize(same, same)
+    assert torch.equal(same, want)
+
+
 def test_a_step_on_expert_gradients():
     """kg_wgrad's gradient of a layer's weights made orthogonal: against 64 bits, and along the
     gradient."""
