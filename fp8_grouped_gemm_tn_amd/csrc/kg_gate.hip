@@ -361,14 +361,14 @@ __device__ __forceinline__ int choose_biased(const float (&x)[V], const float (&
   return l < k ? out : -1;
 }
 
-// The sums over all workgroups' lines, in their order; the last workgroup to finish adds up the
-// loss, in the order of the experts.
+// The sums over all workgroups' lines, in a fixed order; the last workgroup to finish adds up the
+// loss, in one as well.
 constexpr int kGateSumExperts = 8;
-__global__ __launch_bounds__(256) void kg_gate_sum_kernel(GateParams p, int blocks) {
-  constexpr int E = kGateSumExperts, S = 256 / E;
-  __shared__ double sums[S][E];
-  __shared__ int cnts[S][E];
-  __shared__ int last;
+constexpr int kGateSumThreads = 1024;  // 128 lines at a time (65536 tokens, 256 experts: 5 us)
+__global__ __launch_bounds__(kGateSumThreads) void kg_gate_sum_kernel(GateParams p, int blocks) {
+  constexpr int E = kGateSumExperts, S = kGateSumThreads / E, WAVES = kGateSumThreads / 64;
+  __shared__ double sums[WAVES][E];
+  __shared__ int cnts[WAVES][E];
   const int e = threadIdx.x % E, part = threadIdx.x / E, g = blockIdx.x * E + e;
   double sum = 0;
   int cnt = 0;
@@ -379,12 +379,22 @@ __global__ __launch_bounds__(256) void kg_gate_sum_kernel(GateParams p, int bloc
       cnt += p.part_counts[(int64_t)b * p.G + g];
     }
   }
-  sums[part][e] = sum;
-  cnts[part][e] = cnt;
-  __syncthreads();
-  if (threadIdx.x < E) {
 #pragma unroll
-    for (int i = 1; i < S; ++i) {
+  for (int d = E; d < 64; d <<= 1) {
+    sum += __shfl_xor(sum, d, 64);
+    cnt += __shfl_xor(cnt, d, 64);
+  }
+  if ((threadIdx.x & 63) < E) {
+    sums[threadIdx.x >> 6][e] = sum;
+    cnts[threadIdx.x >> 6][e] = cnt;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  const bool own = threadIdx.x < E;
+  double term = 0;
+  if (own) {
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) {
       sum += sums[i][e];
       cnt += cnts[i][e];
     }
@@ -392,21 +402,24 @@ __global__ __launch_bounds__(256) void kg_gate_sum_kernel(GateParams p, int bloc
       if (p.counts) p.counts[g] = cnt;
       if (p.psum) p.psum[g] = (float)sum;
     }
-    double term = sum * (double)cnt;
-#pragma unroll
-    for (int d = 1; d < E; d <<= 1) term += __shfl_xor(term, d, E);
-    if (threadIdx.x == 0 && p.loss) {
-      __hip_atomic_store(&p.part_loss[blockIdx.x], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-             (int)gridDim.x - 1;
-      if (last) {
-        double total = 0;
-        for (unsigned b = 0; b < gridDim.x; ++b)
-          total += __hip_atomic_load(&p.part_loss[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *p.loss = (float)(p.coef * total);
-      }
-    }
+    term = sum * (double)cnt;
   }
+  if (!p.loss) return;
+#pragma unroll
+  for (int d = 1; d < E; d <<= 1) term += __shfl_xor(term, d, 64);
+  int last = 0;
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(&p.part_loss[blockIdx.x], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(p.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+           (int)gridDim.x - 1;
+  }
+  if (!__shfl(last, 0, 64)) return;
+  double total = 0;
+  for (unsigned b = threadIdx.x; b < gridDim.x; b += 64)
+    total += __hip_atomic_load(&p.part_loss[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d, 64);
+  if (threadIdx.x == 0) *p.loss = (float)(p.coef * total);
 }
 
 template <bool B16, int LPR, int C, bool BIAS>
@@ -695,7 +708,7 @@ extern "C" int kg_gate(const void* X, int64_t ldx, const float* bias, int64_t T,
                                 : KG_GATE_PICK(kg_gate_kernel, b16, G, row16, KG_GATE_COMMA_FALSE);
   const int rc = launch(fn, blocks, kGateThreads, 0, stream, p);
   if (rc != KG_OK || !stats) return rc;
-  return launch(kg_gate_sum_kernel, gate_sum_blocks(G), 256, 0, stream, p, (int)blocks);
+  return launch(kg_gate_sum_kernel, gate_sum_blocks(G), kGateSumThreads, 0, stream, p, (int)blocks);
 }
 
 extern "C" int kg_gate_bwd(const void* X, int64_t ldx, const int32_t* idx, const float* dw,
