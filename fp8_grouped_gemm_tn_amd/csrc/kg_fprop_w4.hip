@@ -22,6 +22,7 @@
 #include "kg_host.h"
 #include "kg_rows.h"
 #include "kg_sched.h"
+#include "kg_w4_plan.h"
 #include "kgwgrad.h"
 
 namespace kg {
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(1024, 4) void kg_fprop_w4_stream_kernel(WParams p) 
   const unsigned char* zbase = p.zp + out0 * groups;
   // ... and of this wave, the part-th of those that share them
   const int side = w / p.split, part = w - side * p.split, m0 = side * N0;
-  const int outs = max(0, min(N0, all - m0));
+  const int outs = w_set_outs(all, m0, N0);
   const unsigned char* wbase = p.W + (out0 + (outs ? m0 : 0)) * kbytes;
   const bool zeros = p.zp != nullptr;
   uint32_t woff[NJ];
@@ -294,8 +295,7 @@ __global__ __launch_bounds__(1024, 4) void kg_fprop_w4_stream_kernel(WParams p) 
     // This wave's blocks, [from, to); what lies past them reads as zeros.
     const int from = part * nk / p.split, to = (part + 1) * nk / p.split;
     auto load = [&](int kb, int d) {
-      const bool in = kb < to;
-      const Rsrc wr = rsrc_of(wbase + kb * 64, in ? (uint32_t)(outs * kbytes - kb * 64) : 0u);
+      const Rsrc wr = rsrc_of(wbase + kb * 64, w_codes_left(outs, kbytes, kb, to));
 #pragma unroll
       for (int i = 0; i < NJ; ++i) wx[d][i] = load16(wr, woff[i]);
     };

@@ -1,0 +1,32 @@
+"""kg_fprop_w4's host-side arithmetic: what its launches read and hold, without a GPU."""
+import pytest
+
+import w4_plan
+
+FORMS = [(8, 8, 1), (16, 8, 1), (8, 8, 2), (16, 8, 2), (8, 4, 2), (16, 4, 2)]  # waves, split, nj
+
+
+@pytest.mark.parametrize("waves,split,nj", FORMS)
+@pytest.mark.parametrize("K", [32, 128, 160, 640, 1056, 7168])
+def test_streaming_reads_end_with_the_weights(waves, split, nj, K):
+    """Every wave's buffer of codes ends with the last output of its set at the latest, whatever
+    part of the last workgroup's outputs exists: also where a set has none. (A load's 16 bytes are
+    bounded by the buffer, so this bounds every address.)"""
+    L = w4_plan.lib()
+    n0, kbytes, nk = 16 * nj, K // 2, -(-K // 128)
+    sets = waves // split
+    for outs_there in range(1, n0 * sets + 1):  # of the last workgroup
+        for side in range(sets):
+            m0 = side * n0
+            outs = L.set_outs(outs_there, m0, n0)
+            assert outs == max(0, min(n0, outs_there - m0))
+            base = (m0 if outs else 0) * kbytes
+            for part in range(split):
+                first, to = part * nk // split, (part + 1) * nk // split
+                for kb in range(first, to + 8):  # and the blocks asked for behind the last one
+                    left = L.codes_left(outs, kbytes, kb, to)
+                    if kb >= to or outs == 0:
+                        assert left == 0
+                    else:
+                        assert left > 0 and base + 64 * kb + left == (m0 + outs) * kbytes
+                        assert base + 64 * kb + left <= outs_there * kbytes
