@@ -726,98 +726,17 @@ static WLaunch w_tiled(int kind, int group, bool outb) {
   return WLaunch{w_pick<TiledOf<C>::template F>(kind, group, outb), C::BT, C::BN, 2 * C::STAGE};
 }
 
-// Which kernel and tile, by M_total and G (the experts' sizes are known on the device only), from
-// estimates of the time in ns whose figures are measured; every choice is right for every
-// distribution of the rows. Measured in us, equal rows, streaming / 32 x 128 / 64 x 128 / 128 x 128 /
-// 128 x 256 (/ 256 x 256):
-//   e2m1  1 expert, N 4096, K 7168    16 rows 18 / 32 / 39 / 49 / 83, 64 rows 56 / 34 / 39 / 50 / 85
-//         8 of N 2048, K 2048         16 rows each 10 / 13 / 15 / 19 / 28 / 43, 128 rows 49 / 24 / 18 / 21 / 30 / 45
-//         32 of N 4096, K 7168        4 rows each 101 / 171 / 182 / 208 / 216 / 304,
-//                                     256 rows - / 1127 / 695 / 504 / 517 / 397
-//   whole numbers, 128 per scale, the last 32 experts
-//                                     4 rows each 109 / 231 / 241 / 295 / 287, 256 rows - / 1588 / 940 / 672 / 663
-// (The estimates take experts' rows to be uneven, so at equal rows the next larger tile may be taken.)
-
-// Streaming: 16 waves on a compute unit, as two workgroups, or as one whose LDS then holds twice the
-// rows (8 rows of 8 experts, N 4096, K 7168, e2m1: 42 us as two, 24 as one; 2 rows: 22 and 23). A set
-// has 16 outputs where 32 would leave half of the compute units idle (1 row of 1 expert: 6.9 us with
-// 16, 8.3 with 32; 2 rows of 8 experts: 34 and 27). 8 waves share them, or 4 where that still fills
-// every compute unit (2 rows of 8 experts: 27 us with 8, 22 with 4; of 1 expert: 8.3 and 11).
-struct WStream {
-  int64_t rows, lds, tokens, scales, ns;  // rows 0: it cannot be used
-  int nj, waves, split;
-};
-static WStream w_stream(int64_t M, int G, int N, int K, int cus, int kind, int group, bool zp) {
-  const int64_t live = G < M ? G : M, per_out = K / group, nk = (K + 127) / 128;
-  const int sb = kind == KG_W4_E2M1 ? 1 : kind == KG_W4_INT_BF16 ? 2 : 4;
-  auto kbytes = [](int64_t n) { return (n + 1023) / 1024 * 1024; };
-  const int64_t row_bytes = kbytes(nk * 256);
-  const int64_t most = M < 16 ? M : 16, uneven = G == 1 ? M : (3 * ((M + G - 1) / G) + 1) / 2;
-  const int64_t block_ns = kind == KG_W4_E2M1 ? 400 : group == 32 ? 850 : 600;
-  WStream best;
-  best.rows = 0;
-  best.ns = INT64_MAX;
-  for (int waves = 8; waves <= 16; waves += 8) {
-    WStream s;
-    s.waves = waves;
-    s.nj = live * ((N + 31) / 32) <= cus / 2 ? 1 : 2;
-    s.split = s.nj == 2 && live * ((N + 63) / 64) >= 2 * cus ? 4 : 8;
-    const int bn = 16 * s.nj * waves / s.split;
-    s.scales = kbytes(bn * per_out * sb);
-    const int64_t rest = s.scales + (zp ? kbytes(bn * per_out) : 0);
-    const int64_t room = (waves == 8 ? 79 : 159) * 1024 - rest;
-    s.rows = row_bytes ? room / row_bytes : 16;
-    if (s.rows > most) s.rows = most;
-    if (s.rows < 1) continue;
-    s.tokens = kbytes(s.rows * row_bytes);
-    if (s.tokens < waves * s.nj * 1024) s.tokens = waves * s.nj * 1024;
-    s.lds = s.tokens + rest;
-    // a workgroup's start and end, and a wave's blocks
-    const int64_t wgs = live * ((N + bn - 1) / bn), slots = (int64_t)cus * 16 / waves;
-    const int64_t passes = (uneven + s.rows - 1) / s.rows, blocks = nk / s.split + 1;
-    s.ns = 3000 + passes * ((wgs + slots - 1) / slots) *
-                      (2600 + blocks * block_ns * (wgs * waves > 8 * cus ? 2 : 1));
-    if (s.ns < best.ns) best = s;
-  }
-  return best;
-}
-
-// Tiles: rounds over the compute units times the blocks' time. Of several experts each has a last
-// tile that is half filled on average.
-struct WTile {
-  WLaunch l;
-  int64_t ns;
-};
-static WTile w_tile(int64_t M, int G, int N, int K, int cus, int kind, int group, bool outb) {
-  const bool mx = kind == KG_W4_E2M1;
-  struct {
-    int bt, bn, ns;  // of 128 channels
-  } const tiles[] = {{32, 128, mx ? 500 : 780},
-                     {64, 128, mx ? 630 : 940},
-                     {128, 128, mx ? 830 : 1270},
-                     {128, 256, mx ? 1500 : 2200},
-                     {256, 256, 2350}};
-  const int64_t live = G < M ? G : M;
-  int best = 0;
-  WTile t;
-  t.ns = INT64_MAX;
-  for (int i = 0; i < (mx ? 5 : 4); ++i) {
-    int64_t mt = live == 1 ? (M + tiles[i].bt - 1) / tiles[i].bt * 2 : 2 * M / tiles[i].bt + live;
-    if (mt < 2 * live) mt = 2 * live;
-    const int64_t n = (mt * ((N + tiles[i].bn - 1) / tiles[i].bn) + 1) / 2;
-    const int64_t ns = 4500 + (n + cus - 1) / cus * ((K + 127) / 128 * tiles[i].ns + 1000);
-    if (ns < t.ns) t.ns = ns, best = i;
-  }
+// The tiled kernel of w_tile's choice.
+static WLaunch w_tiled(const WTile& t, int kind, int group, bool outb) {
   // (256 x 256 for e2m1 only: with the sums of whole numbers' groups it does not fit the registers)
   using Large = WCfg<256, 256, 4, 1, 1>;
-  t.l = best == 0   ? w_tiled<WCfg<32, 128, 1, 2, 2>>(kind, group, outb)
-        : best == 1 ? w_tiled<WCfg<64, 128, 2, 2, 2>>(kind, group, outb)
-        : best == 2 ? w_tiled<WCfg<128, 128, 2, 2, 1>>(kind, group, outb)
-        : best == 3 ? w_tiled<WCfg<128, 256, 2, 1, 2>>(kind, group, outb)
-                    : WLaunch{outb ? (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, true>
-                                   : (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, false>,
-                              Large::BT, Large::BN, 2 * Large::STAGE};
-  return t;
+  return t.bt == 32    ? w_tiled<WCfg<32, 128, 1, 2, 2>>(kind, group, outb)
+         : t.bt == 64  ? w_tiled<WCfg<64, 128, 2, 2, 2>>(kind, group, outb)
+         : t.bn == 128 ? w_tiled<WCfg<128, 128, 2, 2, 1>>(kind, group, outb)
+         : t.bt == 128 ? w_tiled<WCfg<128, 256, 2, 1, 2>>(kind, group, outb)
+                       : WLaunch{outb ? (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, true>
+                                      : (const void*)kg_fprop_w4_kernel<Large, kE2M1, false, false>,
+                                 Large::BT, Large::BN, 2 * Large::STAGE};
 }
 
 // Lets a kernel have all of a compute unit's LDS, once per kernel and device.
@@ -828,7 +747,7 @@ static bool w_lds_allowed(const void* fn, int dev) {
   std::lock_guard<std::mutex> lk(mu);
   for (int i = 0; i < count[dev]; ++i)
     if (set[dev][i] == fn) return true;
-  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - 512) != hipSuccess)
+  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kWLds) != hipSuccess)
     return false;
   if (count[dev] < 128) set[dev][count[dev]++] = fn;
   return true;
@@ -887,8 +806,8 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
   int threads = 512;
   const WStream st = w_stream(M_total, G, N, K, cus, kind, group, zp != nullptr);
   const int64_t live = G < M_total ? G : M_total;
-  const WTile tile = w_tile(M_total, G, N, K, cus, kind, group, outb);
-  if (st.rows > 0 && st.ns <= tile.ns) {
+  const WTile tile = w_tile(M_total, G, N, K, cus, kind);
+  if (w_streams(st, tile)) {
     const int bn = 16 * st.nj * st.waves / st.split;
     l.fn = st.nj == 1 ? w_pick<StreamOf<1>::F>(kind, group, outb) : w_pick<StreamOf<2>::F>(kind, group, outb);
     l.lds = (int)st.lds;
@@ -901,7 +820,7 @@ extern "C" int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void
     grid = live * p.tiles_n;
     if (grid > INT32_MAX / 1024) return KG_ERR_UNSUPPORTED;
   } else {
-    l = tile.l;
+    l = w_tiled(tile, kind, group, outb);
     l.lds += 2 * (G + 1) * 4;
     p.tiles_n = (N + l.bn - 1) / l.bn;
     const int64_t max_items = (M_total / l.bt + G) * (int64_t)p.tiles_n;

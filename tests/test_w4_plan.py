@@ -30,3 +30,21 @@ def test_streaming_reads_end_with_the_weights(waves, split, nj, K):
                     else:
                         assert left > 0 and base + 64 * kb + left == (m0 + outs) * kbytes
                         assert base + 64 * kb + left <= outs_there * kbytes
+
+
+def forms():
+    for kind, group in (("bf16", 128), ("bf16", 64), ("bf16", 32), ("f32", 128), ("f32", 64), ("f32", 32),
+                        ("e2m1", 32)):
+        for zp in (0, 1) if kind != "e2m1" else (0,):
+            yield kind, group, zp
+
+
+@pytest.mark.parametrize("kind,group,zp", list(forms()))
+def test_streaming_fits_in_lds(kind, group, zp):
+    """What a streaming launch asks for is what a workgroup may have: over widths, experts and
+    rows, every K of whole groups up to 16384."""
+    for G, M in ((1, 1), (1, 16), (8, 8), (8, 100), (64, 64), (256, 40)):
+        for N in (1, 33, 4096, 5120):
+            for K in range(group, 16385, group):
+                p = w4_plan.Plan(M, G, N, K, kind, group, zp)
+                assert not p.streams or p.lds <= p.limit, (M, G, N, K, p.waves, p.lds)

@@ -13,6 +13,12 @@ extern "C" int set_outs(int all, int m0, int most) { return kg::w_set_outs(all, 
 extern "C" unsigned codes_left(int outs, int kbytes, int kb, int to) {
   return kg::w_codes_left(outs, kbytes, kb, to);
 }
+extern "C" void plan(long long M, int G, int N, int K, int cus, int kind, int group, int zp, long long* out) {
+  const kg::WStream s = kg::w_stream(M, G, N, K, cus, kind, group, zp != 0);
+  const kg::WTile t = kg::w_tile(M, G, N, K, cus, kind);
+  const long long x[] = {kg::w_streams(s, t), s.rows, s.lds, s.tokens, s.scales, s.nj, s.waves, s.split, t.bt, t.bn, kg::kWLds};
+  for (long long v : x) *out++ = v;
+}
 """
 
 
@@ -27,3 +33,14 @@ def lib():
         L = ctypes.CDLL(so)
     L.codes_left.restype = ctypes.c_uint32
     return L
+
+
+class Plan:
+    """What a call takes: `streams`, and then rows, lds, tokens, scales (bytes), nj, waves, split;
+    else a tile of bt x bn. limit: the LDS that a workgroup may ask for."""
+
+    def __init__(self, M, G, N, K, kind, group, zp, cus=256):
+        out = (ctypes.c_longlong * 11)()
+        lib().plan(ctypes.c_longlong(M), G, N, K, cus, {"bf16": 0, "f32": 1, "e2m1": 2}[kind], group, zp, out)
+        (self.streams, self.rows, self.lds, self.tokens, self.scales, self.nj, self.waves, self.split,
+         self.bt, self.bn, self.limit) = out
