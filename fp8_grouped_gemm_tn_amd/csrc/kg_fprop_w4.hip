@@ -252,7 +252,7 @@ __global__ __launch_bounds__(1024, 4) void kg_fprop_w4_stream_kernel(WParams p) 
   // (known to be one value per wave: buffers are described by scalars)
   g = uniform(g), rows = uniform(rows);
   row0 = uniform((int)row0);  // below 2^31
-  const int nk = (p.K + 127) / 128, pieces = max(1, (nk + 3) / 4);
+  const int nk = (p.K + 127) / 128, pieces = w_pieces(nk);
   const int kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
   const int all = min(N0 * sets, p.N - n0);  // outputs of the workgroup
   const int64_t out0 = (int64_t)g * p.N + n0;

@@ -21,6 +21,9 @@ constexpr uint32_t w_codes_left(int outs, int kbytes, int kb, int to) {
   return outs > 0 && kb < to ? (uint32_t)(outs * kbytes - 64 * kb) : 0u;
 }
 
+// Streaming: the KB of LDS of a row's tokens, four blocks of 128 channels each; one at least.
+constexpr int w_pieces(int nk) { return nk > 4 ? (nk + 3) / 4 : 1; }
+
 // Which kernel and tile, by M_total and G (the experts' sizes are known on the device only), from
 // estimates of the time in ns whose figures are measured; every choice is right for every
 // distribution of the rows. Measured in us, equal rows, streaming / 32 x 128 / 64 x 128 / 128 x 128 /
@@ -48,7 +51,7 @@ constexpr int64_t w_kbytes(int64_t n) { return (n + 1023) / 1024 * 1024; }
 constexpr WStream w_stream(int64_t M, int G, int N, int K, int cus, int kind, int group, bool zp) {
   const int64_t live = G < M ? G : M, per_out = K / group, nk = (K + 127) / 128;
   const int sb = kind == KG_W4_E2M1 ? 1 : kind == KG_W4_INT_BF16 ? 2 : 4;
-  const int64_t row_bytes = w_kbytes(nk * 256);
+  const int64_t row_bytes = 1024ll * w_pieces((int)nk);
   const int64_t most = M < 16 ? M : 16, uneven = G == 1 ? M : (3 * ((M + G - 1) / G) + 1) / 2;
   const int64_t block_ns = kind == KG_W4_E2M1 ? 400 : group == 32 ? 850 : 600;
   WStream best{};
@@ -62,7 +65,7 @@ constexpr WStream w_stream(int64_t M, int G, int N, int K, int cus, int kind, in
     s.scales = w_kbytes(bn * per_out * sb);
     const int64_t rest = s.scales + (zp ? w_kbytes(bn * per_out) : 0);
     const int64_t room = (waves == 8 ? 79 : 159) * 1024 - rest;
-    s.rows = row_bytes ? room / row_bytes : 16;
+    s.rows = room / row_bytes;
     if (s.rows > most) s.rows = most;
     if (s.rows < 1) continue;
     s.tokens = w_kbytes(s.rows * row_bytes);

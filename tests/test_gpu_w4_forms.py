@@ -38,3 +38,14 @@ def test_scales_that_fill_the_lds(ms, N, K, group, zero):
     p = plan(sum(ms), len(ms), N, K, "f32", group, zero)
     assert not p.streams or p.lds <= p.limit
     check(ms, N, K, group, "f32", 1, zero, some=torch.tensor([0, 1, 15, 16, 31, 32, N // 2 + 3, N - 17, N - 1]))
+
+
+@pytest.mark.parametrize("kind,dtype", [("bf16", torch.bfloat16), ("f32", torch.float32), ("e2m1", torch.uint8)])
+@pytest.mark.parametrize("rows", [1, 16, 100])
+def test_no_channels(kind, dtype, rows):
+    """K = 0: zeros, from as many rows as a workgroup takes at a time too."""
+    D = torch.full((rows, 40), 3.0, device="cuda")
+    empty = lambda *s, dtype: torch.empty(s, dtype=dtype, device="cuda")
+    kg.kg_fprop_w4(empty(rows, 0, dtype=torch.bfloat16), empty(1, 40, 0, dtype=torch.uint8),
+                   empty(1, 40, 0, dtype=dtype), D, torch.tensor([rows], dtype=torch.int32, device="cuda"))
+    assert kg.kg_status() == kg.KG_OK and (D == 0).all()

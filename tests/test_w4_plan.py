@@ -48,3 +48,21 @@ def test_streaming_fits_in_lds(kind, group, zp):
             for K in range(group, 16385, group):
                 p = w4_plan.Plan(M, G, N, K, kind, group, zp)
                 assert not p.streams or p.lds <= p.limit, (M, G, N, K, p.waves, p.lds)
+
+
+@pytest.mark.parametrize("kind,group,zp", list(forms()))
+def test_a_launch_holds_its_rows(kind, group, zp):
+    """The LDS set aside for tokens holds as many rows as the kernel loads at a time, without any
+    channels too, and the closing sums of every wave; scales and zero points follow."""
+    L, bytes_of = w4_plan.lib(), {"bf16": 2, "f32": 4, "e2m1": 1}[kind]
+    for G, M in ((1, 1), (1, 5), (1, 16), (1, 100), (8, 8), (64, 64), (256, 40), (16, 512)):
+        for N in (1, 33, 700, 4096):
+            for K in (0, group, 4 * group, 512, 640, 1024, 2048, 4096, 7168, 8192, 14336):
+                p = w4_plan.Plan(M, G, N, K, kind, group, zp)
+                if not p.rows:
+                    continue
+                outs = 16 * p.nj * p.waves // p.split
+                assert p.rows * 1024 * L.pieces(-(-K // 128)) <= p.tokens
+                assert 1024 * p.waves * p.nj <= p.tokens
+                assert outs * (K // group) * bytes_of <= p.scales
+                assert p.tokens + p.scales + (outs * (K // group) if zp else 0) <= p.lds <= p.limit

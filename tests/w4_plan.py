@@ -13,6 +13,7 @@ extern "C" int set_outs(int all, int m0, int most) { return kg::w_set_outs(all, 
 extern "C" unsigned codes_left(int outs, int kbytes, int kb, int to) {
   return kg::w_codes_left(outs, kbytes, kb, to);
 }
+extern "C" int pieces(int nk) { return kg::w_pieces(nk); }
 extern "C" void plan(long long M, int G, int N, int K, int cus, int kind, int group, int zp, long long* out) {
   const kg::WStream s = kg::w_stream(M, G, N, K, cus, kind, group, zp != 0);
   const kg::WTile t = kg::w_tile(M, G, N, K, cus, kind);
