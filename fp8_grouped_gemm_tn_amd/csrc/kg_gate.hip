@@ -628,13 +628,18 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_bwd_kernel(GateBwdParams
 
 // Whether a token has 16 lanes. Few tokens of more than 64 experts have 64, so that a lane has fewer
 // of the logits that each step goes through.
-static bool gate_row16(int64_t T, int G) { return G <= 64 || (G <= 256 && T > 1024); }
+constexpr int kGateFew = 1024;
+static bool gate_row16(int64_t T, int G) { return G <= 64 || (G <= 256 && T > kGateFew); }
 static int64_t gate_blocks(int64_t T, int G) {
   const int64_t rows = kGateThreads / 64 * (gate_row16(T, G) ? 4 : 1);
   const int64_t n = (T + rows - 1) / rows;
   return n < 1 ? 1 : n < kGateBlocks ? n : kGateBlocks;
 }
 static int64_t gate_sum_blocks(int G) { return (G + kGateSumExperts - 1) / kGateSumExperts; }
+// Bytes of workspace that a call uses: a line of sums for each workgroup.
+static int64_t gate_bytes(int64_t T, int G) {
+  return 64 + gate_sum_blocks(G) * 8 + gate_blocks(T, G) * G * 8;
+}
 
 static bool gate_sizes_ok(int64_t T, int G, int k) { return T >= 0 && G >= 1 && k >= 1 && k <= G; }
 static bool gate_sizes_taken(int64_t T, int G, int k, int64_t ld) {
@@ -659,7 +664,10 @@ static bool gate_sizes_taken(int64_t T, int G, int k, int64_t ld) {
 extern "C" int64_t kg_gate_workspace_bytes(int64_t T, int G) {
   using namespace kg;
   if (T < 0 || G < 1 || G > 1024 || T > INT32_MAX) return -1;
-  return 64 + gate_sum_blocks(G) * 8 + gate_blocks(T, G) * G * 8;
+  // Enough for fewer tokens too: kGateFew of them may take more workgroups than a few more do. (More
+  // experts never take fewer.)
+  const int64_t few = gate_bytes(T < kGateFew ? T : kGateFew, G), own = gate_bytes(T, G);
+  return few > own ? few : own;
 }
 
 extern "C" int kg_gate(const void* X, int64_t ldx, const float* bias, int64_t T, int G, int k,
@@ -680,7 +688,7 @@ extern "C" int kg_gate(const void* X, int64_t ldx, const float* bias, int64_t T,
       ((uintptr_t)w & 3) || ((uintptr_t)counts & 3) || ((uintptr_t)psum & 3) ||
       ((uintptr_t)loss & 3) || (stats && ((uintptr_t)workspace & 15)))
     return KG_ERR_ALIGN;
-  const int64_t need = stats ? kg_gate_workspace_bytes(T, G) : 0;
+  const int64_t need = stats ? gate_bytes(T, G) : 0;
   if (workspace_bytes < need) return KG_ERR_SHAPE;
   const void* outs[] = {idx, w, counts, psum, loss, stats ? workspace : nullptr};
   const size_t sizes[] = {(size_t)T * k * 4, (size_t)T * k * 4, (size_t)G * 4, (size_t)G * 4, 4,

@@ -145,7 +145,7 @@ def kg_route(idx, ks, pos=None, src=None, ws=None, stream=None):
 
 def new_gate_workspace(T, G, device):
     """The workspace of kg_gate with statistics, for T tokens and G experts; keep it for later
-    calls of these sizes."""
+    calls of at most these sizes."""
     n = _load().kg_gate_workspace_bytes(T, G)
     if n < 0:
         _fail(KG_ERR_SHAPE, "kg_gate_workspace_bytes")
@@ -523,8 +523,8 @@ def kg_adamw(table, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step
 
 
 def new_orthogonalize_workspace(G, R, C, device):
-    """The workspace of kg_orthogonalize for G matrices [R, C]; keep it for later calls of these
-    sizes."""
+    """The workspace of kg_orthogonalize for G matrices [R, C]; keep it for later calls of at most
+    these sizes."""
     n = _load().kg_orthogonalize_workspace_bytes(G, R, C)
     if n < 0:
         _fail(KG_ERR_SHAPE, "kg_orthogonalize_workspace_bytes")

@@ -540,7 +540,8 @@ int kg_adamw(const void* table, int count, int64_t items, int kinds, double lr, 
 int kg_gate(const void* X, int64_t ldx, const float* bias, int64_t T, int G, int k, int type,
             int flags, double scale, double coef, int32_t* idx, float* w, int32_t* counts,
             float* psum, float* loss, void* workspace, int64_t workspace_bytes, void* stream);
-/* Workspace of kg_gate in bytes, or -1 for sizes it does not take. */
+/* Workspace of kg_gate in bytes, enough for calls of fewer tokens and experts too, or -1 for sizes it
+   does not take. */
 int64_t kg_gate_workspace_bytes(int64_t T, int G);
 
 /*
