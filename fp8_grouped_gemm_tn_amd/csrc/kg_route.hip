@@ -19,6 +19,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kg_device.h"
 #include "kg_host.h"
 #include "kgwgrad.h"
@@ -692,6 +694,10 @@ static int64_t route_block(int64_t n) {
   return per > kSortBlock ? per : kSortBlock;
 }
 static int64_t route_blocks(int64_t n) { return (n + route_block(n) - 1) / route_block(n); }
+// Bytes of workspace that a plan of n slots uses: a line of counts for each block.
+static int64_t route_bytes(int64_t n, int G) {
+  return n <= kSoloSlots ? 0 : route_blocks(n) * (G + 1) * 4;
+}
 
 // Checks that the row kernels share, and their launch shape. A token's row is cut into units of
 // `unit` bytes (the last one partial).
@@ -756,16 +762,17 @@ extern "C" int64_t kg_route_workspace_bytes(int64_t T, int k, int G) {
   if (T < 0 || k < 0 || G < 0 || G > kRouteMaxGroups || k > 4096 || T > INT32_MAX - 1 ||
       (k > 0 && T > (int64_t)(INT32_MAX - 1) / k))
     return -1;
-  const int64_t n = T * k;
-  return n <= kSoloSlots ? 0 : route_blocks(n) * (G + 1) * 4;
+  // Enough for fewer slots too: the most blocks of any plan of up to n (blocks grow in whole runs, so a
+  // few more slots may have fewer of them).
+  const int64_t n = T * k, most = std::min<int64_t>((n + kSortBlock - 1) / kSortBlock, kSortBlocks);
+  return n <= kSoloSlots ? 0 : most * (G + 1) * 4;
 }
 
 extern "C" int kg_route(const int32_t* idx, int64_t T, int k, int G, int32_t* ks, int32_t* pos,
                         int32_t* src, void* workspace, int64_t workspace_bytes, void* stream) {
   if (T < 0 || k < 0 || G < 0 || workspace_bytes < 0) return KG_ERR_SHAPE;
-  const int64_t need = kg_route_workspace_bytes(T, k, G);
-  if (need < 0) return KG_ERR_UNSUPPORTED;
-  const int64_t n = T * k;
+  if (kg_route_workspace_bytes(T, k, G) < 0) return KG_ERR_UNSUPPORTED;
+  const int64_t n = T * k, need = route_bytes(n, G);
   if (G == 0 && n == 0) return KG_OK;
   if ((G > 0 && ks == nullptr) || (n > 0 && (idx == nullptr || pos == nullptr)) ||
       (need > 0 && workspace == nullptr))

@@ -391,7 +391,8 @@ int kg_fprop(const void* A, int64_t lda, const float* sa, const void* W, const f
  */
 int kg_route(const int32_t* idx, int64_t T, int k, int G, int32_t* ks, int32_t* pos, int32_t* src,
              void* workspace, int64_t workspace_bytes, void* stream);
-/* Workspace of kg_route in bytes (0: none needed), or -1 for sizes it does not take. */
+/* Workspace of kg_route in bytes (0: none needed), enough for calls of fewer slots and experts too, or
+   -1 for sizes it does not take. */
 int64_t kg_route_workspace_bytes(int64_t T, int k, int G);
 
 /* Element types of the row copies below (argument `type`). */

@@ -29,3 +29,13 @@ def test_orthogonalize_workspaces_grow(sizes):
             assert row == sorted(row) and row[0] == 0
             assert all(a <= L.kg_orthogonalize_workspace_bytes(G + 1, R, C) for a, C in zip(row, sizes))
             assert row == [L.kg_orthogonalize_workspace_bytes(G, C, R) for C in sizes]
+
+
+def test_route_workspaces_grow():
+    L = B.lib()
+    for G in (1, 8, 256, 1024):
+        for k in (1, 8):
+            row = [L.kg_route_workspace_bytes(T, k, G) for T in (0, 1, 100, 2000, 4096, 5000, 65536, 200000)]
+            assert row == sorted(row)
+    row = [L.kg_route_workspace_bytes(n, 1, 16) for n in range(4000, 1100000, 97)]
+    assert row == sorted(row)
