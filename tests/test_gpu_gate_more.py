@@ -25,3 +25,21 @@ def test_smaller_batches_in_a_workspace_of_the_largest(G):
         assert torch.equal(psum, other[0]) and torch.equal(loss, other[1]) and torch.equal(counts, other[2])
         assert int(counts.sum()) == 4 * T
     assert (store[n:] == 77).all()
+
+
+@pytest.mark.parametrize("T,G", [(70, 17), (333, 40), (3000, 64), (1500, 100), (2000, 256), (500, 300)])
+@pytest.mark.parametrize("k", [15, 16])
+def test_last_choices_that_differ_in_the_last_bits(T, G, k):
+    """The k-th and the next logit a few last bits apart, which cut keys do not tell apart, or equal, or far
+    apart, and with fewer experts left than k: with 16 choices of 16 lanes the 17th key has no lane."""
+    x = base.logits(T, G, T + k)
+    order = x.argsort(1, descending=True)
+    last = x.gather(1, order[:, k - 1:k])
+    step = torch.tensor([0, 1, 2, 7, 100, 200, 1 << 12], device="cuda")[torch.arange(T, device="cuda") % 7][:, None]
+    bits = last.view(torch.int32)
+    near = torch.where(bits >= 0, bits - step, bits + step).int()  # below by `step` places
+    x.scatter_(1, order[:, k:k + 1], near.view(torch.float32))
+    x[3::11, G // 2:] = -float("inf")
+    x[5::11] = -float("inf")
+    base.check(x, k, norm=True)
+    base.check(-x.masked_fill(x.isinf(), 0), k)
