@@ -251,6 +251,7 @@ __global__ __launch_bounds__(1024, 4) void kg_fprop_w4_stream_kernel(WParams p) 
   }
   // (known to be one value per wave: buffers are described by scalars)
   g = uniform(g), rows = uniform(rows);
+  if (rows == 0) return;  // fewer experts have rows than could: no load is under way yet
   row0 = uniform((int)row0);  // below 2^31
   const int nk = (p.K + 127) / 128, pieces = w_pieces(nk);
   const int kbytes = p.K / 2, groups = p.K / kPerScale<GRP>;
