@@ -43,3 +43,75 @@ def test_last_choices_that_differ_in_the_last_bits(T, G, k):
     x[5::11] = -float("inf")
     base.check(x, k, norm=True)
     base.check(-x.masked_fill(x.isinf(), 0), k)
+
+
+# The gradient's roundings, one by one. With u = 2^-24: a score's relative error e is 3 u |x - max| from its
+# exponent (difference, factor, product) plus 2 u of v_exp_f32, and 24 u + u from the sum of up to 16 terms a
+# lane and six steps across lanes and the quotient; a sigmoid's is 3 u |x| + 2 u for the exponential, u for the
+# sum and 2 u for v_rcp_f32. The formulas then round each operation by u.
+U = 2.0 ** -24
+
+
+def gradient_bound(x, idx, dw, counts, dloss, sigmoid, norm, scale, coef):
+    """|dx - the definition's|, by element."""
+    x64 = x.detach().cpu().double()
+    live = ~torch.isneginf(x64)
+    far = torch.where(live, x64, 0.0).abs() if sigmoid else \
+        torch.where(live, x64.amax(1, keepdim=True) - x64, 0.0)
+    s, p = base.scores64(x, sigmoid)
+    e = (3 * far + (5 if sigmoid else 27)) * U
+    ok = (idx >= 0) & (idx < x.shape[1])
+    at = torch.where(ok, idx, 0)
+    dw64 = torch.where(ok, dw.cpu().double(), 0.0) if dw is not None else torch.zeros(idx.shape, dtype=torch.float64)
+    sj, ej = torch.where(ok, s.gather(1, at), 0.0), torch.where(ok, e.gather(1, at), 0.0)
+    if norm:
+        total, et = sj.sum(1, keepdim=True) + 1e-20, ej.amax(1, keepdim=True) + 7 * U
+        mean = (dw64 * sj).sum(1, keepdim=True) / total
+        off_mean = ((dw64 * sj).abs() * (ej + et + 9 * U)).sum(1, keepdim=True) / total
+        d = (dw64 - mean) / total
+        off = (off_mean + U * (dw64.abs() + mean.abs())) / total + d.abs() * (et + 3 * U)
+    else:
+        d, off = dw64, torch.zeros_like(dw64)
+    d, off = scale * d, scale * (off + U * d.abs())
+    zero = torch.zeros_like(x64)
+    d, off = zero.scatter_add(1, at, torch.where(ok, d, 0.0)), zero.scatter_add(1, at, torch.where(ok, off, 0.0))
+    size = zero.scatter_add(1, at, torch.where(ok, d.gather(1, at).abs(), 0.0))  # (sums of a few named twice)
+    off = off + 16 * U * size
+    c = dloss * coef * counts.cpu().double()[None] if counts is not None else zero
+    off_c = 4 * U * c.abs()
+    if sigmoid:
+        whole = s.sum(1, keepdim=True)
+        mean = (p * c).sum(1, keepdim=True)
+        et = e.amax(1, keepdim=True) + 26 * U
+        off_mean = (p * (c.abs() * (e + et + 26 * U) + off_c)).sum(1, keepdim=True)
+        even, off_even = (c - mean) / whole, (off_c + off_mean + U * (c - mean).abs()) / whole
+        off_even = off_even + even.abs() * (et + 3 * U)
+        t = d + even
+        return s * (1 - s) * ((2 * e + 6 * U) * t.abs() + off + off_even + U * (d.abs() + even.abs()))
+    v, off_v = d + c, off + off_c + U * (d.abs() + c.abs())
+    mean = (p * v).sum(1, keepdim=True)
+    off_mean = (p * (v.abs() * (e + 26 * U) + off_v)).sum(1, keepdim=True)
+    return p * ((e + 3 * U) * (v - mean).abs() + off_v + off_mean + U * (v.abs() + mean.abs()))
+
+
+@pytest.mark.parametrize("G,k", [(2, 1), (8, 2), (37, 3), (64, 8), (200, 16), (256, 8), (300, 6), (1024, 8)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_to_its_last_roundings(G, k, sigmoid, norm, dtype):
+    for T, with_dw, with_loss in ((1100, True, True), (70, True, False), (70, False, True)):
+        x = base.logits(T, G, T + G, dtype)
+        flags, scale, coef = base.flags_of(sigmoid, norm), 2.5, 1.0 / T
+        idx = kg.kg_gate(x, k, None, flags)[0]
+        gen = torch.Generator("cuda").manual_seed(T + G)
+        dw = torch.randn((T, k), generator=gen, device="cuda") if with_dw else None
+        counts = torch.randint(0, T, (G,), generator=gen, device="cuda", dtype=torch.int32) if with_loss else None
+        dloss = torch.full((1,), 0.625, device="cuda")
+        dx = kg.kg_gate_bwd(x, idx, dw, counts, dloss, flags, scale, coef)
+        args = (x, idx.cpu().long(), dw, counts, 0.625, sigmoid, norm, scale, coef)
+        want, bound = base.grad64(*args), gradient_bound(*args)
+        if dtype == "bf16":
+            bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+        off = (dx.cpu().double() - want).abs()
+        # (2^-120: exponentials below fp32's range are zeros, bf16's last steps of what is next to zero)
+        assert bool((off <= bound + 2.0 ** -120).all()), float((off / (bound + 2.0 ** -120)).max())
