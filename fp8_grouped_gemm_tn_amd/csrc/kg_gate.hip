@@ -476,7 +476,7 @@ __global__ __launch_bounds__(kGateThreads) void kg_gate_kernel(GateParams p) {
     if (norm) w = w / (sum_of<LPR>(w) + kGateTiny);
     if (live && l < p.k) {
       p.idx[t * p.k + l] = index;
-      p.w[t * p.k + l] = p.scale * w;
+      p.w[t * p.k + l] = index >= 0 ? p.scale * w : 0.0f;  // (the sum of a row with NaN may be NaN)
     }
     if (p.stats && live) {
       if (index >= 0) atomicAdd(&counts[index], 1);

@@ -532,8 +532,8 @@ int kg_adamw(const void* table, int count, int64_t items, int kinds, double lr, 
  *          psum or loss is given (else it is not used); needs no initialisation. Calls that share
  *          one must not run concurrently
  *
- * All sums are taken in an order that does not depend on timing. A NaN logit makes the token's
- * softmax (and its p) NaN. Errors before any launch: KG_ERR_DTYPE, KG_ERR_SHAPE (T < 0, G < 1,
+ * All sums are taken in an order that does not depend on timing. A logit of NaN makes the token's
+ * softmax and p NaN, one of +inf its softmax (and the p of that). Errors before any launch: KG_ERR_DTYPE, KG_ERR_SHAPE (T < 0, G < 1,
  * k < 1, k > G, ldx < G, a workspace that is too small), KG_ERR_NULL, KG_ERR_ALIGN (tensors by
  * their elements), KG_ERR_ALIAS, KG_ERR_UNSUPPORTED (G > 1024, k > 16, T * k > 2^31 - 1,
  * ldx > 2^30), KG_ERR_HIP.

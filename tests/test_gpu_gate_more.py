@@ -115,3 +115,21 @@ def test_gradient_to_its_last_roundings(G, k, sigmoid, norm, dtype):
         off = (dx.cpu().double() - want).abs()
         # (2^-120: exponentials below fp32's range are zeros, bf16's last steps of what is next to zero)
         assert bool((off <= bound + 2.0 ** -120).all()), float((off / (bound + 2.0 ** -120)).max())
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("G", [6, 100, 300])
+def test_empty_slots_of_rows_with_nan(G, norm, sigmoid, biased):
+    """A slot without an expert has weight 0 whatever else its row holds."""
+    x = base.logits(40, G, G)
+    x[::2, 3:] = -float("inf")
+    x[::4, 1] = float("nan")
+    x[1] = float("nan")
+    x[2, 0] = float("inf")
+    idx, w = kg.kg_gate(x, 5, torch.zeros(G, device="cuda") if biased else None, base.flags_of(sigmoid, norm), 2.0)
+    assert (idx[::2, 3:] == -1).all() and (idx[1] == -1).all()
+    assert (w[idx == -1] == 0).all()
+    good = torch.tensor([t for t in range(40) if t % 4 and t > 2])
+    assert (idx[good, :2] >= 0).all() and w[good].isfinite().all()
