@@ -533,10 +533,10 @@ int kg_adamw(const void* table, int count, int64_t items, int kinds, double lr, 
  *          one must not run concurrently
  *
  * All sums are taken in an order that does not depend on timing. A logit of NaN makes the token's
- * softmax and p NaN, one of +inf its softmax (and the p of that). Errors before any launch: KG_ERR_DTYPE, KG_ERR_SHAPE (T < 0, G < 1,
- * k < 1, k > G, ldx < G, a workspace that is too small), KG_ERR_NULL, KG_ERR_ALIGN (tensors by
- * their elements), KG_ERR_ALIAS, KG_ERR_UNSUPPORTED (G > 1024, k > 16, T * k > 2^31 - 1,
- * ldx > 2^30), KG_ERR_HIP.
+ * softmax and p NaN, one of +inf its softmax (and the p of that). Errors before any launch:
+ * KG_ERR_DTYPE, KG_ERR_SHAPE (T < 0, G < 1, k < 1, k > G, ldx < G, a workspace that is too small),
+ * KG_ERR_NULL, KG_ERR_ALIGN (tensors by their elements), KG_ERR_ALIAS, KG_ERR_UNSUPPORTED (G > 1024,
+ * k > 16, T * k > 2^31 - 1, ldx > 2^30), KG_ERR_HIP.
  */
 int kg_gate(const void* X, int64_t ldx, const float* bias, int64_t T, int G, int k, int type,
             int flags, double scale, double coef, int32_t* idx, float* w, int32_t* counts,
@@ -617,14 +617,15 @@ int kg_fprop_w4(const void* A, int64_t lda, const void* W, const void* sw, const
  * The products take fp16 operands with fp32 sums; what their rounding would add to small singular
  * values and to the diagonals is carried beside them. Before their rounding to bf16, results are within
  * 2e-3 of their norm of the same steps in 64 bits for up to 5 steps, 4e-3 for up to 8. The steps do not
- * settle (a singular value of 0.868 stays, but one beside it moves away 1.6 times as far with each step), so
- * roundings grow with more of them: 1e-2 was measured after 16, 5e-2 after 64. The singular vectors and the
- * singular values' range hold for any number. A NaN or an infinity in a matrix makes NaNs
- * of that matrix's result alone. Nothing depends on timing. Errors before any launch: KG_ERR_DTYPE,
- * KG_ERR_SHAPE (negative sizes, steps < 1, a workspace that is too small), KG_ERR_NULL,
- * KG_ERR_ALIGN (U and O by their elements), KG_ERR_ALIAS (the workspace overlapping U or O),
- * KG_ERR_UNSUPPORTED (G > 65535, R or C > 65536, steps > 64, more tiles than a launch has),
- * KG_ERR_HIP. G, R or C == 0: KG_OK, no launch.
+ * settle (a singular value of 0.868 stays, but one beside it moves 1.6 times as far away with each
+ * step), so roundings grow with more of them: 1e-2 was measured after 16, 5e-2 after 64. The singular
+ * vectors and the singular values' range hold for any number. A NaN or an infinity in a matrix makes
+ * NaNs of that matrix's result alone. Nothing depends on timing; G and the sizes choose the tiles, so
+ * a matrix's last bits depend on how many it comes with.
+ * Errors before any launch: KG_ERR_DTYPE, KG_ERR_SHAPE (negative sizes, steps < 1, a workspace that is
+ * too small), KG_ERR_NULL, KG_ERR_ALIGN (U and O by their elements), KG_ERR_ALIAS (the workspace
+ * overlapping U or O), KG_ERR_UNSUPPORTED (G > 65535, R or C > 65536, steps > 64, more tiles than a
+ * launch has), KG_ERR_HIP. G, R or C == 0: KG_OK, no launch.
  */
 int kg_orthogonalize(const void* U, void* O, int G, int R, int C, int type, int steps,
                      void* workspace, int64_t workspace_bytes, void* stream);

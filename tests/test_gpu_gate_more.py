@@ -133,3 +133,32 @@ def test_empty_slots_of_rows_with_nan(G, norm, sigmoid, biased):
     assert (w[idx == -1] == 0).all()
     good = torch.tensor([t for t in range(40) if t % 4 and t > 2])
     assert (idx[good, :2] >= 0).all() and w[good].isfinite().all()
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_logits_past_32_bit_offsets(sigmoid):
+    """More than 2^31 logits: rows behind that are what they are alone, in choice and gradient, and the sums
+    are those of all rows."""
+    T, G, k = 2_200_000, 1024, 4
+    gen = torch.Generator("cuda").manual_seed(1)
+    x = torch.empty((T, G), dtype=torch.bfloat16, device="cuda")
+    for at in range(0, T, 200_000):
+        x[at:at + 200_000] = torch.randn((200_000, G), generator=gen, device="cuda")
+    flags = base.flags_of(sigmoid, True)
+    counts, psum = torch.empty(G, dtype=torch.int32, device="cuda"), torch.empty(G, device="cuda")
+    idx, w = kg.kg_gate(x, k, None, flags, counts=counts, psum=psum)
+    dx = kg.kg_gate_bwd(x, idx, w, counts, None, flags, 1.0, 1.0 / T)
+    for rows in (slice(0, 500), slice(2 ** 21 - 300, 2 ** 21 + 300), slice(T - 700, T)):
+        i, v = kg.kg_gate(x[rows], k, None, flags)
+        assert torch.equal(i, idx[rows]) and torch.equal(v, w[rows])
+        assert torch.equal(kg.kg_gate_bwd(x[rows], i, v, counts, None, flags, 1.0, 1.0 / T), dx[rows])
+    base.check(x[T - 300:], k, sigmoid, True)
+    want, n = torch.zeros(G, dtype=torch.float64, device="cuda"), torch.zeros(G, dtype=torch.int64, device="cuda")
+    for at in range(0, T, 100_000):
+        y = x[at:at + 100_000].double()
+        s = torch.sigmoid(y) if sigmoid else torch.softmax(y, 1)
+        want += (s / s.sum(1, keepdim=True)).sum(0)
+        n += torch.bincount(idx[at:at + 100_000].flatten(), minlength=G)
+    assert torch.equal(counts.long(), n)
+    # a lane adds T / 4096 rows, then 8 waves and, in 64 bits, the workgroups
+    assert bool(((psum.double() - want).abs() <= want * (base.TOL + (T / 4096 + 8) * 2.0 ** -24)).all())
