@@ -58,10 +58,6 @@ __device__ __forceinline__ v4i load16(Rsrc r, uint32_t off) {
   typedef unsigned int v4u __attribute__((ext_vector_type(4)));
   return __builtin_bit_cast(v4i, (v4u)__builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
-__device__ __forceinline__ v2i load8(Rsrc r, uint32_t off) {
-  typedef unsigned int v2u __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(v2i, (v2u)__builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
-}
 __device__ __forceinline__ uint32_t load4(Rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
 }
@@ -441,7 +437,7 @@ struct WCfg {
   static constexpr int STAGE = KS * PART;
   static constexpr int WORDS = BN * KS / 64;              // of eight codes, of a thread and block
   static constexpr int UNITS = (BT * 8 * KS + 511) / 512; // of 16 bytes of tokens
-  static_assert(NI % 2 == 0 && (WORDS == 2 || WORDS == 4), "whole runs of outputs, whole words");
+  static_assert(NI % 2 == 0 && WORDS == 4, "whole runs of outputs, one load of codes");
   static_assert((KS - 1) * BT * BN * 4 <= 2 * STAGE, "the halves' sums fit");
 };
 // Row m of MFMA row tile i holds output wrow(i, m) of the wave's.
@@ -523,12 +519,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void kg_fprop_w4_kernel(WParams p) {
                               in ? (uint32_t)max(0, outs * kbytes - kb * (C::TK / 2)) : 0u);
       const Rsrc sr = rsrc_of(sbase + n * kScaleBytes<GRP, SB>,
                               in ? (uint32_t)((outs * groups - n) * kScaleBytes<GRP, SB>) : 0u);
-      if constexpr (C::WORDS == 4) {
-        wx[d] = load16(wr, woff);
-      } else {
-        const v2i x = load8(wr, woff);
-        wx[d] = v4i{x.x, x.y, 0, 0};
-      }
+      wx[d] = load16(wr, woff);
       // (the last channels of K's last block may not exist)
       const bool exists = C::TK * kb + 32 * quarter < p.K;
       const uint32_t at = exists ? soff : kOobOffset / 4;
