@@ -522,7 +522,8 @@ int kg_adamw(const void* table, int count, int64_t items, int kinds, double lr, 
  *          expert is left holds -1, which kg_route drops
  *   w      [T, k] fp32 out: scale * s[idx], with KG_GATE_NORM divided by the token's sum of
  *          chosen scores plus 1e-20; 0 for -1. Scores s are softmax(x), or sigmoid(x) with
- *          KG_GATE_SIGMOID, in fp32
+ *          KG_GATE_SIGMOID, in fp32 (below 2^-126, logits under -87 by sigmoids, one may count as 0,
+ *          and a token with no larger one has a p that adds up to less than 1)
  *   counts [G] int32 out, may be NULL: slots that hold g (kg_route's ks)
  *   psum   [G] fp32 out, may be NULL: the sum over tokens of p[t][g] = softmax(x), or
  *          s / (sum of the token's s); zeros for a token whose logits are all -inf
